@@ -1,0 +1,484 @@
+// kvpop_qk_norm_rope and its gradient: the RMS norm of every query and key head
+// and the position rotation, in one pass over the projections.
+//
+// For a head row x (D values), weights w, frequencies f_i and position t:
+//   r = (mean x^2 + eps)^(-1/2),  y = r x w,
+//   (z_a, z_b) = (y_a cos - y_b sin, y_b cos + y_a sin) at the angle t f_i
+// for the pairs (i, i + R/2) or (2i, 2i + 1), i < R/2; dims >= R keep y.
+// Backward, g = dL/dz: dy turns g back by the same angle, e = dy w,
+//   dx = r (e - x r^2 mean(e x)),  dw = sum over rows of dy x r.
+//
+// Layout: a lane holds both members of its pairs -- two 16-byte pieces of a
+// row, D/16 lanes to a row -- so the rotation needs no exchange and a row's sum
+// takes log2(D/16) shuffles.  A warp takes one token: its lanes compute the
+// token's R/2 angles once (shared out over the row groups) and use them for
+// every head.  HBM-bound: 4 bytes a value forward, 8 backward.
+//
+// Angles: f / 2 pi becomes a 64-bit fixed-point fraction of a turn, so the
+// product with an integer position wraps at whole turns without any loss; the
+// top 32 bits, as a signed number, go to sincospif.  The rounding of f / 2 pi to
+// 53 bits leaves 2^-33 rad at position 2^20.
+#include "common.cuh"
+
+namespace kvpop {
+namespace {
+
+constexpr int kWarps = 4;           // per CTA
+constexpr int kCtasPerSm = 4;       // grid limit: resident CTAs
+constexpr int kBwdMaxCtas = 1024;   // rows of the weight gradients' workspace
+
+struct QkParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  long long q_stride, k_stride;  // elements between tokens
+  const float* wq;
+  const float* wk;
+  const float* inv_freq;
+  const int32_t* pos;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_out;
+  long long qo_stride, ko_stride;
+  const float* dq;  // backward only: [T, Hq, D], [T, H, D]
+  const float* dk;
+  float* part;      // backward only: [CTAs, D] partial weight gradients
+  int T, S, Hq, H, nrot;  // nrot = R / 16: lanes of a row that rotate
+  int slices;             // warps that share a token's heads
+  int ctas_q;             // backward only: CTAs that take query heads
+  float eps;
+};
+
+// Which two 8-column pieces of a row lane j holds: the two members of its eight
+// pairs, or two neighbours where it does not rotate.
+template <bool INTER>
+__device__ __forceinline__ void pieces(int j, int nrot, int& a, int& b) {
+  if (!INTER && j < nrot) {
+    a = j;
+    b = j + nrot;
+  } else {
+    a = 2 * j;
+    b = 2 * j + 1;
+  }
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// Turns per position as a fraction of 2^64 (whole turns dropped).
+__device__ __forceinline__ unsigned long long turns64(float f) {
+  double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
+  t -= floor(t);
+  return (unsigned long long)(t * 18446744073709551616.0);
+}
+
+// The eight angles of lane j = lane % LPR: each of the 32 / LPR row groups computes
+// its share and the lanes of equal j exchange them.
+template <int LPR>
+struct Angles {
+  static constexpr int RPP = 32 / LPR, MINE = 8 / RPP;
+  unsigned long long turn[MINE];
+  float c[8], s[8];
+
+  __device__ __forceinline__ void init(const float* inv_freq, int j, int rg, int nrot) {
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) turn[i] = j < nrot ? turns64(inv_freq[8 * j + rg * MINE + i]) : 0ull;
+  }
+  __device__ __forceinline__ void at(int pos, int j) {
+    float mc[MINE], ms[MINE];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      const unsigned long long a = turn[i] * (unsigned long long)(long long)pos;
+      sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &ms[i], &mc[i]);  // half turns in [-1, 1]
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int src = (e / MINE) * LPR + j;
+      c[e] = __shfl_sync(0xffffffffu, mc[e % MINE], src);
+      s[e] = __shfl_sync(0xffffffffu, ms[e % MINE], src);
+    }
+  }
+};
+
+// Pair e of a lane: half-split pairs sit at the same place of the two pieces,
+// adjacent pairs next to each other in one of them.
+template <bool INTER>
+__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8],
+                                       float sign) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float& u = INTER ? (e < 4 ? a[2 * e] : b[2 * e - 8]) : a[e];
+    float& v = INTER ? (e < 4 ? a[2 * e + 1] : b[2 * e - 7]) : b[e];
+    const float sn = sign * s[e];
+    const float u2 = u * c[e] - v * sn, v2 = v * c[e] + u * sn;
+    u = u2;
+    v = v2;
+  }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32) qk_norm_fwd(const QkParams p) {
+  constexpr int LPR = D / 16, RPP = 32 / LPR;
+  __shared__ __align__(16) float w_s[2][D];
+  const int lane = lane_id(), j = lane % LPR, rg = lane / LPR;
+  grid_dep_launch();
+  grid_dep_wait();  // the projections, positions and weights come from earlier kernels
+  for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
+    const float* w = i < D ? p.wq : p.wk;
+    w_s[i / D][i % D] = w ? w[i % D] : 1.0f;
+  }
+  __syncthreads();
+  Angles<LPR> ang;
+  if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
+  int pa, pb;
+  pieces<INTER>(j, p.nrot, pa, pb);
+  const int rows = p.Hq + p.H, passes = (rows + RPP - 1) / RPP;
+  const long long ntask = (long long)p.T * p.slices;
+  for (long long task = (long long)blockIdx.x * kWarps + warp_id(); task < ntask;
+       task += (long long)gridDim.x * kWarps) {
+    const int t = (int)(task / p.slices), sl = (int)(task % p.slices);
+    const int p0 = (int)((long long)passes * sl / p.slices), p1 = (int)((long long)passes * (sl + 1) / p.slices);
+    if (p.nrot) ang.at(p.pos ? p.pos[t] : t % p.S, j);
+    for (int ps = p0; ps < p1; ++ps) {
+      const int row = ps * RPP + rg;
+      const bool on = row < rows, is_k = row >= p.Hq;
+      float a[8] = {}, b[8] = {};
+      if (on) {
+        const __nv_bfloat16* src =
+            is_k ? p.k + t * p.k_stride + (size_t)(row - p.Hq) * D : p.q + t * p.q_stride + (size_t)row * D;
+        unpack8(reinterpret_cast<const uint4*>(src)[pa], a);
+        unpack8(reinterpret_cast<const uint4*>(src)[pb], b);
+      }
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+      const float* wa = &w_s[is_k][8 * pa];
+      const float* wb = &w_s[is_k][8 * pb];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        a[e] = a[e] * r * wa[e];
+        b[e] = b[e] * r * wb[e];
+      }
+      if (j < p.nrot) rotate<INTER>(a, b, ang.c, ang.s, 1.0f);
+      if (on) {
+        __nv_bfloat16* dst =
+            is_k ? p.k_out + t * p.ko_stride + (size_t)(row - p.Hq) * D : p.q_out + t * p.qo_stride + (size_t)row * D;
+        reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
+        reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
+      }
+    }
+  }
+}
+
+// CTAs [0, ctas_q) take the query heads, the others the key heads, so that a lane
+// keeps the weights and the weight gradient of its 16 columns in registers.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32) qk_norm_bwd(const QkParams p) {
+  constexpr int LPR = D / 16, RPP = 32 / LPR;
+  __shared__ float red[kWarps][D];
+  const int lane = lane_id(), warp = warp_id(), j = lane % LPR, rg = lane / LPR;
+  grid_dep_launch();
+  grid_dep_wait();
+  const bool is_k = (int)blockIdx.x >= p.ctas_q;
+  const int cta = is_k ? blockIdx.x - p.ctas_q : blockIdx.x;
+  const int ctas = is_k ? gridDim.x - p.ctas_q : p.ctas_q;
+  const int heads = is_k ? p.H : p.Hq;
+  const __nv_bfloat16* x_base = is_k ? p.k : p.q;
+  const long long x_stride = is_k ? p.k_stride : p.q_stride, o_stride = is_k ? p.ko_stride : p.qo_stride;
+  const float* g_base = is_k ? p.dk : p.dq;
+  __nv_bfloat16* o_base = is_k ? p.k_out : p.q_out;
+  const float* w = is_k ? p.wk : p.wq;
+  Angles<LPR> ang;
+  if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
+  int pa, pb;
+  pieces<INTER>(j, p.nrot, pa, pb);
+  float wa[8], wb[8], da[8] = {}, db[8] = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    wa[e] = w ? w[8 * pa + e] : 1.0f;
+    wb[e] = w ? w[8 * pb + e] : 1.0f;
+  }
+  const int passes = (heads + RPP - 1) / RPP;
+  const int slices = min(p.slices, passes);
+  const long long ntask = (long long)p.T * slices;
+  for (long long task = (long long)cta * kWarps + warp; task < ntask; task += (long long)ctas * kWarps) {
+    const int t = (int)(task / slices), sl = (int)(task % slices);
+    const int p0 = (int)((long long)passes * sl / slices), p1 = (int)((long long)passes * (sl + 1) / slices);
+    if (p.nrot) ang.at(p.pos ? p.pos[t] : t % p.S, j);
+    for (int ps = p0; ps < p1; ++ps) {
+      const int row = ps * RPP + rg;
+      const bool on = row < heads;
+      float a[8] = {}, b[8] = {}, ga[8] = {}, gb[8] = {};
+      if (on) {
+        const __nv_bfloat16* src = x_base + t * x_stride + (size_t)row * D;
+        unpack8(reinterpret_cast<const uint4*>(src)[pa], a);
+        unpack8(reinterpret_cast<const uint4*>(src)[pb], b);
+        const float4* g = reinterpret_cast<const float4*>(g_base + ((size_t)t * heads + row) * D);
+        const float4 g0 = g[2 * pa], g1 = g[2 * pa + 1], g2 = g[2 * pb], g3 = g[2 * pb + 1];
+        ga[0] = g0.x, ga[1] = g0.y, ga[2] = g0.z, ga[3] = g0.w;
+        ga[4] = g1.x, ga[5] = g1.y, ga[6] = g1.z, ga[7] = g1.w;
+        gb[0] = g2.x, gb[1] = g2.y, gb[2] = g2.z, gb[3] = g2.w;
+        gb[4] = g3.x, gb[5] = g3.y, gb[6] = g3.z, gb[7] = g3.w;
+      }
+      if (j < p.nrot) rotate<INTER>(ga, gb, ang.c, ang.s, -1.0f);  // g is now dL/dy
+      float ss = 0.f, ex = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ss += a[e] * a[e] + b[e] * b[e];
+        ex += ga[e] * wa[e] * a[e] + gb[e] * wb[e] * b[e];
+      }
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        ex += __shfl_xor_sync(0xffffffffu, ex, o);
+      }
+      const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+      const float back = r * r * (ex * (1.0f / D));
+      if (on) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          da[e] += ga[e] * (a[e] * r);
+          db[e] += gb[e] * (b[e] * r);
+          a[e] = r * (ga[e] * wa[e] - a[e] * back);
+          b[e] = r * (gb[e] * wb[e] - b[e] * back);
+        }
+        __nv_bfloat16* dst = o_base + t * o_stride + (size_t)row * D;
+        reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
+        reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
+      }
+    }
+  }
+  // this CTA's sums over its rows, in a fixed order
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) {
+      da[e] += __shfl_xor_sync(0xffffffffu, da[e], o);
+      db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+    }
+    if (rg == 0) {
+      red[warp][8 * pa + e] = da[e];
+      red[warp][8 * pb + e] = db[e];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < D; i += kWarps * 32) {
+    float v = 0.f;
+    for (int u = 0; u < kWarps; ++u) v += red[u][i];
+    p.part[(size_t)blockIdx.x * D + i] = v;
+  }
+}
+
+// dwq / dwk from the CTAs' sums: CTA = 32 columns of one of the two, 8 warps over the rows.
+__global__ void __launch_bounds__(256)
+    qk_norm_dw(const float* part, int D, int ctas_q, int ctas, float* dwq, float* dwk) {
+  __shared__ float red[8][32];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int nc = D / 32;
+  const bool is_k = (int)blockIdx.x >= nc;
+  const int col = (blockIdx.x % nc) * 32 + lane_id();
+  const int lo = is_k ? ctas_q : 0, hi = is_k ? ctas : ctas_q;
+  float v = 0.f;
+  for (int i = lo + warp_id(); i < hi; i += 8) v += part[(size_t)i * D + col];
+  red[warp_id()][lane_id()] = v;
+  __syncthreads();
+  if (warp_id() == 0) {
+    v = 0.f;
+    for (int u = 0; u < 8; ++u) v += red[u][lane_id()];
+    float* dw = is_k ? dwk : dwq;
+    if (dw) dw[col] = v;
+  }
+}
+
+kvpop_status check_common(const char* what, const void* q, long long q_stride, const void* k, long long k_stride, int b,
+                          int S, int Hq, int H, int D, float eps, const float* inv_freq, int R, const void* qo,
+                          long long qo_stride, const void* ko, long long ko_stride) {
+  if (!q || !k || !qo || !ko) {
+    set_last_error("%s: q, k and the outputs must be non-NULL", what);
+    return KVPOP_ERR_INVALID_ARG;
+  }
+  if (b <= 0 || S <= 0 || Hq <= 0 || H <= 0) {
+    set_last_error("%s: bad shape b=%d S=%d Hq=%d H=%d", what, b, S, Hq, H);
+    return KVPOP_ERR_INVALID_ARG;
+  }
+  if (D != 64 && D != 128) {
+    set_last_error("%s: D=%d unsupported (64 or 128)", what, D);
+    return KVPOP_ERR_UNSUPPORTED;
+  }
+  if ((long long)b * S > 0x7fffffffll || Hq > 65535 || H > 65535) {
+    set_last_error("%s: at most 2^31 - 1 tokens and 65535 heads", what);
+    return KVPOP_ERR_UNSUPPORTED;
+  }
+  if (!(eps >= 0.0f) || eps > 3.0e38f) {
+    set_last_error("%s: eps must be finite and >= 0", what);
+    return KVPOP_ERR_INVALID_ARG;
+  }
+  if (R < 0 || R > D || (R > 0 && !inv_freq)) {
+    set_last_error("%s: R=%d must be in [0, D], with inv_freq when R > 0", what, R);
+    return KVPOP_ERR_INVALID_ARG;
+  }
+  if (R % 16 != 0) {
+    set_last_error("%s: R=%d must be a multiple of 16", what, R);
+    return KVPOP_ERR_UNSUPPORTED;
+  }
+  const long long strides[4] = {q_stride, qo_stride, k_stride, ko_stride};
+  for (int i = 0; i < 4; ++i) {
+    const long long row = (long long)(i < 2 ? Hq : H) * D;
+    if (strides[i] < row && (long long)b * S > 1) {
+      set_last_error("%s: a token stride of %lld is less than the heads' %lld values", what, strides[i], row);
+      return KVPOP_ERR_INVALID_ARG;
+    }
+  }
+  const uintptr_t am = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
+                       reinterpret_cast<uintptr_t>(qo) | reinterpret_cast<uintptr_t>(ko);
+  if ((am & 15) || ((q_stride | k_stride | qo_stride | ko_stride) & 7)) {
+    set_last_error("%s: q, k and the outputs must be 16-byte aligned with token strides that are multiples of 8", what);
+    return KVPOP_ERR_UNSUPPORTED;
+  }
+  return KVPOP_OK;
+}
+
+// Warps that share one token: as many as it takes to give every resident warp a task,
+// at most one a pass.
+int pick_slices(long long T, int passes, int warps) {
+  const long long want = (warps + T - 1) / T;
+  return (int)(want < passes ? want : passes);
+}
+
+}  // namespace
+}  // namespace kvpop
+
+using namespace kvpop;
+
+extern "C" kvpop_status kvpop_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int b,
+                                           int S, int Hq, int H, int D, const float* wq, const float* wk, float eps,
+                                           const float* inv_freq, int R, int interleaved, const int32_t* pos,
+                                           void* q_out, void* k_out, kvpop_stream stream) {
+  const long long qo = (long long)Hq * D, ko = (long long)H * D;
+  kvpop_status st = check_common("kvpop_qk_norm_rope", q, q_stride, k, k_stride, b, S, Hq, H, D, eps, inv_freq, R,
+                                 q_out, qo, k_out, ko);
+  if (st != KVPOP_OK) return st;
+  QkParams p = {};
+  p.q = (const __nv_bfloat16*)q;
+  p.k = (const __nv_bfloat16*)k;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.wq = wq;
+  p.wk = wk;
+  p.inv_freq = inv_freq;
+  p.pos = pos;
+  p.q_out = (__nv_bfloat16*)q_out;
+  p.k_out = (__nv_bfloat16*)k_out;
+  p.qo_stride = qo;
+  p.ko_stride = ko;
+  p.T = b * S;
+  p.S = S;
+  p.Hq = Hq;
+  p.H = H;
+  p.nrot = R / 16;
+  p.eps = eps;
+  const int rpp = 512 / D, passes = (Hq + H + rpp - 1) / rpp;
+  const int max_ctas = num_sms() * kCtasPerSm;
+  p.slices = pick_slices(p.T, passes, max_ctas * kWarps);
+  const long long ntask = (long long)p.T * p.slices;
+  const long long ctas = (ntask + kWarps - 1) / kWarps;
+  const dim3 grid((unsigned)(ctas < max_ctas ? ctas : max_ctas));
+  auto kern = D == 128 ? (interleaved ? qk_norm_fwd<128, true> : qk_norm_fwd<128, false>)
+                       : (interleaved ? qk_norm_fwd<64, true> : qk_norm_fwd<64, false>);
+  return cuda_check(launch_pdl(kern, grid, dim3(kWarps * 32), 0, reinterpret_cast<cudaStream_t>(stream), p),
+                    "kvpop_qk_norm_rope: launch");
+}
+
+extern "C" kvpop_status kvpop_qk_norm_rope_bwd_workspace_size(int D, size_t* bytes) {
+  if (!bytes) {
+    set_last_error("kvpop_qk_norm_rope_bwd_workspace_size: bytes is NULL");
+    return KVPOP_ERR_INVALID_ARG;
+  }
+  if (D != 64 && D != 128) {
+    set_last_error("kvpop_qk_norm_rope_bwd_workspace_size: D=%d unsupported (64 or 128)", D);
+    return KVPOP_ERR_UNSUPPORTED;
+  }
+  *bytes = (size_t)kBwdMaxCtas * D * 4;
+  return KVPOP_OK;
+}
+
+extern "C" kvpop_status kvpop_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                               const float* dq, const float* dk, int b, int S, int Hq, int H, int D,
+                                               const float* wq, const float* wk, float eps, const float* inv_freq,
+                                               int R, int interleaved, const int32_t* pos, void* dq_in,
+                                               int64_t dq_stride, void* dk_in, int64_t dk_stride, float* dwq,
+                                               float* dwk, void* workspace, size_t workspace_bytes,
+                                               kvpop_stream stream) {
+  kvpop_status st = check_common("kvpop_qk_norm_rope_bwd", q, q_stride, k, k_stride, b, S, Hq, H, D, eps, inv_freq, R,
+                                 dq_in, dq_stride, dk_in, dk_stride);
+  if (st != KVPOP_OK) return st;
+  if (!dq || !dk || !workspace) {
+    set_last_error("kvpop_qk_norm_rope_bwd: dq, dk and workspace must be non-NULL");
+    return KVPOP_ERR_INVALID_ARG;
+  }
+  size_t need = 0;
+  st = kvpop_qk_norm_rope_bwd_workspace_size(D, &need);
+  if (st != KVPOP_OK) return st;
+  if (workspace_bytes < need) {
+    set_last_error("kvpop_qk_norm_rope_bwd: workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    return KVPOP_ERR_INVALID_ARG;
+  }
+  if (((reinterpret_cast<uintptr_t>(dq) | reinterpret_cast<uintptr_t>(dk)) & 15) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255)) {
+    set_last_error("kvpop_qk_norm_rope_bwd: dq and dk must be 16-byte, workspace 256-byte aligned");
+    return KVPOP_ERR_UNSUPPORTED;
+  }
+  QkParams p = {};
+  p.q = (const __nv_bfloat16*)q;
+  p.k = (const __nv_bfloat16*)k;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.wq = wq;
+  p.wk = wk;
+  p.inv_freq = inv_freq;
+  p.pos = pos;
+  p.q_out = (__nv_bfloat16*)dq_in;
+  p.k_out = (__nv_bfloat16*)dk_in;
+  p.qo_stride = dq_stride;
+  p.ko_stride = dk_stride;
+  p.dq = dq;
+  p.dk = dk;
+  p.part = (float*)workspace;
+  p.T = b * S;
+  p.S = S;
+  p.Hq = Hq;
+  p.H = H;
+  p.nrot = R / 16;
+  p.eps = eps;
+  const int rpp = 512 / D, pq = (Hq + rpp - 1) / rpp, pk = (H + rpp - 1) / rpp;
+  const int max_ctas = min(num_sms() * kCtasPerSm, kBwdMaxCtas);
+  p.slices = pick_slices(p.T, pq + pk, max_ctas * kWarps);
+  // the two kinds of CTAs in proportion to their passes
+  const long long tasks_q = (long long)p.T * min(p.slices, pq), tasks_k = (long long)p.T * min(p.slices, pk);
+  const int share_q = max(1, min(max_ctas - 1, (int)((long long)max_ctas * pq / (pq + pk))));
+  const int ctas_q = (int)min((long long)share_q, (tasks_q + kWarps - 1) / kWarps);
+  const int ctas_k = (int)min((long long)(max_ctas - share_q), (tasks_k + kWarps - 1) / kWarps);
+  p.ctas_q = ctas_q;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  auto kern = D == 128 ? (interleaved ? qk_norm_bwd<128, true> : qk_norm_bwd<128, false>)
+                       : (interleaved ? qk_norm_bwd<64, true> : qk_norm_bwd<64, false>);
+  st = cuda_check(launch_pdl(kern, dim3(ctas_q + ctas_k), dim3(kWarps * 32), 0, cs, p),
+                  "kvpop_qk_norm_rope_bwd: launch");
+  if (st != KVPOP_OK || (!dwq && !dwk)) return st;
+  return cuda_check(launch_pdl(qk_norm_dw, dim3(2 * D / 32), dim3(256), 0, cs, (const float*)workspace, D, ctas_q,
+                               ctas_q + ctas_k, dwq, dwk),
+                    "kvpop_qk_norm_rope_bwd: weight gradient launch");
+}

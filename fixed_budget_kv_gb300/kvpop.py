@@ -7,6 +7,7 @@ call raises ``KvpopUnavailable`` -- there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -21,6 +22,7 @@ LIST_QBLOCK = 64
 
 c_int = ctypes.c_int
 c_i32 = ctypes.c_int32
+c_i64 = ctypes.c_int64
 c_size = ctypes.c_size_t
 c_float = ctypes.c_float
 c_void_p = ctypes.c_void_p
@@ -80,6 +82,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvpop_target_normalize": ([P, c_int, c_int, c_int, c_int, c_int, c_float, P, P], c_int),
         "kvpop_teacher_labels": ([P, c_int, c_int, c_int, Budget, c_int, P, P, P, P], c_int),
         "kvpop_boundary_loss": ([P, P, P, P, c_int, c_int, c_int, c_int, c_int, P, c_float, P, P, P], c_int),
+        "kvpop_qk_norm_rope": ([P, c_i64, P, c_i64, c_int, c_int, c_int, c_int, c_int, P, P, c_float, P, c_int, c_int, P,
+                                P, P, P], c_int),
+        "kvpop_qk_norm_rope_bwd_workspace_size": ([c_int, P], c_int),
+        "kvpop_qk_norm_rope_bwd": ([P, c_i64, P, c_i64, P, P, c_int, c_int, c_int, c_int, c_int, P, P, c_float, P, c_int,
+                                    c_int, P, P, c_i64, P, c_i64, P, P, P, c_size, P], c_int),
+        "kvpop_prefix_attn_workspace_size": ([c_int, c_int, c_int, c_int, c_int, c_int, P], c_int),
+        "kvpop_prefix_attn": ([P, P, P, c_int, c_int, c_int, c_int, c_int, c_int, c_float, P, P, P, P, P, P, P, c_size,
+                               P], c_int),
         "kvpop_cache_create": ([c_int, c_int, c_int, c_int, Budget, P], c_int),
         "kvpop_cache_destroy": ([P], c_int),
         "kvpop_cache_prefill": ([P, P, P, P, c_int, P, P], c_int),
@@ -127,6 +137,25 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _same(ref, *named):
+    """The tensors that are given are on ref's device, and that is the current one."""
+    if ref.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {ref.device}: make it the current device first")
+    for t, name in named:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _on(stream):
+    """Memory that a call allocates belongs to the stream that uses it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def device_status(reset: bool = True):
@@ -311,6 +340,166 @@ def boundary_loss(r_hat, t_bnd, y, w: int, n: int, log_gamma, tau: float, omega=
                                       _p(log_gamma), float(tau), _p(loss), _p(grad), _stream(stream)),
            "kvpop_boundary_loss")
     return loss, grad
+
+
+# ----------------------------------------------------------------------------
+# before the attention: per-head norm of q and k with the position rotation
+# ----------------------------------------------------------------------------
+
+def _token_stride(t, name):
+    """Elements between the tokens of a bf16 [b, S, heads, D] view whose heads are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [b, S, heads, D]")
+    b, S, heads, D = t.shape
+    if (D > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if S > 1:
+        if b > 1 and t.stride(0) != S * t.stride(1):
+            raise ValueError(f"{name}: the tokens must be evenly spaced over the batch")
+        return t.stride(1)
+    return t.stride(0) if b > 1 else heads * D
+
+
+def _qk_args(q, k, wq, wk, inv_freq, pos):
+    sq, sk = _token_stride(q, "q"), _token_stride(k, "k")
+    b, S, Hq, D = q.shape
+    _shape(k, (b, S, k.shape[2], D), "k")
+    for t, name in ((wq, "wq"), (wk, "wk")):
+        if t is not None:
+            _need(t, torch.float32, name)
+            _shape(t, (D,), name)
+    R = 0
+    if inv_freq is not None:
+        _need(inv_freq, torch.float32, "inv_freq")
+        R = 2 * inv_freq.numel()
+    if pos is not None:
+        _need(pos, torch.int32, "pos")
+        _shape(pos, (b, S), "pos")
+    _same(q, (k, "k"), (wq, "wq"), (wk, "wk"), (inv_freq, "inv_freq"), (pos, "pos"))
+    return sq, sk, b, S, Hq, k.shape[2], D, R
+
+
+def qk_norm_rope(q, k, wq, wk, eps: float, inv_freq, pos=None, interleaved: bool = False, out=None, stream=None):
+    """RMS norm of each head of q [b,S,Hq,D] and k [b,S,H,D] (weights wq, wk: fp32 [D] or
+    None) and the rotation of the first 2 * len(inv_freq) dims at positions pos (int32
+    [b,S]; None: 0..S-1).  q and k may be views of a packed projection.  Returns
+    contiguous (q_out, k_out); a decode step's n tokens are [n,1,heads,D]."""
+    sq, sk, b, S, Hq, H, D, R = _qk_args(q, k, wq, wk, inv_freq, pos)
+    if out is None:
+        with _on(stream):
+            qo = torch.empty((b, S, Hq, D), dtype=torch.bfloat16, device=q.device)
+            ko = torch.empty((b, S, H, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        qo, ko = out
+        for t, x, name in ((qo, q, "q_out"), (ko, k, "k_out")):
+            _need(t, torch.bfloat16, name)
+            _shape(t, x.shape, name)
+        _same(q, (qo, "q_out"), (ko, "k_out"))
+    _check(load().kvpop_qk_norm_rope(_p(q), sq, _p(k), sk, b, S, Hq, H, D, _p(wq), _p(wk), float(eps), _p(inv_freq), R,
+                                     int(bool(interleaved)), _p(pos), _p(qo), _p(ko), _stream(stream)),
+           "kvpop_qk_norm_rope")
+    return qo, ko
+
+
+def qk_norm_rope_bwd_workspace_size(D: int) -> int:
+    n = c_size()
+    _check(load().kvpop_qk_norm_rope_bwd_workspace_size(D, ctypes.byref(n)), "qk_norm_rope_bwd_workspace_size")
+    return n.value
+
+
+def qk_norm_rope_bwd(q, k, dq, dk, wq, wk, eps: float, inv_freq, pos=None, interleaved: bool = False, workspace=None,
+                     out=None, stream=None):
+    """Gradient of qk_norm_rope for the upstream fp32 dq [b,S,Hq,D] and dk [b,S,H,D]
+    (attn_bwd's): (dq_in, dk_in bf16, dwq, dwk fp32 [D]).  q and k are the forward's
+    inputs.  `out` may hold views of a packed projection's gradient, and None for a
+    weight gradient that is not wanted."""
+    sq, sk, b, S, Hq, H, D, R = _qk_args(q, k, wq, wk, inv_freq, pos)
+    for t, x, name in ((dq, q, "dq"), (dk, k, "dk")):
+        _need(t, torch.float32, name)
+        _shape(t, x.shape, name)
+    _same(q, (dq, "dq"), (dk, "dk"), (workspace, "workspace"))
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(qk_norm_rope_bwd_workspace_size(D), dtype=torch.uint8, device=q.device)
+        if out is None:
+            out = (torch.empty((b, S, Hq, D), dtype=torch.bfloat16, device=q.device),
+                   torch.empty((b, S, H, D), dtype=torch.bfloat16, device=q.device),
+                   torch.empty(D, dtype=torch.float32, device=q.device),
+                   torch.empty(D, dtype=torch.float32, device=q.device))
+    dqi, dki, dwq, dwk = out
+    _shape(dqi, q.shape, "dq_in")
+    _shape(dki, k.shape, "dk_in")
+    for t, name in ((dwq, "dwq"), (dwk, "dwk")):
+        if t is not None:
+            _need(t, torch.float32, name)
+            _shape(t, (D,), name)
+    _same(q, (dqi, "dq_in"), (dki, "dk_in"), (dwq, "dwq"), (dwk, "dwk"))
+    _need(workspace, torch.uint8, "workspace")
+    _check(load().kvpop_qk_norm_rope_bwd(_p(q), sq, _p(k), sk, _p(dq), _p(dk), b, S, Hq, H, D, _p(wq), _p(wk), float(eps),
+                                         _p(inv_freq), R, int(bool(interleaved)), _p(pos), _p(dqi),
+                                         _token_stride(dqi, "dq_in"), _p(dki), _token_stride(dki, "dk_in"), _p(dwq),
+                                         _p(dwk), _p(workspace), workspace.numel(), _stream(stream)),
+           "kvpop_qk_norm_rope_bwd")
+    return dqi, dki, dwq, dwk
+
+
+# ----------------------------------------------------------------------------
+# decode over shared prefixes
+# ----------------------------------------------------------------------------
+
+def prefix_attn_workspace_size(n, m, P, Hq, H, D) -> int:
+    nb = c_size()
+    _check(load().kvpop_prefix_attn_workspace_size(n, m, P, Hq, H, D, ctypes.byref(nb)), "prefix_attn_workspace_size")
+    return nb.value
+
+
+def prefix_attn(q, pk, pv, cu=None, lens=None, join=None, scale: float = 0.0, workspace=None, out=None, stream=None):
+    """Attention of decode rows q [n,Hq,D] over prefixes pk, pv [m,P,H,D] that groups of
+    sequences share: group j is the sequences cu[j]..cu[j+1]-1 (int32 [m+1]; None with
+    one prefix) and sees the first lens[j] keys (int32 [m]; None: all P).  `join` =
+    (O2 [n,Hq,D] bf16, lse2 [n,Hq] fp32), the rows' attention over other keys such as
+    Cache.step's, makes the result the attention over both.  Returns (O, lse)."""
+    for t, name in ((q, "q"), (pk, "pk"), (pv, "pv")):
+        _need(t, torch.bfloat16, name)
+    if q.dim() != 3 or pk.dim() != 4:
+        raise ValueError("q must be [n, Hq, D] and pk [m, P, H, D]")
+    n, Hq, D = q.shape
+    m, P, H, _ = pk.shape
+    _shape(pk, (m, P, H, D), "pk")
+    _shape(pv, (m, P, H, D), "pv")
+    for t, size, name in ((cu, m + 1, "cu"), (lens, m, "lens")):
+        if t is not None:
+            _need(t, torch.int32, name)
+            _shape(t, (size,), name)
+    O2, lse2 = (None, None) if join is None else join
+    if join is not None:
+        _need(O2, torch.bfloat16, "O2")
+        _need(lse2, torch.float32, "lse2")
+        _shape(O2, (n, Hq, D), "O2")
+        _shape(lse2, (n, Hq), "lse2")
+    with _on(stream):
+        if out is None:
+            O = torch.empty_like(q)
+            lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+        else:
+            O, lse = out
+            _need(O, torch.bfloat16, "O")
+            _need(lse, torch.float32, "lse")
+            _shape(O, (n, Hq, D), "O")
+            _shape(lse, (n, Hq), "lse")
+        if workspace is None:
+            workspace = torch.empty(prefix_attn_workspace_size(n, m, P, Hq, H, D), dtype=torch.uint8, device=q.device)
+    _need(workspace, torch.uint8, "workspace")
+    _same(q, (pk, "pk"), (pv, "pv"), (cu, "cu"), (lens, "lens"), (O2, "O2"), (lse2, "lse2"), (O, "O"), (lse, "lse"),
+          (workspace, "workspace"))
+    _check(load().kvpop_prefix_attn(_p(q), _p(pk), _p(pv), n, m, P, Hq, H, D, float(scale), _p(cu), _p(lens), _p(O2),
+                                    _p(lse2), _p(O), _p(lse), _p(workspace), workspace.numel(), _stream(stream)),
+           "kvpop_prefix_attn")
+    return O, lse
 
 
 # ----------------------------------------------------------------------------

@@ -255,6 +255,53 @@ kvpop_status kvpop_boundary_loss(const float* r_hat, const int32_t* t_bnd, const
                                  kvpop_stream stream);
 
 /* ------------------------------------------------------------------------
+ * kvpop_qk_norm_rope -- what comes before the attention: the RMS norm of every
+ * query and key head and the position rotation, in one pass.  Not in the pages
+ * (their backbone computes it); the attention above takes its outputs.
+ *
+ * For each token at position t and each head row x of q (weights wq) and k (wk):
+ *   y = x * (mean(x^2) + eps)^(-1/2) * w
+ *   z_a = y_a cos(t f_i) - y_b sin(t f_i),  z_b = y_b cos(t f_i) + y_a sin(t f_i)
+ * for the pairs i < R/2 with (a, b) = (i, i + R/2), or (2i, 2i + 1) when
+ * `interleaved` is non-zero; dims >= R are normed only (R = 0: no rotation).
+ *   q        [b, S, Hq, D] bf16: the heads of a token are contiguous, tokens are
+ *            q_stride elements apart (Hq * D, or the packed projection's width);
+ *            likewise k [b, S, H, D] with k_stride
+ *   wq, wk   [D] fp32, nullable (all 1)
+ *   inv_freq [R/2] fp32; angles are taken from its exact values at any int32 position
+ *   pos      [b, S] int32, nullable: the position of token s is s
+ *   q_out    [b, S, Hq, D], k_out [b, S, H, D] bf16, contiguous.  q_out may be q
+ *            (and k_out k) when the strides are equal too; no other overlap.
+ * A decode step's single tokens are b = n sequences of S = 1 with their positions.
+ * D 64 or 128, any Hq and H up to 65535, R a multiple of 16 up to D, b * S < 2^31,
+ * strides multiples of 8, q, k and outputs 16-byte aligned, eps >= 0.  fp32
+ * arithmetic, one rounding to bf16 at the end.
+ * Errors: INVALID_ARG, UNSUPPORTED (D, R, sizes, alignment), CUDA.
+ *
+ * kvpop_qk_norm_rope_bwd -- its gradient, for the upstream gradients dq
+ * [b, S, Hq, D] and dk [b, S, H, D] fp32 contiguous (kvpop_attn_bwd's), the same
+ * q, k (the inputs, not the outputs), weights, eps, inv_freq and pos:
+ *   dq_in, dk_in  bf16 gradients of q and k, tokens dq_stride / dk_stride elements
+ *                 apart (so they may be the parts of a packed projection's gradient)
+ *   dwq, dwk      [D] fp32, nullable: gradients of the weights, summed over all
+ *                 tokens and heads in a fixed order (the same bits every run)
+ * All overwritten.  dq_in may be q and dk_in k when the strides are equal too.
+ * workspace: kvpop_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned,
+ * contents undefined between calls.
+ * ---------------------------------------------------------------------- */
+kvpop_status kvpop_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int b, int S,
+                                int Hq, int H, int D, const float* wq, const float* wk, float eps,
+                                const float* inv_freq, int R, int interleaved, const int32_t* pos, void* q_out,
+                                void* k_out, kvpop_stream stream);
+kvpop_status kvpop_qk_norm_rope_bwd_workspace_size(int D, size_t* bytes);
+kvpop_status kvpop_qk_norm_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                    const float* dq, const float* dk, int b, int S, int Hq, int H, int D,
+                                    const float* wq, const float* wk, float eps, const float* inv_freq, int R,
+                                    int interleaved, const int32_t* pos, void* dq_in, int64_t dq_stride,
+                                    void* dk_in, int64_t dk_stride, float* dwq, float* dwk, void* workspace,
+                                    size_t workspace_bytes, kvpop_stream stream);
+
+/* ------------------------------------------------------------------------
  * Fixed-budget decode cache ([notes] section 2.4 and section 3.3: B slots
  * per KV head, the token u = q - w leaving the window is kept or evicted by
  * comparing its priority with the worst held long-range token; [summary]
@@ -304,6 +351,44 @@ kvpop_status kvpop_decode_step(kvpop_cache* cache, const void* q_new, const void
 kvpop_status kvpop_cache_slots(const kvpop_cache* cache, int32_t* slot_pos, kvpop_stream stream);
 /* Host value of the next decode position. */
 kvpop_status kvpop_cache_position(const kvpop_cache* cache, int32_t* q_next);
+
+/* ------------------------------------------------------------------------
+ * kvpop_prefix_attn -- decode attention over prefixes shared by groups of
+ * sequences (parallel samples of a prompt): each prefix is held once, in full,
+ * and read once for its whole group.  Not in the pages; it stands beside
+ * kvpop_decode_step, whose cache then holds only a sequence's own tokens.
+ *
+ * Group j is the sequences cu[j] .. cu[j+1]-1 and attends over the first lens[j]
+ * keys of prefix j; there is no causal mask.  For query head h * G + g of
+ * sequence i in group j, s_t = scale * q . k_{j,t,h}, t < lens[j]:
+ *   lse = log sum_t exp(s_t),  O = sum_t exp(s_t - lse) v_t
+ * and, when O2 and lse2 (another attention of the same rows over other keys:
+ * kvpop_decode_step's O and lse) are given, the attention over both key sets:
+ *   L = log(exp(lse) + exp(lse2)),  O = O exp(lse - L) + O2 exp(lse2 - L),  lse = L.
+ *   q      [n, Hq, D] bf16; several query tokens of a sequence are several rows
+ *          of its group
+ *   pk, pv [m, P, H, D] bf16 (the K and V of a prompt batch as kvpop_attn_fwd
+ *          takes them); keys at or past lens[j] are never used, whatever they hold
+ *   cu     [m + 1] int32 device, non-decreasing in [0, n]; NULL with m = 1: all n.
+ *          Rows of O and lse outside cu[0] .. cu[m]-1 are left as they were.
+ *   lens   [m] int32 device in [0, P]; NULL: all P.  A row without any key (and
+ *          with lse2 = -inf, if given) gets O = 0 and lse = -inf.
+ *          Out-of-range values of cu and lens are clamped.
+ *   O2     [n, Hq, D] bf16, lse2 [n, Hq] fp32, both or neither; a row with
+ *          lse2 = -inf contributes nothing, whatever O2 holds
+ *   O      [n, Hq, D] bf16, lse [n, Hq] fp32 natural log; O may be O2 and lse lse2
+ * scale <= 0 selects 1/sqrt(D).  D 64 or 128, G dividing 128, H, Hq and m up to
+ * 65535, n up to 2^24, tensors 16-byte aligned.  bf16 operands (the softmax
+ * weights rounded to bf16 before their product with V), fp32 accumulation.
+ * workspace: kvpop_prefix_attn_workspace_size() bytes, 256-byte aligned; contents
+ * undefined between calls, so calls that overlap in time need one each.
+ * Errors: INVALID_ARG, UNSUPPORTED (D, G, sizes, alignment), CUDA.
+ * ---------------------------------------------------------------------- */
+kvpop_status kvpop_prefix_attn_workspace_size(int n, int m, int P, int Hq, int H, int D, size_t* bytes);
+kvpop_status kvpop_prefix_attn(const void* q, const void* pk, const void* pv, int n, int m, int P, int Hq, int H,
+                               int D, float scale, const int32_t* cu, const int32_t* lens, const void* O2,
+                               const float* lse2, void* O, float* lse, void* workspace, size_t workspace_bytes,
+                               kvpop_stream stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,324 @@
+"""kvpop_prefix_attn on the GPU against the 64-bit form, and a decode loop and a
+training step that use it and the norm-and-rotation pair with the library's own
+attention.
+
+Tolerances.  O: half a bf16 step of the result (2^-8) plus the softmax weights'
+rounding to bf16 (2^-8 of the weighted mean of |v|) plus the scores' fp32 error ds
+(at most D roundings of 2^-24 of sum |q k|, which moves a weight by 2 ds relative)
+and 2^-16 for the fp32 sums and exponentials.  LSE: ds plus 2^-20 relative."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import ref64
+from fixed_budget_kv_gb300 import kvpop
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    kvpop.device_status(reset=True)
+    yield
+    st, words = kvpop.device_status(reset=True)
+    assert st == 0, f"device status {words}"
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def make(groups, P, H, G, D, seed, join=False, scale=1.0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    n, m = sum(groups), len(groups)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=gen, device="cuda")
+    q, k, v = (randn(n, H * G, D) * scale).bfloat16(), randn(m, P, H, D).bfloat16(), randn(m, P, H, D).bfloat16()
+    j = ((randn(n, H * G, D) * 0.1).bfloat16(), randn(n, H * G) + 5) if join else None
+    return q, k, v, j
+
+
+def check(O, lse, q, k, v, cu, lens, join=None, scale=None, rows=None):
+    rO, rl, mass, ds = ref64.prefix_attn(q, k, v, cu, lens, scale, join)
+    sel = slice(None) if rows is None else rows
+    O, lse, rO, rl, mass = O[sel].double(), lse[sel].double(), rO[sel], rl[sel], mass[sel]
+    ninf = rl == -math.inf
+    assert torch.equal(lse == -math.inf, ninf)
+    assert ((lse - rl).abs()[~ninf] <= ds + 2.0 ** -20 * (1 + rl.abs()[~ninf])).all(), float((lse - rl).abs()[~ninf].max())
+    tol = 2.0 ** -8 * rO.abs() + (2.0 ** -8 + 2 * ds + 2.0 ** -16) * mass
+    bad = ~((O - rO).abs() <= tol)
+    assert not bad.any(), f"O: {int(bad.sum())} off, worst {float((O - rO).abs().max())}"
+
+
+CASES = [
+    # groups, lens, P, H, G, D, join
+    ([1], [1], 1, 1, 1, 64, False),                              # one row, one key
+    ([1], [130], 130, 1, 1, 128, True),
+    ([2], [257], 257, 1, 2, 64, False),
+    ([3], [128], 128, 2, 4, 128, False),                         # whole tiles
+    ([5], [127], 300, 2, 4, 128, True),                          # a length that ends inside a tile
+    ([5, 0, 2, 9], [0, 50, 129, 384], 400, 2, 4, 128, True),     # no keys, no sequences
+    ([32], [700], 700, 2, 4, 128, False),                        # 128 rows
+    ([33], [700], 701, 1, 4, 128, True),                         # 129 rows
+    ([64], [1000], 1000, 2, 4, 128, False),                      # 256 rows
+    ([65, 1], [513, 2], 513, 1, 4, 64, True),                    # 257 rows
+    ([150], [900], 900, 1, 4, 128, True),                        # 600 rows: three blocks
+    ([200], [300], 300, 3, 8, 64, False),
+    ([9], [400], 400, 1, 16, 128, True),
+    ([5], [333], 333, 1, 64, 64, False),
+    ([3], [200], 200, 2, 128, 128, True),                        # one sequence a row tile
+    ([4] * 37, list(range(0, 37 * 11, 11)), 400, 2, 4, 128, True),   # more groups than a warp has lanes
+    ([1] * 90, [129] * 90, 140, 4, 2, 64, False),                # more work items than SMs
+    ([16], [20000], 20000, 8, 4, 128, True),                     # a long prefix split over all SMs
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "n{}m{}P{}H{}G{}D{}j{}".format(sum(c[0]), len(c[0]), *c[2:6], int(c[6])))
+def test_prefix_attention(case):
+    groups, lens, P, H, G, D, join = case
+    q, k, v, j = make(groups, P, H, G, D, seed=P + sum(groups), join=join)
+    cu = [0] + np.cumsum(groups).tolist()
+    O, lse = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), j)
+    check(O, lse, q, k, v, cu, lens, j)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_defaults_and_scale(D):
+    """One prefix without cu and lens; a scale of the caller's; peaked and flat rows."""
+    q, k, v, _ = make([10], 500, 2, 4, D, seed=D, scale=3.0)
+    O, lse = kvpop.prefix_attn(q, k, v)
+    check(O, lse, q, k, v, [0, 10], [500])
+    O, lse = kvpop.prefix_attn(q, k, v, scale=0.5)
+    check(O, lse, q, k, v, [0, 10], [500], scale=0.5)
+    k.zero_()
+    O, lse = kvpop.prefix_attn(q, k, v)
+    check(O, lse, q, k, v, [0, 10], [500])
+
+
+def test_growing_scores():
+    """Scores that grow along the keys move the running maximum at every tile."""
+    q, k, v, _ = make([3], 1500, 1, 4, 128, seed=1)
+    k = (q[:1, :1].float() * torch.linspace(-1, 1, 1500, device="cuda")[None, :, None, None] * 0.8).bfloat16()
+    k = k.reshape(1, 1500, 1, 128).contiguous()
+    O, lse = kvpop.prefix_attn(q, k, v)
+    check(O, lse, q, k, v, [0, 3], [1500])
+
+
+@pytest.mark.parametrize("groups", [[6, 40], [70, 3]], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3.0e38])
+def test_keys_past_the_length_are_never_used(bad, groups):
+    lens, P = [131, 260], 400
+    q, k, v, j = make(groups, P, 2, 4, 128, seed=2, join=True)
+    cu = [0, groups[0], sum(groups)]
+    ref = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), j)
+    for b, ln in enumerate(lens):
+        k[b, ln:] = bad
+        v[b, ln:] = bad
+    got = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), j)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_join_edges():
+    """lse2 = -inf: nothing joins, whatever O2 holds; no keys: the joined result alone;
+    neither: zeros and -inf; a dominant side gives that side."""
+    q, k, v, j = make([4, 4], 200, 1, 2, 64, seed=3, join=True)
+    O2, l2 = j
+    l2[0] = -math.inf
+    O2[0] = float("nan")
+    l2[4] = -math.inf
+    O2[4] = float("inf")
+    l2[1] = 500.0
+    l2[2] = -500.0
+    cu, lens = [0, 4, 8], [200, 0]
+    O, lse = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), (O2, l2))
+    check(O, lse, q, k, v, cu, lens, (O2, l2))
+    assert torch.equal(O[5:], O2[5:]) and torch.equal(O[1], O2[1])
+    assert (O[4] == 0).all() and (lse[4] == -math.inf).all()
+    alone, al = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens))
+    assert torch.equal(alone[0], O[0]) and torch.equal(alone[2], O[2])
+    assert (alone[4:] == 0).all() and (al[4:] == -math.inf).all()
+
+
+def test_in_place_join_and_rows_outside():
+    """The result may replace what it joins; rows outside the groups stay as they were."""
+    q, k, v, j = make([12], 300, 2, 4, 128, seed=4, join=True)
+    cu, lens = [3, 9], [300]
+    ref = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), j)
+    O, lse = j[0].clone(), j[1].clone()
+    kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), (O, lse), out=(O, lse))
+    assert torch.equal(O[3:9], ref[0][3:9]) and torch.equal(lse[3:9], ref[1][3:9])
+    for a, b in ((O, j[0]), (lse, j[1])):
+        assert torch.equal(a[:3], b[:3]) and torch.equal(a[9:], b[9:])
+    full = [torch.full((12, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((12, 8), 5.0, device="cuda")]
+    kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), None, out=tuple(full))
+    assert all((t[:3] == 5).all() and (t[9:] == 5).all() for t in full)
+    assert torch.isfinite(full[0].float()).all()
+
+
+def test_out_of_range_groups_and_lengths_are_clamped():
+    q, k, v, _ = make([5, 5], 150, 1, 2, 64, seed=5)
+    want = kvpop.prefix_attn(q, k, v, i32([0, 5, 10]), i32([150, 0]))
+    got = kvpop.prefix_attn(q, k, v, i32([-7, 5, 4000]), i32([99999, -4]))
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_stream_graph_and_repeat():
+    """Side stream, and a captured call replayed with other lengths and data: each replay
+    equals the eager call, bit for bit."""
+    groups, P = [20, 1, 45], 600
+    q, k, v, j = make(groups, P, 2, 4, 128, seed=6, join=True)
+    cu = i32([0, 20, 21, 66])
+    lens = i32([600, 77, 300])
+    ref = kvpop.prefix_attn(q, k, v, cu, lens, j)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = kvpop.prefix_attn(q, k, v, cu, lens, j, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = kvpop.prefix_attn(q, k, v, cu, lens, j)
+    for lv in ([600, 77, 300], [1, 600, 0], [128, 129, 590]):
+        lens.copy_(i32(lv))
+        q.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        ref = kvpop.prefix_attn(q, k, v, cu, lens, j)
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1]), lv
+
+
+def test_two_streams_at_once():
+    q, k, v, j = make([40], 3000, 4, 4, 128, seed=7, join=True)
+    ref = kvpop.prefix_attn(q, k, v, None, None, j)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        outs += [kvpop.prefix_attn(q, k, v, None, None, j, stream=s) for s in streams]
+    torch.cuda.synchronize()
+    for O, lse in outs:
+        assert torch.equal(O, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_offsets_past_32_bits():
+    """Prefixes of more than 2^31 elements: the last one is right."""
+    m, P, H, G, D = 5, 131072, 32, 2, 128
+    k = torch.empty(m, P, H, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty(m, P, H, D, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    for t in (k, v):
+        t[-1, -1000:] = torch.randn(1000, H, D, generator=gen, device="cuda").bfloat16()
+        t[-1, :-1000] = 0
+    q = torch.randn(2, H * G, D, generator=gen, device="cuda").bfloat16()
+    cu, lens = [0, 0, 0, 0, 0, 2], [P] * m
+    O, lse = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens))
+    check(O, lse, q, k, v, cu, lens)
+
+
+def test_binding_refusals():
+    q, k, v, j = make([4], 100, 2, 2, 64, seed=9, join=True)
+    with pytest.raises(ValueError, match="bfloat16"):
+        kvpop.prefix_attn(q.float(), k, v)
+    with pytest.raises(ValueError, match="pv"):
+        kvpop.prefix_attn(q, k, v[:, :50].contiguous())
+    with pytest.raises(ValueError, match="contiguous"):
+        kvpop.prefix_attn(q, k[:, ::2], v[:, ::2])
+    with pytest.raises(ValueError, match="cu"):
+        kvpop.prefix_attn(q, k, v, cu=i32([0, 2, 4]))
+    with pytest.raises(ValueError, match="lens"):
+        kvpop.prefix_attn(q, k, v, lens=torch.tensor([100], device="cuda"))
+    with pytest.raises(ValueError, match="lse2"):
+        kvpop.prefix_attn(q, k, v, join=(j[0], j[1][:2].contiguous()))
+    with pytest.raises(kvpop.KvpopError):
+        kvpop.prefix_attn(q, torch.cat([k, k]), torch.cat([v, v]))           # two prefixes, no groups
+    with pytest.raises(kvpop.KvpopError):
+        kvpop.prefix_attn(q, k, v, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+def test_decode_over_a_shared_prompt():
+    """Samples of two prompts decode together: norm and rotation, the step on each
+    sequence's own cache (which holds all of its own tokens here), and the prompt joined.
+    Against one 64-bit softmax over the rotated keys of prompt and own tokens, with the
+    library's tolerances for O (2e-2) and LSE (2e-3)."""
+    groups, lens, P = [3, 2], [150, 97], 150
+    H, G, D, s, w, kk, steps = 2, 4, 128, 2, 8, 8, 12
+    Hq, n, m = H * G, sum(groups), len(groups)
+    gen = torch.Generator(device="cuda").manual_seed(10)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=gen, device="cuda")
+    wq, wk = 1 + 0.1 * randn(D), 1 + 0.1 * randn(D)
+    f = (1.0e6 ** (-torch.arange(0, D, 2).double() / D)).float().cuda()
+    prompt = randn(m, P, (Hq + 2 * H) * D).bfloat16()
+    pq, pk = prompt[..., : Hq * D].view(m, P, Hq, D), prompt[..., Hq * D:(Hq + H) * D].view(m, P, H, D)
+    pv = prompt[..., (Hq + H) * D:].reshape(m, P, H, D).contiguous()
+    _, pk2 = kvpop.qk_norm_rope(pq, pk, wq, wk, 1e-6, f)
+    cu, ln = i32([0, 3, 5]), i32(lens)
+    gid = [0, 0, 0, 1, 1]
+    start = i32([lens[j] for j in gid])[:, None]
+    cache = kvpop.Cache(n, H, G, D, s, w, kk)
+    own_k, own_v = [], []
+    for i in range(steps):
+        qkv = randn(n, 1, (Hq + 2 * H) * D).bfloat16()
+        q, k = qkv[..., : Hq * D].view(n, 1, Hq, D), qkv[..., Hq * D:(Hq + H) * D].view(n, 1, H, D)
+        v = qkv[..., (Hq + H) * D:].reshape(n, H, D).contiguous()
+        pos = (start + i).contiguous()
+        q2, k2 = kvpop.qk_norm_rope(q, k, wq, wk, 1e-6, f, pos)
+        O2, l2, _ = cache.step(q2[:, 0], k2[:, 0], v, randn(n, H))
+        O, lse = kvpop.prefix_attn(q2[:, 0], pk2, pv, cu, ln, (O2, l2))
+        q64, kp = q2[:, 0].double(), pk2.double()
+        for got, x, ww in ((q2, q, wq), (k2, k, wk)):
+            z, y = ref64.norm_rope(x, ww, 1e-6, f, pos)
+            assert ((got.double() - z).abs() <= 2.0 ** -8 * z.abs() + 2.0 ** -17 * y.abs().amax(-1, keepdim=True)).all()
+        own_k.append(k2[:, 0].double())
+        own_v.append(v.double())
+        for r in range(n):
+            j = gid[r]
+            ka = torch.cat([kp[j, : lens[j]], torch.stack([t[r] for t in own_k])])
+            va = torch.cat([pv[j, : lens[j]].double(), torch.stack([t[r] for t in own_v])])
+            for hq in range(Hq):
+                sc = (ka[:, hq // G] @ q64[r, hq]) / math.sqrt(D)
+                assert abs(float(lse[r, hq]) - float(torch.logsumexp(sc, 0))) <= 2e-3
+                o = torch.softmax(sc, 0) @ va[:, hq // G]
+                assert float((O[r, hq].double() - o).abs().max()) <= 2e-2
+    cache.close()
+
+
+def test_training_step_through_norm_and_sparse_attention():
+    """Projections -> norm and rotation -> mask, sparse attention -> its gradient -> the
+    projections' and weights' gradient: the attention's part against the oracle (1e-2 of
+    the largest entry, as its own tests have it), the norm's part against the 64-bit form
+    on the gradients that the attention gave."""
+    b, S, H, G, D, s, w, kk = 1, 200, 2, 4, 128, 4, 32, 40
+    Hq = H * G
+    gen = torch.Generator(device="cuda").manual_seed(12)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=gen, device="cuda")
+    qkv = randn(b, S, (Hq + 2 * H) * D).bfloat16()
+    q, k = qkv[..., : Hq * D].view(b, S, Hq, D), qkv[..., Hq * D:(Hq + H) * D].view(b, S, H, D)
+    v = qkv[..., (Hq + H) * D:].reshape(b, S, H, D).contiguous()
+    wq, wk = 0.5 + 0.1 * randn(D), 0.5 + 0.1 * randn(D)
+    f = (1.0e4 ** (-torch.arange(0, D, 2).double() / D)).float().cuda()
+    prio, dO = randn(b, H, S), randn(b, S, Hq, D).bfloat16()
+    q2, k2 = kvpop.qk_norm_rope(q, k, wq, wk, 1e-6, f)
+    _, _, ev, lists = kvpop.mask(prio, s, w, kk)
+    O, lse = kvpop.attn_fwd(q2, k2, v, 0.0, ev, lists, (s, w, kk))
+    gq, gk, gv = kvpop.attn_bwd(q2, k2, v, O, dO, lse, ev, lists, (s, w, kk))
+    got = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, 1e-6, f)
+    r, tau, _ = oracle.mask(prio.cpu().numpy(), s, w, kk)
+    rq, rk, _ = oracle.attn_bwd(q2.float().cpu().numpy(), k2.float().cpu().numpy(), v.float().cpu().numpy(),
+                                dO.float().cpu().numpy(), 1 / math.sqrt(D), r, tau, s, w)
+    for g, ref in ((gq, rq), (gk, rk)):
+        assert np.abs(g.cpu().numpy() - ref).max() <= 1e-2 * np.abs(ref).max()
+    for dx, dw, x, g, ww in ((got[0], got[2], q, gq, wq), (got[1], got[3], k, gk, wk)):
+        rx, rw, size, terms = ref64.norm_rope_bwd(x, g, ww, 1e-6, f)
+        assert ((dx.double() - rx).abs() <= 2.0 ** -8 * rx.abs() + 2.0 ** -17 * size).all()
+        assert ((dw.double() - rw).abs() <= 512 * 2.0 ** -24 * terms).all()

@@ -1,0 +1,237 @@
+"""kvpop_qk_norm_rope and its gradient on the GPU against the 64-bit form.
+
+Tolerances.  Outputs are rounded to bf16 once: half a step, 2^-8 of the value.
+Before that, fp32: the sum of squares and the products carry a few dozen
+roundings of 2^-24, the angles at most 2^-22 rad (an fp32 fraction of a turn and
+sincospif), each relative to the row's largest terms -- 2^-17 of them covers both.
+Weight gradients are fp32 sums in a tree whose longest path is below 512
+additions, so 512 * 2^-24 of the sum of the terms' magnitudes."""
+import pytest
+import torch
+
+import ref64
+from fixed_budget_kv_gb300 import kvpop
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    kvpop.device_status(reset=True)
+    yield
+    st, words = kvpop.device_status(reset=True)
+    assert st == 0, f"device status {words}"
+
+
+def freqs(R, theta=1.0e6):
+    if not R:
+        return None
+    return (theta ** (-torch.arange(0, R, 2, dtype=torch.float64) / R)).float().cuda()
+
+
+def make(b, S, Hq, H, D, seed, packed=False, scale=1.5):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def randn(*shape):
+        return torch.randn(shape, generator=gen, device="cuda")
+    if packed:
+        qkv = (randn(b, S, (Hq + 2 * H) * D) * scale).bfloat16()
+        q, k = qkv[..., : Hq * D].view(b, S, Hq, D), qkv[..., Hq * D:(Hq + H) * D].view(b, S, H, D)
+    else:
+        q, k = (randn(b, S, Hq, D) * scale).bfloat16(), (randn(b, S, H, D) * scale).bfloat16()
+    return q, k, 1 + 0.2 * randn(D), 1 + 0.2 * randn(D), randn(b, S, Hq, D), randn(b, S, H, D)
+
+
+def check_fwd(got, x, w, f, pos, inter, what):
+    z, y = ref64.norm_rope(x, w, EPS, f, pos, inter)
+    tol = 2.0 ** -8 * z.abs() + 2.0 ** -17 * y.abs().amax(-1, keepdim=True)
+    bad = (got.double() - z).abs() > tol
+    assert not bad.any() and torch.isfinite(got.float()).all(), f"{what}: {int(bad.sum())} off"
+
+
+def check_bwd(dx, dw, x, g, w, f, pos, inter, what):
+    rx, rw, size, terms = ref64.norm_rope_bwd(x, g, w, EPS, f, pos, inter)
+    bad = (dx.double() - rx).abs() > 2.0 ** -8 * rx.abs() + 2.0 ** -17 * size
+    assert not bad.any() and torch.isfinite(dx.float()).all(), f"{what}: dx {int(bad.sum())} off"
+    if dw is not None:
+        assert ((dw.double() - rw).abs() <= 512 * 2.0 ** -24 * terms).all(), f"{what}: dw"
+
+
+CASES = [
+    # b, S, Hq, H, D, R, interleaved, packed, positions
+    (1, 1, 8, 2, 128, 128, False, False, None),        # one token
+    (64, 1, 32, 8, 128, 128, False, True, 131072),     # a decode step
+    (7, 1, 5, 1, 64, 64, True, True, 1000),            # heads that do not fill a pass
+    (1, 300, 32, 8, 128, 128, False, True, None),
+    (3, 101, 6, 2, 64, 32, True, False, 50000),        # half of the dims, adjacent pairs
+    (2, 77, 3, 3, 128, 64, False, True, 2000000000),   # half of the dims, halves; positions near 2^31
+    (1, 130, 1, 1, 128, 16, False, False, None),
+    (1, 50, 2, 1, 64, 16, True, False, 9),
+    (2, 33, 4, 4, 64, 0, False, True, None),           # norm only
+    (1, 5000, 4, 1, 128, 128, True, False, None),      # more tokens than warps
+    (1, 3, 130, 65, 64, 64, False, False, None),       # many heads
+]
+
+
+def ids(c):
+    return "b{}S{}Hq{}H{}D{}R{}i{}p{}@{}".format(*(int(x) if isinstance(x, bool) else x for x in c))
+
+
+def positions(b, S, start):
+    if start is None:
+        return None
+    base = torch.arange(b, device="cuda", dtype=torch.int32)[:, None] * 7 + start
+    return (base + torch.arange(S, device="cuda", dtype=torch.int32)).contiguous()
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_forward_and_backward(case):
+    b, S, Hq, H, D, R, inter, packed, start = case
+    q, k, wq, wk, gq, gk = make(b, S, Hq, H, D, seed=sum(case[:6]), packed=packed)
+    f, pos = freqs(R), positions(b, S, start)
+    qo, ko = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f, pos, inter)
+    check_fwd(qo, q, wq, f, pos, inter, "q")
+    check_fwd(ko, k, wk, f, pos, inter, "k")
+    dq, dk, dwq, dwk = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f, pos, inter)
+    check_bwd(dq, dwq, q, gq, wq, f, pos, inter, "q")
+    check_bwd(dk, dwk, k, gk, wk, f, pos, inter, "k")
+
+
+def test_no_weights_and_no_weight_gradients():
+    q, k, _, _, gq, gk = make(2, 40, 4, 2, 128, seed=5)
+    f = freqs(128)
+    qo, ko = kvpop.qk_norm_rope(q, k, None, None, EPS, f)
+    check_fwd(qo, q, None, f, None, False, "q")
+    check_fwd(ko, k, None, f, None, False, "k")
+    out = (torch.empty_like(q), torch.empty_like(k), None, None)
+    dq, dk, a, b = kvpop.qk_norm_rope_bwd(q, k, gq, gk, None, None, EPS, f, out=out)
+    assert a is None and b is None
+    check_bwd(dq, None, q, gq, None, f, None, False, "q")
+    check_bwd(dk, None, k, gk, None, f, None, False, "k")
+
+
+def test_zero_rows_and_large_values():
+    """A row of zeros stays zeros (eps > 0) with a finite gradient; rows near the bf16
+    range's ends are normed like any other as long as their squares fit 32 bits."""
+    q, k, wq, wk, gq, gk = make(1, 8, 4, 2, 64, seed=6)
+    q[0, 0] = 0
+    q[0, 1] *= 1e15
+    q[0, 2] *= 1e-12
+    f = freqs(64)
+    qo, ko = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f)
+    assert (qo[0, 0] == 0).all()
+    check_fwd(qo, q, wq, f, None, False, "q")
+    dq, dk, dwq, dwk = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f)
+    check_bwd(dq, dwq, q, gq, wq, f, None, False, "q")
+
+
+def test_bad_row_stays_in_its_row():
+    q, k, wq, wk, gq, gk = make(1, 9, 4, 2, 128, seed=7)
+    f = freqs(128)
+    clean, _ = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f)
+    q2 = q.clone()
+    q2[0, 4, 1, 77] = float("nan")
+    q2[0, 4, 2, 3] = float("inf")
+    got, _ = kvpop.qk_norm_rope(q2, k, wq, wk, EPS, f)
+    assert torch.isnan(got[0, 4, 1]).all()
+    keep = torch.ones(1, 9, 4, dtype=torch.bool, device="cuda")
+    keep[0, 4, 1:3] = False
+    assert torch.equal(got[keep], clean[keep])
+
+
+def test_negative_and_extreme_positions():
+    q, k, wq, wk, _, _ = make(1, 6, 2, 1, 128, seed=8)
+    f = freqs(128)
+    pos = torch.tensor([[-1, -100000, 2147483647, -2147483648, 0, 1048576]], dtype=torch.int32, device="cuda")
+    qo, ko = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f, pos)
+    check_fwd(qo, q, wq, f, pos, False, "q")
+
+
+def test_in_place_and_strided_gradients():
+    """In place for contiguous inputs; gradients written into a packed projection's
+    gradient leave its value part alone."""
+    b, S, Hq, H, D = 2, 65, 8, 2, 128
+    q, k, wq, wk, gq, gk = make(b, S, Hq, H, D, seed=9)
+    f = freqs(D)
+    ref = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f)
+    grads = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f)
+    dqkv = torch.full((b, S, (Hq + 2 * H) * D), 7.0, dtype=torch.bfloat16, device="cuda")
+    views = (dqkv[..., : Hq * D].view(b, S, Hq, D), dqkv[..., Hq * D:(Hq + H) * D].view(b, S, H, D))
+    out = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f,
+                                 out=(*views, torch.empty_like(wq), torch.empty_like(wk)))
+    for a, r in zip(out, grads):
+        assert torch.equal(a, r)  # the same bits: the sums' order is fixed
+    assert (dqkv[..., (Hq + H) * D:] == 7.0).all()
+    q2, k2 = q.clone(), k.clone()
+    kvpop.qk_norm_rope(q2, k2, wq, wk, EPS, f, out=(q2, k2))
+    assert torch.equal(q2, ref[0]) and torch.equal(k2, ref[1])
+
+
+def test_stream_graph_and_repeat():
+    """On a side stream, and captured and replayed on new data, the same bits."""
+    q, k, wq, wk, gq, gk = make(2, 200, 8, 2, 128, seed=10, packed=True)
+    f = freqs(128)
+    ref = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f) + kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = (kvpop.qk_norm_rope(q, k, wq, wk, EPS, f, stream=side)
+           + kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f, stream=side))
+    torch.cuda.current_stream().wait_stream(side)
+    for a, r in zip(got, ref):
+        assert torch.equal(a, r)
+    q0, k0 = torch.zeros_like(q), torch.zeros_like(k)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = kvpop.qk_norm_rope(q0, k0, wq, wk, EPS, f) + kvpop.qk_norm_rope_bwd(q0, k0, gq, gk, wq, wk, EPS, f)
+    q0.copy_(q)
+    k0.copy_(k)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, r in zip(out, ref):
+        assert torch.equal(a, r)
+
+
+def test_offsets_past_32_bits():
+    """A packed projection of more than 2^31 elements: the last tokens are right."""
+    b, S, Hq, H, D = 1, 90000, 1, 1, 128
+    width = 24576
+    buf = torch.empty(b, S, width, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    buf[:, -200:] = torch.randn(b, 200, width, generator=gen, device="cuda").bfloat16()
+    buf[:, :-200, -256:] = 1
+    q, k = buf[..., -256:-128].view(b, S, 1, D), buf[..., -128:].view(b, S, 1, D)
+    f = freqs(D)
+    qo, ko = kvpop.qk_norm_rope(q, k, None, None, EPS, f)
+    tail = torch.arange(S - 200, S, device="cuda", dtype=torch.int32)[None]
+    check_fwd(qo[:, -200:], q[:, -200:], None, f, tail, False, "q")
+    check_fwd(ko[:, -200:], k[:, -200:], None, f, tail, False, "k")
+
+
+def test_binding_refusals():
+    q, k, wq, wk, gq, gk = make(2, 8, 4, 2, 64, seed=12)
+    f = freqs(64)
+    ok = (q, k, wq, wk, EPS, f)
+    with pytest.raises(ValueError, match="bfloat16"):
+        kvpop.qk_norm_rope(q.float(), *ok[1:])
+    with pytest.raises(ValueError, match="contiguous"):
+        kvpop.qk_norm_rope(q.transpose(1, 2), *ok[1:])
+    with pytest.raises(ValueError, match="evenly"):
+        kvpop.qk_norm_rope(torch.empty(2, 9, 4, 64, dtype=torch.bfloat16, device="cuda")[:, :8], *ok[1:])
+    with pytest.raises(ValueError, match="pos"):
+        kvpop.qk_norm_rope(*ok, pos=torch.zeros(8, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="wq"):
+        kvpop.qk_norm_rope(q, k, wq[:32].contiguous(), wk, EPS, f)
+    with pytest.raises(ValueError, match="k must be"):
+        kvpop.qk_norm_rope(q, k[:1], wq, wk, EPS, f)
+    with pytest.raises(kvpop.KvpopError):
+        kvpop.qk_norm_rope(q, k, wq, wk, EPS, freqs(64)[:5].contiguous())   # R = 10
+    with pytest.raises(ValueError, match="dq"):
+        kvpop.qk_norm_rope_bwd(q, k, gq[:1].contiguous(), gk, wq, wk, EPS, f)
+    with pytest.raises(ValueError, match="dwk"):
+        kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f,
+                               out=(torch.empty_like(q), torch.empty_like(k), wq, wq.double()))
