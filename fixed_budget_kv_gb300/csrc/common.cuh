@@ -34,6 +34,10 @@ enum Site : int {
   SITE_TARGET_MMA = 21,
   SITE_TARGET_SOFTMAX = 22,
   SITE_DECODE = 30,
+  SITE_PREFIX_PRODUCER = 50,
+  SITE_PREFIX_MMA = 51,
+  SITE_PREFIX_SOFTMAX = 52,
+  SITE_PREFIX_EPILOGUE = 53,
   SITE_INTERNAL_CHECK = 40,
 };
 

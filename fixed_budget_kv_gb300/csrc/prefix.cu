@@ -1,88 +1,755 @@
 // kvpop_prefix_attn: decode rows over key/value prefixes that groups of sequences
 // share, joined with another attention result of the same rows.
+//
+// For query head h G + g of sequence i in group j: s_t = scale q . k_{j,t,h},
+// t < lens[j]; lse = log sum exp s_t, O = sum exp(s_t - lse) v_t; a join adds the
+// keys behind (O2, lse2) by their log-sum-exp.
+//
+// The rows of one (prefix, KV head) are the G query heads of the group's
+// sequences.  A block of up to 256 of them meets each 128-key tile of K and V
+// once, so a prefix is read from memory once per 256 rows; the arithmetic is
+// rows flop a byte, memory-bound up to about that many rows.
+//
+// Work split: a unit is (group, 256-row block, KV head, 128-key tile), numbered in
+// that order, and CTA c takes the units [c U / C, (c + 1) U / C) -- one CTA an SM,
+// every SM the same number of key tiles however ragged the groups and lengths.
+// A CTA's units fall into segments of one (group, block, head) each.  A segment
+// that covers all key tiles is finished by its CTA; of the others a CTA has at
+// most two (it begins inside one and ends inside another), whose running
+// maximum, sum and unnormalised O go to two slots of the workspace, and
+// prefix_merge joins the slots of a row in the order of the CTAs.  No atomics:
+// the same call gives the same bits.
+//
+// Warp roles of prefix_kernel (384 threads):
+//   warp 0      TMA producer: one ring of K and V tiles in the order of their use
+//   warp 1      TMEM allocation and the single-thread tcgen05.mma issuer
+//   warp 2      query tiles of each segment
+//   warp 3      the CTA's share of the units, handed to the others segment by segment
+//   warps 4-7, 8-11  softmax, one thread a row (TMEM lane)
+// The two softmax warpgroups are two streams that alternate, so that the tensor
+// core works on one while the other is in its softmax.  A segment of more than
+// 128 rows gives each its own row tile; a smaller one gives both the same rows
+// and every other key tile, and joins the two in the epilogue.  S = Q K^T lands in
+// TMEM (fp32), becomes bf16 P in place, and O += P V reads P from TMEM.  Running
+// maxima are moved lazily, when they grow by more than 2^8.
+#include <string.h>
+
 #include "common.cuh"
 
 namespace kvpop {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kKeys = 128;
+constexpr int kBlockRows = 256;
+constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kMergeThreads = 128;
+constexpr int kSegs = 4;  // segments between the walker and the last reader
+// Register split: warps 0-3 drop to kRegsIo, the softmax warpgroups rise to kRegsSoftmax.
+constexpr int kRegsIo = 64;
+constexpr int kRegsSoftmax = 216;
+constexpr int kRegsNeeded = (128 * kRegsIo + 256 * kRegsSoftmax + kThreads - 1) / kThreads;
 
 struct PrefixParams {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
+  CUtensorMap tq, tk, tv;
   const int32_t* cu;
   const int32_t* lens;
   const __nv_bfloat16* o2;
   const float* lse2;
   __nv_bfloat16* O;
   float* lse;
-  int n, m, P, Hq, H, G;
+  long long* unit0;  // [m + 1] first unit of each group
+  float2* part_ml;   // [CTA, 2 slots, 256 rows] (maximum in log2 units, sum)
+  float4* part_o;    // [CTA, 2 slots, 2 row tiles, D / 4, 128 rows]
+  int* status;
+  int n, m, P, Hq, H, G, seqs;  // seqs = 256 / G sequences of a row block
   float scale_log2;
 };
 
-// One CTA per (sequence, query head): each warp takes every 8th key with a running
-// maximum and sum, then the warps' results are joined.
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+// Group j: its sequences [lo, hi), rows, key tiles and units.
+struct Group {
+  int lo, hi, len, nt;
+  long long rows, units;
+};
+__device__ __forceinline__ Group group_of(const PrefixParams& p, int j) {
+  Group g;
+  g.lo = p.cu ? max(0, min(p.cu[j], p.n)) : 0;
+  g.hi = p.cu ? max(g.lo, min(p.cu[j + 1], p.n)) : p.n;
+  g.len = p.lens ? max(0, min(p.lens[j], p.P)) : p.P;
+  g.nt = (g.len + kKeys - 1) / kKeys;
+  g.rows = (long long)(g.hi - g.lo) * p.G;
+  g.units = (g.rows + kBlockRows - 1) / kBlockRows * p.H * g.nt;
+  return g;
+}
+
+__device__ __forceinline__ long long scan_incl(long long x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane_id() >= o) x += y;
+  }
+  return x;
+}
+
+// CTA c's first unit, and the CTA that holds unit u, for U units over C CTAs.
+__device__ __forceinline__ long long first_unit(long long U, int C, int c) { return U * c / C; }
+__device__ __forceinline__ int cta_of(long long U, int C, long long u) { return (int)(((u + 1) * C + U - 1) / U) - 1; }
+
+// One segment: key tiles [kt0, kt0 + NT) of a row block of (group j, head h).
+struct __align__(16) Seg {
+  int j, h, seq0, nrow;  // first sequence and rows (up to 256) of the block
+  int kt0, NT, len, flags;
+  // two row tiles, one a stream; otherwise one, its key tiles alternating
+  __device__ __forceinline__ bool two() const { return flags & 1; }
+  // all key tiles of the block
+  __device__ __forceinline__ bool whole() const { return flags & 2; }
+  // otherwise: 0 when an earlier CTA began the block, 1 when this one did
+  __device__ __forceinline__ int slot() const { return flags >> 2; }
+};
+
+// Walks the segments of units [u, end) starting in group j (first unit base).
+struct Walk {
+  long long u, end, base;
+  int j;
+  __device__ __forceinline__ Seg next(const PrefixParams& p) {
+    Seg s = {};
+    if (u >= end) return s;  // NT = 0 ends the CTA's work
+    Group g = group_of(p, j);
+    while (u >= base + g.units) {
+      base += g.units;
+      g = group_of(p, ++j);
+    }
+    const long long item = (u - base) / g.nt;
+    s.kt0 = (int)((u - base) - item * g.nt);
+    s.NT = (int)min((long long)(g.nt - s.kt0), end - u);
+    s.j = j;
+    const long long rb = item / p.H;
+    s.h = (int)(item - rb * p.H);
+    s.seq0 = g.lo + (int)rb * p.seqs;
+    s.nrow = (int)min((long long)kBlockRows, g.rows - rb * kBlockRows);
+    s.len = g.len;
+    s.flags = (s.nrow > 128 ? 1 : 0) | (s.NT == g.nt ? 2 : 0) | (s.kt0 == 0 ? 4 : 0);
+    u += s.NT;
+    return s;
+  }
+};
+
+// Place of a key tile's K and V among the segment's 2 NT loads: the order in which
+// the MMA warp uses them (S runs two events ahead of P V).
+__device__ __forceinline__ int pos_k(bool two, int t) { return two ? 2 * t : (t < 2 ? t : 2 * t - 1); }
+__device__ __forceinline__ int pos_v(bool two, int NT, int t) { return two ? 2 * t + 1 : min(NT, t + 2) + t; }
+
+template <int NS>
+struct Bars {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[NS], kv_empty[NS];
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_full, o_empty;
+  uint64_t ml_full;
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t drain;
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) prefix_simple(const PrefixParams p) {
-  constexpr int E = D / 32;
-  __shared__ float m_s[8], l_s[8], o_s[8][D];
-  const int i = blockIdx.x, hq = blockIdx.y, h = hq / p.G;
-  const int lane = lane_id(), warp = warp_id();
+struct Layout {
+  static constexpr int DH = D / 64;
+  static constexpr int NS = D == 128 ? 5 : 10;  // 32 KB or 16 KB tiles
+  static constexpr int kTile = DH * kBlockBytes;
+  static constexpr int q_off = 0;
+  static constexpr int kv_off = q_off + 2 * kTile;
+  static constexpr int bar_off = kv_off + NS * kTile;
+  static constexpr int seg_off = bar_off + ((int)sizeof(Bars<NS>) + 15) / 16 * 16;
+  static constexpr int ml_off = seg_off + kSegs * (int)sizeof(Seg);  // [stream][row] (maximum, sum)
+  static constexpr int misc_off = ml_off + 2 * 128 * 8;
+  static constexpr int total = misc_off + 16;
+  static_assert(total <= 232448, "shared memory of one CTA");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using L = Layout<D>;
+  constexpr int DH = L::DH, NS = L::NS;
+  extern __shared__ __align__(1024) uint8_t smem[];  // no slack left to align by hand: checked
+  if (smem_u32(smem) & 1023) {
+    if (threadIdx.x == 0) report_error(p.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 50);
+    return;
+  }
+  Bars<NS>* bars = reinterpret_cast<Bars<NS>*>(smem + L::bar_off);
+  Seg* segs = reinterpret_cast<Seg*>(smem + L::seg_off);
+  float2* ml_s = reinterpret_cast<float2*>(smem + L::ml_off);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc_off + 4);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = warp_id(), lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bars->kv_full[i], 1);
+      mbar_init(&bars->kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 4);
+    }
+    mbar_init(&bars->o_full, 1);
+    mbar_init(&bars->o_empty, 8);
+    mbar_init(&bars->ml_full, 8);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&bars->seg_full[i], 1);
+      mbar_init(&bars->seg_empty[i], 11);  // producer, query tiles, MMA, 8 softmax warps
+    }
+    mbar_init(&bars->drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  // the previous kernel of the stream may still be running (programmatic launch):
+  // wait for it before any global access; this CTA already holds its tensor memory
+  grid_dep_wait();
+  grid_dep_launch();
+
+  auto fail = [&](int site, int detail) {
+    report_error(p.status, KVPOP_ERR_TIMEOUT, site, detail);
+    *abort_flag = 1;
+  };
+  // segment n, once the walker has written it; false at the end of the work
+  auto get_seg = [&](int n, Seg& s) -> bool {
+    if (!mbar_wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1, abort_flag)) {
+      fail(SITE_PREFIX_PRODUCER, 3);
+      return false;
+    }
+    s = segs[n % kSegs];
+    mbar_arrive(&bars->seg_empty[n % kSegs]);
+    return s.NT > 0;
+  };
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsIo>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ K / V producer
+      tma_prefetch_desc(&p.tk);
+      tma_prefetch_desc(&p.tv);
+      Seg s;
+      int seq = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap* map, int t) {
+        const int st = seq % NS;
+        if (!mbar_wait(&bars->kv_empty[st], ((seq / NS) & 1) ^ 1, abort_flag)) {
+          fail(SITE_PREFIX_PRODUCER, 1);
+          ok = false;
+          return;
+        }
+        mbar_arrive_expect_tx(&bars->kv_full[st], L::kTile);
+        for (int dh = 0; dh < DH; ++dh)
+          tma_load_4d(smem + L::kv_off + st * L::kTile + dh * kBlockBytes, map, &bars->kv_full[st], dh * 64, s.h,
+                      (s.kt0 + t) * kKeys, s.j);
+        ++seq;
+      };
+      for (int n = 0; ok && get_seg(n, s); ++n) {
+        const int ahead = s.two() ? 1 : 2;  // K tiles before the first V
+        for (int t = 0; ok && t < min(ahead, s.NT); ++t) load(&p.tk, t);
+        for (int t = 0; ok && t < s.NT; ++t) {
+          load(&p.tv, t);
+          if (ok && t + ahead < s.NT) load(&p.tk, t + ahead);
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      // Event e of a segment is stream w = (e & 1) ^ par and key tile e (or e / 2 with two
+      // row tiles).  S runs two events ahead of P V, into the next segment, so S of a
+      // stream always follows P V of the stream's event before.
+      // TMEM: S / P of stream w at column 128 w, O at 256 + 128 w.
+      constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16(128, D, 1);
+      const uint32_t q_addr = sbase + L::q_off, kv_addr = sbase + L::kv_off;
+      struct Ev {
+        int NT, flags;  // of its segment; NT = 0 at the end
+        int e, n, sb;   // event, segment number, loads before the segment
+        uint32_t par;
+      };
+      Ev a = {0, 0, 0, 0, 0, 0}, b = a;  // next S, next P V
+      auto fetch = [&](Ev& x, bool last_reader) {
+        x.NT = 0;
+        if (!mbar_wait(&bars->seg_full[x.n % kSegs], (x.n / kSegs) & 1, abort_flag)) {
+          fail(SITE_PREFIX_MMA, 6);
+          return;
+        }
+        x.NT = segs[x.n % kSegs].NT;
+        x.flags = segs[x.n % kSegs].flags;
+        if (last_reader) mbar_arrive(&bars->seg_empty[x.n % kSegs]);
+      };
+      auto step = [&](Ev& x, bool last_reader) {
+        const int events = (x.flags & 1) ? 2 * x.NT : x.NT;
+        if (++x.e < events) return;
+        x.par ^= events & 1;
+        x.sb += 2 * x.NT;
+        ++x.n;
+        x.e = 0;
+        fetch(x, last_reader);
+      };
+      fetch(a, false);
+      fetch(b, true);
+      uint32_t np = 0;  // bit w: parity of stream w's next P
+      bool ok = true;
+      auto wait_bar = [&](uint64_t* bar, uint32_t ph, int detail) -> bool {
+        if (!mbar_wait(bar, ph, abort_flag)) {
+          fail(SITE_PREFIX_MMA, detail);
+          return false;
+        }
+        tc_fence_after();
+        return true;
+      };
+      auto issue_s = [&]() {
+        const bool two = a.flags & 1;
+        const int w = (a.e & 1) ^ a.par, t = two ? a.e >> 1 : a.e, qt = two ? a.e & 1 : 0;
+        const int seq = a.sb + pos_k(two, t), st = seq % NS;
+        if (a.e == 0 && !(ok = wait_bar(&bars->q_full, a.n & 1, 1))) return;
+        if (!(ok = wait_bar(&bars->kv_full[st], (seq / NS) & 1, 2))) return;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int dh = ks >> 2;
+          const uint32_t w32 = (uint32_t)(ks & 3) * 32;
+          mma_ss(tbase + 128 * w, smem_desc_sw128(q_addr + (qt * DH + dh) * kBlockBytes + w32, 16, 1024),
+                 smem_desc_sw128(kv_addr + st * L::kTile + dh * kBlockBytes + w32, 16, 1024), idesc_qk,
+                 ks > 0 ? 1u : 0u);
+        }
+        mma_commit(&bars->s_full[w]);
+        if (!two || (a.e & 1)) mma_commit(&bars->kv_empty[st]);
+        if (a.e == (two ? 2 * a.NT : a.NT) - 1) mma_commit(&bars->q_empty);
+        step(a, false);
+      };
+      for (int i = 0; i < 2 && ok && a.NT; ++i) issue_s();
+      while (ok && b.NT) {
+        const bool two = b.flags & 1;
+        const int w = (b.e & 1) ^ b.par, t = two ? b.e >> 1 : b.e;
+        const int seq = b.sb + pos_v(two, b.NT, t), st = seq % NS;
+        if (!(ok = wait_bar(&bars->p_full[w], (np >> w) & 1, 3))) break;
+        np ^= 1u << w;
+        if (!(ok = wait_bar(&bars->kv_full[st], (seq / NS) & 1, 4))) break;
+        if (b.e == 0 && !(ok = wait_bar(&bars->o_empty, (b.n & 1) ^ 1, 5))) break;
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          mma_ts(tbase + 256 + 128 * w, tbase + 128 * w + ks * 8,
+                 smem_desc_sw128(kv_addr + st * L::kTile + ks * 2048, DH > 1 ? kBlockBytes : 16, 1024), idesc_pv,
+                 (b.e > 1 || ks > 0) ? 1u : 0u);
+        if (!two || (b.e & 1)) mma_commit(&bars->kv_empty[st]);
+        if (b.e == (two ? 2 * b.NT : b.NT) - 1) mma_commit(&bars->o_full);
+        step(b, true);
+        if (a.NT) issue_s();
+      }
+      // drain every issued MMA before teardown
+      mma_commit(&bars->drain);
+      mbar_wait(&bars->drain, 0, nullptr);
+    } else if (warp == 2 && lane == 0) {
+      // ------------------------------------------------------------ query tiles
+      tma_prefetch_desc(&p.tq);
+      Seg s;
+      for (int n = 0; get_seg(n, s); ++n) {
+        if (!mbar_wait(&bars->q_empty, (n & 1) ^ 1, abort_flag)) {
+          fail(SITE_PREFIX_PRODUCER, 2);
+          break;
+        }
+        const int tiles = s.two() ? 2 : 1;
+        mbar_arrive_expect_tx(&bars->q_full, tiles * L::kTile);
+        for (int i = 0; i < tiles; ++i)
+          for (int dh = 0; dh < DH; ++dh)
+            tma_load_4d(smem + L::q_off + i * L::kTile + dh * kBlockBytes, &p.tq, &bars->q_full, dh * 64, s.h * p.G,
+                        s.seq0 + i * (p.seqs / 2), 0);
+      }
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ the CTA's share
+      // all units, then the group in which this CTA's share begins
+      long long U = 0;
+      for (int j0 = 0; j0 < p.m; j0 += 32) {
+        const long long x = j0 + lane < p.m ? group_of(p, j0 + lane).units : 0, incl = scan_incl(x);
+        if (blockIdx.x == 0 && j0 + lane < p.m) p.unit0[j0 + lane] = U + incl - x;
+        U += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (blockIdx.x == 0 && lane == 0) p.unit0[p.m] = U;
+      const int C = (int)min((long long)gridDim.x, U);
+      Walk walk = {0, 0, 0, 0};
+      if ((int)blockIdx.x < C) {
+        walk.u = first_unit(U, C, blockIdx.x);
+        walk.end = first_unit(U, C, blockIdx.x + 1);
+        long long base = 0;
+        for (int j0 = 0; j0 < p.m; j0 += 32) {
+          const long long x = j0 + lane < p.m ? group_of(p, j0 + lane).units : 0, incl = scan_incl(x);
+          const unsigned past = __ballot_sync(0xffffffffu, base + incl > walk.u);
+          if (past) {
+            const int l = __ffs(past) - 1;
+            walk.j = j0 + l;
+            walk.base = base + __shfl_sync(0xffffffffu, incl - x, l);
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
+      if (lane == 0) {
+        for (int n = 0;; ++n) {
+          const Seg s = walk.next(p);
+          if (!mbar_wait(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag)) {
+            fail(SITE_PREFIX_PRODUCER, 4);
+            break;
+          }
+          segs[n % kSegs] = s;
+          mbar_arrive(&bars->seg_full[n % kSegs]);
+          if (s.NT == 0) break;
+        }
+      }
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax
+    const int w = (warp - 4) >> 2;  // stream
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_col = 128 * w, o_col = 256 + 128 * w, o_oth = 256 + 128 * (w ^ 1);
+    const float sl2 = p.scale_log2;
+    const uint64_t s2 = pack2(sl2, sl2);
+    uint32_t cnt = 0, par = 0, nml = 0;
+    int sb = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!warp_wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1, abort_flag)) {
+        if (lane == 0) fail(SITE_PREFIX_SOFTMAX, 3);
+        break;
+      }
+      const Seg& s = segs[n % kSegs];
+      if (s.NT == 0) break;
+      const bool two = s.two();
+      const int a = w ^ par;  // row tile, or first key tile
+      const int steps = two ? s.NT : (s.NT - a + 1) / 2;
+      const int rrow = two ? 128 * a + row : row;  // row within the block
+      const bool warp_on = rrow - lane < s.nrow, row_on = rrow < s.nrow;
+      float m_ref = neg_inf(), l = 0.0f;
+      for (int i = 0; i < steps; ++i, ++cnt) {
+        const int t = two ? i : 2 * i + a;
+        if (!warp_wait(&bars->s_full[w], cnt & 1, abort_flag)) {
+          if (lane == 0) fail(SITE_PREFIX_SOFTMAX, 1);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int left = s.len - (s.kt0 + t) * kKeys;  // keys of this tile within the length
+        if (warp_on) {
+          // the whole S row of this thread (128 fp32) in registers; keys past the length -> -inf
+          uint32_t sr[4][32];
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) tmem_ld32(tl + s_col + ch * 32, sr[ch]);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) tmem_wait_ld_dep(sr[ch]);
+          float mt = neg_inf();
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            if (left < ch * 32 + 32) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (ch * 32 + c >= left) sr[ch][c] = 0xff800000u;
+            }
+            mt = fmaxf(mt, max32(sr[ch]));
+          }
+          const float m_new = fmaxf(m_ref, mt);
+          const bool need = (m_new - m_ref) * sl2 > kRescaleLog2;  // true when m_ref == -inf and mt finite
+          float alpha = 1.0f;
+          if (need) {
+            alpha = ex2_approx((m_ref - m_new) * sl2);
+            l *= alpha;
+            m_ref = m_new;
+          }
+          if (__any_sync(0xffffffffu, need) && i > 0) {
+            // O of this stream's last event is complete: S of this one was issued after it
+#pragma unroll
+            for (int cd = 0; cd < D / 32; ++cd) {
+              uint32_t r[32];
+              tmem_ld32(tl + o_col + cd * 32, r);
+              tmem_wait_ld_dep(r);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
+              tmem_st32(tl + o_col + cd * 32, r);
+            }
+            tmem_wait_st();
+          }
+          // P = exp2(s * scale_log2 - m) as bf16, written over S
+          const float nm = (m_ref == neg_inf()) ? 0.0f : -m_ref * sl2;
+          const uint64_t n2 = pack2(nm, nm);
+          uint64_t lacc = 0;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const uint64_t xx = fma2(pack2(__uint_as_float(sr[ch][c]), __uint_as_float(sr[ch][c + 1])), s2, n2);
+              float e0, e1;
+              unpack2(xx, e0, e1);
+              const float p0 = ex2_approx(e0), p1 = ex2_approx(e1);
+              lacc = add2(lacc, pack2(p0, p1));
+              pk[c >> 1] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(tl + s_col + ch * 16, pk);
+          }
+          float l0, l1;
+          unpack2(lacc, l0, l1);
+          l += l0 + l1;
+          tmem_wait_st();
+        }
+        if (left < kKeys && s.len < p.P) {
+          // V rows past the length hold anything, and 0 * NaN would be NaN: zero them
+          const int seq = sb + pos_v(two, s.NT, t), st = seq % NS;
+          if (!warp_wait(&bars->kv_full[st], (seq / NS) & 1, abort_flag)) {
+            if (lane == 0) fail(SITE_PREFIX_SOFTMAX, 2);
+            ok = false;
+            break;
+          }
+          if (row >= left) {
+#pragma unroll
+            for (int dh = 0; dh < DH; ++dh) {
+              uint4* r = reinterpret_cast<uint4*>(smem + L::kv_off + st * L::kTile + dh * kBlockBytes + row * 128);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) r[u] = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[w]);
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      const size_t orow = (size_t)(s.seq0 + rrow / p.G) * p.Hq + s.h * p.G + rrow % p.G;
+      // read before lse, which may be lse2, is written
+      const float j2 = s.whole() && p.o2 != nullptr && row_on ? p.lse2[orow] * 1.4426950408889634f : neg_inf();
+      float w_own = 1.0f, w_oth = 0.0f;
+      // no weight: -inf; a NaN among the scores keeps a finite maximum and travels in l
+      float m2 = l == 0.0f ? neg_inf() : (m_ref == neg_inf() ? 0.0f : m_ref * sl2);
+      if (!warp_wait(&bars->o_full, n & 1, abort_flag)) {
+        if (lane == 0) fail(SITE_PREFIX_EPILOGUE, 1);
+        break;
+      }
+      tc_fence_after();
+      if (!two) {
+        // join the two streams.  O of this segment is complete, so every warp has left the
+        // segment before (o_empty) and has read its exchange: one buffer is enough.
+        ml_s[w * 128 + row] = make_float2(m2, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->ml_full);
+        if (!warp_wait(&bars->ml_full, nml & 1, abort_flag)) {
+          if (lane == 0) fail(SITE_PREFIX_EPILOGUE, 2);
+          break;
+        }
+        ++nml;
+        const float2 o = ml_s[(w ^ 1) * 128 + row];
+        const float M = fmaxf(m2, o.x);
+        w_own = m2 != neg_inf() ? ex2_approx(m2 - M) : 0.0f;
+        w_oth = o.x != neg_inf() ? ex2_approx(o.x - M) : 0.0f;
+        l = l * w_own + o.y * w_oth;
+        m2 = M;
+      }
+      // a single-tile segment's columns are shared out between the two streams
+      const int c_lo = two ? 0 : w * (D / 2), c_n = two ? D : D / 2;
+      const bool both = !two && s.NT > 1, mine = two || steps > 0;
+      float w_j = 0.0f;
+      if (s.whole()) {
+        const float T = fmaxf(m2, j2);
+        const float w_p = m2 != neg_inf() ? ex2_approx(m2 - T) : 0.0f;
+        w_j = j2 != neg_inf() ? ex2_approx(j2 - T) : 0.0f;
+        l = l * w_p + w_j;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        w_own *= w_p * inv;
+        w_oth *= w_p * inv;
+        w_j *= inv;
+        m2 = T;
+      }
+      if (warp_on) {
+        const size_t slot = (size_t)blockIdx.x * 2 + s.slot();
+        float4* po = p.part_o + (slot * 2 + (two ? a : 0)) * (D / 4) * 128 + row;
+#pragma unroll 1
+        for (int c0 = c_lo; c0 < c_lo + c_n; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32(tl + (mine ? o_col : o_oth) + c0, r);
+          tmem_wait_ld_dep(r);
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]) * (mine ? w_own : w_oth);
+          if (both) {
+            tmem_ld32(tl + o_oth + c0, r);
+            tmem_wait_ld_dep(r);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] += __uint_as_float(r[c]) * w_oth;
+          }
+          if (row_on && s.whole()) {
+            if (w_j != 0.0f) {
+              const uint4* j = reinterpret_cast<const uint4*>(p.o2 + orow * D + c0);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const uint4 y = j[u];
+                const uint32_t yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  v[8 * u + 2 * c] += w_j * __uint_as_float(yy[c] << 16);
+                  v[8 * u + 2 * c + 1] += w_j * __uint_as_float(yy[c] & 0xffff0000u);
+                }
+              }
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.O + orow * D + c0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              dst[u] = make_uint4(pack_bf16x2(v[8 * u], v[8 * u + 1]), pack_bf16x2(v[8 * u + 2], v[8 * u + 3]),
+                                  pack_bf16x2(v[8 * u + 4], v[8 * u + 5]), pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+          } else if (row_on) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              po[(size_t)(c0 / 4 + u) * 128] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+          }
+          __syncwarp();
+        }
+        if (row_on && c_lo == 0) {
+          if (s.whole())
+            p.lse[orow] = l != 0.0f ? (m2 + __log2f(l)) * 0.69314718055994531f : neg_inf();
+          else
+            p.part_ml[slot * kBlockRows + rrow] = make_float2(m2, l);
+        }
+      }
+      tc_fence_before();
+      par ^= (two ? 2 * s.NT : s.NT) & 1;
+      sb += 2 * s.NT;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars->o_empty);
+        mbar_arrive(&bars->seg_empty[n % kSegs]);
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// One CTA per (sequence, KV head): joins the slots of its G rows and (O2, lse2).
+// Rows that prefix_kernel finished, and rows outside the groups, are left alone.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) prefix_merge(const __grid_constant__ PrefixParams p, int ctas) {
   grid_dep_launch();
   grid_dep_wait();
-  int g = -1;
-  if (!p.cu) {
-    g = 0;
-  } else {
-    int seen = 0;
-    for (int j = 0; j < p.m; ++j) {
-      const int lo = max(seen, min(p.cu[j], p.n)), hi = max(lo, min(p.cu[j + 1], p.n));
-      if (i >= lo && i < hi) g = j;
-      seen = hi;
+  const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H;
+  int j = 0;  // the last group that begins at or before sequence i
+  if (p.cu) {
+    int hi = p.m;
+    while (hi - j > 1) {
+      const int mid = (j + hi) >> 1;
+      if (p.cu[mid] <= i) j = mid;
+      else hi = mid;
     }
   }
-  if (g < 0) return;
-  const int len = p.lens ? max(0, min(p.lens[g], p.P)) : p.P;
-  const size_t row = (size_t)i * p.Hq + hq;
-  float qr[E], o[E] = {};
-  for (int e = 0; e < E; ++e) qr[e] = __bfloat162float(p.q[row * D + lane * E + e]) * p.scale_log2;
-  const float ninf = __int_as_float(0xff800000);
-  float mx = ninf, l = 0.f;
-  for (int t = warp; t < len; t += 8) {
-    const size_t at = (((size_t)g * p.P + t) * p.H + h) * D + lane * E;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += qr[e] * __bfloat162float(p.k[at + e]);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(mx, s);
-    const float a = mn == ninf ? 1.f : exp2f(mx - mn), w = mn == ninf ? 0.f : exp2f(s - mn);
-    l = l * a + w;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * __bfloat162float(p.v[at + e]);
-    mx = mn;
+  const Group g = group_of(p, j);
+  if (i < g.lo || i >= g.hi) return;
+  const int row0 = (i - g.lo) % p.seqs * p.G, rb = (i - g.lo) / p.seqs;
+  int c0 = 0, c1 = -1, first_slot = 0;  // the CTAs that had key tiles of this row block
+  if (g.nt > 0) {
+    const long long U = p.unit0[p.m], u0 = p.unit0[j] + ((long long)rb * p.H + h) * g.nt;
+    const int C = (int)min((long long)ctas, U);
+    c0 = cta_of(U, C, u0);
+    c1 = cta_of(U, C, u0 + g.nt - 1);
+    if (c0 == c1) return;  // one CTA had them all, and finished the rows
+    first_slot = 1;        // the block begins in c0's share; it reaches into the others'
   }
-  if (lane == 0) m_s[warp] = mx, l_s[warp] = l;
-  for (int e = 0; e < E; ++e) o_s[warp][lane * E + e] = o[e];
-  const float j2 = p.o2 ? p.lse2[row] * 1.4426950408889634f : ninf;  // read before lse, which may be lse2, is written
-  __syncthreads();
-  if (threadIdx.x < D) {
-    const int d = threadIdx.x;
-    float M = j2, L = 0.f, O = 0.f;
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, m_s[w]);
-    for (int w = 0; w < 8; ++w)
-      if (m_s[w] != ninf) {
-        const float f = exp2f(m_s[w] - M);
-        L += f * l_s[w];
-        O += f * o_s[w][d];
+  const int G = p.G;
+  for (int x0 = 0; x0 < G * (D / 4); x0 += kMergeThreads) {
+    const int x = x0 + threadIdx.x;
+    const bool on = x < G * (D / 4);
+    const int r = row0 + x % G, c4 = x / G;
+    const size_t orow = (size_t)i * p.Hq + h * G + x % G;
+    float j2 = neg_inf(), M = neg_inf(), l = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
+      if (p.o2) j2 = p.lse2[orow] * 1.4426950408889634f;
+      M = j2;
+      for (int c = c0; c <= c1; ++c) {
+        const size_t slot = (size_t)c * 2 + (c == c0 ? first_slot : 0);
+        M = fmaxf(M, p.part_ml[slot * kBlockRows + r].x);
       }
-    if (j2 != ninf) {
-      const float f = exp2f(j2 - M);
-      L += f;
-      O += f * __bfloat162float(p.o2[row * D + d]);
+      for (int c = c0; c <= c1; ++c) {
+        const size_t slot = (size_t)c * 2 + (c == c0 ? first_slot : 0);
+        const float2 ml = p.part_ml[slot * kBlockRows + r];
+        const float4 y = p.part_o[((slot * 2 + (r >> 7)) * (D / 4) + c4) * 128 + (r & 127)];
+        const float f = ml.x != neg_inf() ? ex2_approx(ml.x - M) : 0.0f;
+        l += f * ml.y;
+        if (f != 0.0f) {
+          o.x += f * y.x;
+          o.y += f * y.y;
+          o.z += f * y.z;
+          o.w += f * y.w;
+        }
+      }
+      if (j2 != neg_inf()) {
+        const float f = ex2_approx(j2 - M);
+        l += f;
+        if (f != 0.0f) {
+          const uint2 y = *reinterpret_cast<const uint2*>(p.o2 + orow * D + 4 * c4);
+          o.x += f * __uint_as_float(y.x << 16);
+          o.y += f * __uint_as_float(y.x & 0xffff0000u);
+          o.z += f * __uint_as_float(y.y << 16);
+          o.w += f * __uint_as_float(y.y & 0xffff0000u);
+        }
+      }
     }
-    p.O[row * D + d] = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
-    __syncwarp();
-    if (d == 0) p.lse[row] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : ninf;
+    __syncthreads();  // lse, which may be lse2, is written after every thread has read it
+    if (on) {
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+      *reinterpret_cast<uint2*>(p.O + orow * D + 4 * c4) =
+          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+      if (c4 == 0) p.lse[orow] = l != 0.0f ? (M + __log2f(l)) * 0.69314718055994531f : neg_inf();
+    }
   }
+}
+
+int max_ctas(int n, int m, int P, int H, int G) {
+  const long long units = (m + (long long)n * G / kBlockRows) * H * ((P + kKeys - 1ll) / kKeys);
+  return (int)min((long long)num_sms(), units);
+}
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+size_t ml_offset(int m) { return round256((size_t)(m + 1) * 8); }
+size_t o_offset(int m, int ctas) { return ml_offset(m) + (size_t)ctas * 2 * kBlockRows * 8; }
+
+template <int D>
+kvpop_status launch(PrefixParams& prm, int ctas, cudaStream_t cs) {
+  using L = Layout<D>;
+  auto kern = prefix_kernel<D>;
+  kvpop_status st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total),
+                               "kvpop_prefix_attn: smem attribute");
+  if (st != KVPOP_OK) return st;
+  // the register re-split must fit in the launch allocation (granule: 8 per thread)
+  cudaFuncAttributes fa;
+  st = cuda_check(cudaFuncGetAttributes(&fa, kern), "kvpop_prefix_attn: attributes");
+  if (st != KVPOP_OK) return st;
+  if (((fa.numRegs + 7) / 8) * 8 < kRegsNeeded) {
+    set_last_error("kvpop_prefix_attn: kernel built with %d registers per thread, %d needed", fa.numRegs, kRegsNeeded);
+    return KVPOP_ERR_INTERNAL;
+  }
+  st = cuda_check(launch_pdl(kern, dim3(ctas), dim3(kThreads), L::total, cs, prm), "kvpop_prefix_attn: launch");
+  if (st != KVPOP_OK) return st;
+  return cuda_check(launch_pdl(prefix_merge<D>, dim3((unsigned)((long long)prm.n * prm.H)), dim3(kMergeThreads), 0, cs,
+                               prm, ctas),
+                    "kvpop_prefix_attn: merge launch");
 }
 
 }  // namespace
@@ -99,7 +766,8 @@ extern "C" kvpop_status kvpop_prefix_attn_workspace_size(int n, int m, int P, in
     set_last_error("kvpop_prefix_attn_workspace_size: D=%d (64 or 128), G=%d (dividing 128) unsupported", D, Hq / H);
     return KVPOP_ERR_UNSUPPORTED;
   }
-  *bytes = 256;
+  const int ctas = max_ctas(n, m, P, H, Hq / H);
+  *bytes = o_offset(m, ctas) + (size_t)ctas * 2 * kBlockRows * D * 4;
   return KVPOP_OK;
 }
 
@@ -133,28 +801,42 @@ extern "C" kvpop_status kvpop_prefix_attn(const void* q, const void* pk, const v
     set_last_error("kvpop_prefix_attn: q, pk, pv, O, O2 must be 16-byte, workspace 256-byte aligned");
     return KVPOP_ERR_UNSUPPORTED;
   }
-  if (H > 65535 || Hq > 65535 || m > 65535 || n > (1 << 24)) {
-    set_last_error("kvpop_prefix_attn: at most 65535 heads and prefixes and 2^24 sequences");
+  if (H > 65535 || Hq > 65535 || m > 65535 || n > (1 << 24) || (long long)n * H > 0x7fffffffll) {
+    set_last_error("kvpop_prefix_attn: at most 65535 heads and prefixes, 2^24 sequences and 2^31 - 1 sequence heads");
     return KVPOP_ERR_UNSUPPORTED;
   }
-  PrefixParams prm = {};
-  prm.q = (const __nv_bfloat16*)q;
-  prm.k = (const __nv_bfloat16*)pk;
-  prm.v = (const __nv_bfloat16*)pv;
+  const int G = Hq / H;
+  PrefixParams prm;
+  memset(&prm, 0, sizeof(prm));
+  const uint64_t dq[4] = {(uint64_t)D, (uint64_t)Hq, (uint64_t)n, 1};
+  const uint64_t sq[3] = {(uint64_t)D * 2, (uint64_t)Hq * D * 2, (uint64_t)n * Hq * D * 2};
+  const uint32_t bq[4] = {64, (uint32_t)G, (uint32_t)(128 / G), 1};
+  const uint64_t dk[4] = {(uint64_t)D, (uint64_t)H, (uint64_t)P, (uint64_t)m};
+  const uint64_t sk[3] = {(uint64_t)D * 2, (uint64_t)H * D * 2, (uint64_t)P * H * D * 2};
+  const uint32_t bk[4] = {64, 1, kKeys, 1};
+  if (!make_tmap_4d(&prm.tq, q, dq, sq, bq) || !make_tmap_4d(&prm.tk, pk, dk, sk, bk) ||
+      !make_tmap_4d(&prm.tv, pv, dk, sk, bk))
+    return KVPOP_ERR_CUDA;
+  const int ctas = max_ctas(n, m, P, H, G);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   prm.cu = cu;
   prm.lens = lens;
   prm.o2 = (const __nv_bfloat16*)O2;
   prm.lse2 = lse2;
   prm.O = (__nv_bfloat16*)O;
   prm.lse = lse;
+  prm.unit0 = reinterpret_cast<long long*>(ws);
+  prm.part_ml = reinterpret_cast<float2*>(ws + ml_offset(m));
+  prm.part_o = reinterpret_cast<float4*>(ws + o_offset(m, ctas));
+  prm.status = device_status_ptr();
   prm.n = n;
   prm.m = m;
   prm.P = P;
   prm.Hq = Hq;
   prm.H = H;
-  prm.G = Hq / H;
+  prm.G = G;
+  prm.seqs = kBlockRows / G;
   prm.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
-  auto kern = D == 128 ? prefix_simple<128> : prefix_simple<64>;
-  return cuda_check(launch_pdl(kern, dim3(n, Hq), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), prm),
-                    "kvpop_prefix_attn: launch");
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  return D == 128 ? launch<128>(prm, ctas, cs) : launch<64>(prm, ctas, cs);
 }
