@@ -34,6 +34,8 @@
 // maxima are moved lazily, when they grow by more than 2^8.
 #include <string.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace kvpop {
@@ -734,16 +736,22 @@ template <int D>
 kvpop_status launch(PrefixParams& prm, int ctas, cudaStream_t cs) {
   using L = Layout<D>;
   auto kern = prefix_kernel<D>;
-  kvpop_status st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total),
-                               "kvpop_prefix_attn: smem attribute");
-  if (st != KVPOP_OK) return st;
-  // the register re-split must fit in the launch allocation (granule: 8 per thread)
-  cudaFuncAttributes fa;
-  st = cuda_check(cudaFuncGetAttributes(&fa, kern), "kvpop_prefix_attn: attributes");
-  if (st != KVPOP_OK) return st;
-  if (((fa.numRegs + 7) / 8) * 8 < kRegsNeeded) {
-    set_last_error("kvpop_prefix_attn: kernel built with %d registers per thread, %d needed", fa.numRegs, kRegsNeeded);
-    return KVPOP_ERR_INTERNAL;
+  kvpop_status st = KVPOP_OK;
+  static std::atomic<uint64_t> ready{0};  // bit d: the kernel is set up on device d
+  const int dev = current_device();
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total),
+                    "kvpop_prefix_attn: smem attribute");
+    if (st != KVPOP_OK) return st;
+    // the register re-split must fit in the launch allocation (granule: 8 per thread)
+    cudaFuncAttributes fa;
+    st = cuda_check(cudaFuncGetAttributes(&fa, kern), "kvpop_prefix_attn: attributes");
+    if (st != KVPOP_OK) return st;
+    if (((fa.numRegs + 7) / 8) * 8 < kRegsNeeded) {
+      set_last_error("kvpop_prefix_attn: kernel built with %d registers per thread, %d needed", fa.numRegs, kRegsNeeded);
+      return KVPOP_ERR_INTERNAL;
+    }
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   st = cuda_check(launch_pdl(kern, dim3(ctas), dim3(kThreads), L::total, cs, prm), "kvpop_prefix_attn: launch");
   if (st != KVPOP_OK) return st;

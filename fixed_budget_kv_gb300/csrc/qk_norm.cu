@@ -16,16 +16,18 @@
 //
 // Angles: f / 2 pi becomes a 64-bit fixed-point fraction of a turn, so the
 // product with an integer position wraps at whole turns without any loss; the
-// top 32 bits, as a signed number, go to sincospif.  The rounding of f / 2 pi to
-// 53 bits leaves 2^-33 rad at position 2^20.
+// top 32 bits, as a signed number, go to sincospif.  The fraction is off by at
+// most 1 + f units of 2^-64, which leaves 2^-30 rad at position 2^31 (f <= 1).
 #include "common.cuh"
 
 namespace kvpop {
 namespace {
 
-constexpr int kWarps = 4;           // per CTA
-constexpr int kCtasPerSm = 4;       // grid limit: resident CTAs
-constexpr int kBwdMaxCtas = 1024;   // rows of the weight gradients' workspace
+constexpr int kWarps = 4;          // per CTA
+constexpr int kCtasPerSm = 6;      // grid limit: resident CTAs
+constexpr int kBwdWarps = 8;
+constexpr int kBwdCtasPerSm = 2;
+constexpr int kBwdMaxCtas = 1024;  // rows of the weight gradients' workspace
 
 struct QkParams {
   const __nv_bfloat16* q;
@@ -42,7 +44,8 @@ struct QkParams {
   const float* dk;
   float* part;      // backward only: [CTAs, D] partial weight gradients
   int T, S, Hq, H, nrot;  // nrot = R / 16: lanes of a row that rotate
-  int slices;             // warps that share a token's heads
+  int slices;             // warps that share a token's heads (backward: its query heads)
+  int slices_k;           // backward only: warps that share a token's key heads
   int ctas_q;             // backward only: CTAs that take query heads
   float eps;
 };
@@ -74,11 +77,19 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// Turns per position as a fraction of 2^64 (whole turns dropped).
+// Turns per position as a fraction of 2^64, whole turns dropped: the 24-bit
+// significand times 2^64 / 2 pi, moved to the exponent's place.
 __device__ __forceinline__ unsigned long long turns64(float f) {
-  double t = (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= floor(t);
-  return (unsigned long long)(t * 18446744073709551616.0);
+  const uint32_t u = __float_as_uint(f);
+  const int exp = (int)(u >> 23 & 255), sh = 150 - exp;  // |f| = sig 2^-sh
+  const unsigned long long sig = exp ? (u & 0x7fffffu) | 0x800000u : 0ull;
+  const unsigned long long c = 0x28be60db9391054aull;  // 2^64 / (2 pi)
+  const unsigned long long lo = sig * c, hi = __umul64hi(sig, c);
+  unsigned long long r;
+  if (sh <= 0) r = sh > -64 ? lo << -sh : 0ull;
+  else if (sh < 64) r = lo >> sh | hi << (64 - sh);
+  else r = sh < 128 ? hi >> (sh - 64) : 0ull;
+  return u >> 31 ? 0ull - r : r;
 }
 
 // The eight angles of lane j = lane % LPR: each of the 32 / LPR row groups computes
@@ -125,69 +136,110 @@ __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float
   }
 }
 
+// The passes of a warp's tasks, one after the other: pass ps of token t takes head
+// rows ps * RPP .. of the Hq + H rows.  Loads run one pass ahead, into the next task.
+struct Passes {
+  long long task, ntask, step;
+  int t, ps, p1;
+
+  __device__ __forceinline__ void enter(int slices, int passes) {
+    if (task >= ntask) return;
+    int sl = 0;
+    t = (int)task;
+    if (slices > 1) {
+      t = (int)(task / slices);
+      sl = (int)(task - (long long)t * slices);
+    }
+    ps = passes * sl / slices;
+    p1 = passes * (sl + 1) / slices;
+  }
+  __device__ __forceinline__ bool live() const { return task < ntask; }
+  __device__ __forceinline__ void next(int slices, int passes) {
+    if (++ps < p1) return;
+    task += step;
+    enter(slices, passes);
+  }
+};
+
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_fwd(const QkParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) qk_norm_fwd(const QkParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;
   __shared__ __align__(16) float w_s[2][D];
   const int lane = lane_id(), j = lane % LPR, rg = lane / LPR;
   grid_dep_launch();
   grid_dep_wait();  // the projections, positions and weights come from earlier kernels
+  int pa, pb;
+  pieces<INTER>(j, p.nrot, pa, pb);
+  const int rows = p.Hq + p.H, passes = (rows + RPP - 1) / RPP;
+  Passes cur;
+  cur.task = (long long)blockIdx.x * kWarps + warp_id();
+  cur.ntask = (long long)p.T * p.slices;
+  cur.step = (long long)gridDim.x * kWarps;
+  cur.enter(p.slices, passes);
+  auto load = [&](const Passes& c, uint4& a, uint4& b) {
+    const int row = c.ps * RPP + rg;
+    if (!c.live() || row >= rows) return;
+    const __nv_bfloat16* src = row >= p.Hq ? p.k + c.t * p.k_stride + (size_t)(row - p.Hq) * D
+                                           : p.q + c.t * p.q_stride + (size_t)row * D;
+    a = reinterpret_cast<const uint4*>(src)[pa];
+    b = reinterpret_cast<const uint4*>(src)[pb];
+  };
+  uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+  load(cur, ra, rb);
   for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
     const float* w = i < D ? p.wq : p.wk;
     w_s[i / D][i % D] = w ? w[i % D] : 1.0f;
   }
-  __syncthreads();
   Angles<LPR> ang;
   if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
-  int pa, pb;
-  pieces<INTER>(j, p.nrot, pa, pb);
-  const int rows = p.Hq + p.H, passes = (rows + RPP - 1) / RPP;
-  const long long ntask = (long long)p.T * p.slices;
-  for (long long task = (long long)blockIdx.x * kWarps + warp_id(); task < ntask;
-       task += (long long)gridDim.x * kWarps) {
-    const int t = (int)(task / p.slices), sl = (int)(task % p.slices);
-    const int p0 = (int)((long long)passes * sl / p.slices), p1 = (int)((long long)passes * (sl + 1) / p.slices);
-    if (p.nrot) ang.at(p.pos ? p.pos[t] : t % p.S, j);
-    for (int ps = p0; ps < p1; ++ps) {
-      const int row = ps * RPP + rg;
-      const bool on = row < rows, is_k = row >= p.Hq;
-      float a[8] = {}, b[8] = {};
-      if (on) {
-        const __nv_bfloat16* src =
-            is_k ? p.k + t * p.k_stride + (size_t)(row - p.Hq) * D : p.q + t * p.q_stride + (size_t)row * D;
-        unpack8(reinterpret_cast<const uint4*>(src)[pa], a);
-        unpack8(reinterpret_cast<const uint4*>(src)[pb], b);
-      }
-      float ss = 0.f;
+  __syncthreads();
+  bool fresh = true;
+#pragma unroll 1
+  while (cur.live()) {
+    Passes nxt = cur;
+    nxt.next(p.slices, passes);
+    uint4 na = make_uint4(0, 0, 0, 0), nb = na;
+    load(nxt, na, nb);
+    if (fresh && p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j);
+    const int row = cur.ps * RPP + rg;
+    const bool is_k = row >= p.Hq;
+    float a[8], b[8];
+    unpack8(ra, a);
+    unpack8(rb, b);
+    float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+    for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
 #pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-      const float* wa = &w_s[is_k][8 * pa];
-      const float* wb = &w_s[is_k][8 * pb];
+    for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+    const float* wa = &w_s[is_k][8 * pa];
+    const float* wb = &w_s[is_k][8 * pb];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] = a[e] * r * wa[e];
-        b[e] = b[e] * r * wb[e];
-      }
-      if (j < p.nrot) rotate<INTER>(a, b, ang.c, ang.s, 1.0f);
-      if (on) {
-        __nv_bfloat16* dst =
-            is_k ? p.k_out + t * p.ko_stride + (size_t)(row - p.Hq) * D : p.q_out + t * p.qo_stride + (size_t)row * D;
-        reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
-        reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
-      }
+    for (int e = 0; e < 8; ++e) {
+      a[e] = a[e] * r * wa[e];
+      b[e] = b[e] * r * wb[e];
     }
+    if (j < p.nrot) rotate<INTER>(a, b, ang.c, ang.s, 1.0f);
+    if (row < rows) {
+      __nv_bfloat16* dst = is_k ? p.k_out + cur.t * p.ko_stride + (size_t)(row - p.Hq) * D
+                                : p.q_out + cur.t * p.qo_stride + (size_t)row * D;
+      reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
+      reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
+    }
+    fresh = nxt.task != cur.task;
+    cur = nxt;
+    ra = na;
+    rb = nb;
   }
 }
 
 // CTAs [0, ctas_q) take the query heads, the others the key heads, so that a lane
-// keeps the weights and the weight gradient of its 16 columns in registers.
+// keeps the weight gradient of its 16 columns in registers.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_bwd(const QkParams p) {
+__global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(const QkParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;
-  __shared__ float red[kWarps][D];
+  __shared__ float red[kBwdWarps][D];
+  __shared__ __align__(16) float w_s[D];
   const int lane = lane_id(), warp = warp_id(), j = lane % LPR, rg = lane / LPR;
   grid_dep_launch();
   grid_dep_wait();
@@ -200,65 +252,87 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_bwd(const QkParams p) {
   const float* g_base = is_k ? p.dk : p.dq;
   __nv_bfloat16* o_base = is_k ? p.k_out : p.q_out;
   const float* w = is_k ? p.wk : p.wq;
-  Angles<LPR> ang;
-  if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
   int pa, pb;
   pieces<INTER>(j, p.nrot, pa, pb);
-  float wa[8], wb[8], da[8] = {}, db[8] = {};
+  const int passes = (heads + RPP - 1) / RPP, slices = is_k ? p.slices_k : p.slices;
+  Passes cur;
+  cur.task = (long long)cta * kBwdWarps + warp;
+  cur.ntask = (long long)p.T * slices;
+  cur.step = (long long)ctas * kBwdWarps;
+  cur.enter(slices, passes);
+  struct Raw {
+    uint4 xa, xb;
+    float4 g[4];
+  };
+  auto load = [&](const Passes& c, Raw& v) {
+    const int row = c.ps * RPP + rg;
+    v.xa = v.xb = make_uint4(0, 0, 0, 0);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    wa[e] = w ? w[8 * pa + e] : 1.0f;
-    wb[e] = w ? w[8 * pb + e] : 1.0f;
-  }
-  const int passes = (heads + RPP - 1) / RPP;
-  const int slices = min(p.slices, passes);
-  const long long ntask = (long long)p.T * slices;
-  for (long long task = (long long)cta * kWarps + warp; task < ntask; task += (long long)ctas * kWarps) {
-    const int t = (int)(task / slices), sl = (int)(task % slices);
-    const int p0 = (int)((long long)passes * sl / slices), p1 = (int)((long long)passes * (sl + 1) / slices);
-    if (p.nrot) ang.at(p.pos ? p.pos[t] : t % p.S, j);
-    for (int ps = p0; ps < p1; ++ps) {
-      const int row = ps * RPP + rg;
-      const bool on = row < heads;
-      float a[8] = {}, b[8] = {}, ga[8] = {}, gb[8] = {};
-      if (on) {
-        const __nv_bfloat16* src = x_base + t * x_stride + (size_t)row * D;
-        unpack8(reinterpret_cast<const uint4*>(src)[pa], a);
-        unpack8(reinterpret_cast<const uint4*>(src)[pb], b);
-        const float4* g = reinterpret_cast<const float4*>(g_base + ((size_t)t * heads + row) * D);
-        const float4 g0 = g[2 * pa], g1 = g[2 * pa + 1], g2 = g[2 * pb], g3 = g[2 * pb + 1];
-        ga[0] = g0.x, ga[1] = g0.y, ga[2] = g0.z, ga[3] = g0.w;
-        ga[4] = g1.x, ga[5] = g1.y, ga[6] = g1.z, ga[7] = g1.w;
-        gb[0] = g2.x, gb[1] = g2.y, gb[2] = g2.z, gb[3] = g2.w;
-        gb[4] = g3.x, gb[5] = g3.y, gb[6] = g3.z, gb[7] = g3.w;
-      }
-      if (j < p.nrot) rotate<INTER>(ga, gb, ang.c, ang.s, -1.0f);  // g is now dL/dy
-      float ss = 0.f, ex = 0.f;
+    for (int i = 0; i < 4; ++i) v.g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!c.live() || row >= heads) return;
+    const __nv_bfloat16* src = x_base + c.t * x_stride + (size_t)row * D;
+    v.xa = reinterpret_cast<const uint4*>(src)[pa];
+    v.xb = reinterpret_cast<const uint4*>(src)[pb];
+    const float4* g = reinterpret_cast<const float4*>(g_base + ((size_t)c.t * heads + row) * D);
+    v.g[0] = g[2 * pa];
+    v.g[1] = g[2 * pa + 1];
+    v.g[2] = g[2 * pb];
+    v.g[3] = g[2 * pb + 1];
+  };
+  Raw raw;
+  load(cur, raw);
+  float da[8] = {}, db[8] = {};
+  for (int i = threadIdx.x; i < D; i += kBwdWarps * 32) w_s[i] = w ? w[i] : 1.0f;
+  const float* wa = &w_s[8 * pa];
+  const float* wb = &w_s[8 * pb];
+  Angles<LPR> ang;
+  if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
+  __syncthreads();
+  bool fresh = true;
+#pragma unroll 1
+  while (cur.live()) {
+    Passes nxt = cur;
+    nxt.next(slices, passes);
+    float a[8], b[8], ga[8], gb[8];
+    unpack8(raw.xa, a);
+    unpack8(raw.xb, b);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ga[4 * i] = raw.g[i].x, ga[4 * i + 1] = raw.g[i].y, ga[4 * i + 2] = raw.g[i].z, ga[4 * i + 3] = raw.g[i].w;
+      gb[4 * i] = raw.g[2 + i].x, gb[4 * i + 1] = raw.g[2 + i].y, gb[4 * i + 2] = raw.g[2 + i].z,
+             gb[4 * i + 3] = raw.g[2 + i].w;
+    }
+    load(nxt, raw);
+    if (fresh && p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j);
+    if (j < p.nrot) rotate<INTER>(ga, gb, ang.c, ang.s, -1.0f);  // g is now dL/dy
+    float ss = 0.f, ex = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      ss += a[e] * a[e] + b[e] * b[e];
+      ex += ga[e] * wa[e] * a[e] + gb[e] * wb[e] * b[e];
+    }
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      ex += __shfl_xor_sync(0xffffffffu, ex, o);
+    }
+    const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+    const float back = r * r * (ex * (1.0f / D));
+    const int row = cur.ps * RPP + rg;
+    if (row < heads) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        ss += a[e] * a[e] + b[e] * b[e];
-        ex += ga[e] * wa[e] * a[e] + gb[e] * wb[e] * b[e];
+        da[e] += ga[e] * (a[e] * r);
+        db[e] += gb[e] * (b[e] * r);
+        a[e] = r * (ga[e] * wa[e] - a[e] * back);
+        b[e] = r * (gb[e] * wb[e] - b[e] * back);
       }
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        ex += __shfl_xor_sync(0xffffffffu, ex, o);
-      }
-      const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-      const float back = r * r * (ex * (1.0f / D));
-      if (on) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          da[e] += ga[e] * (a[e] * r);
-          db[e] += gb[e] * (b[e] * r);
-          a[e] = r * (ga[e] * wa[e] - a[e] * back);
-          b[e] = r * (gb[e] * wb[e] - b[e] * back);
-        }
-        __nv_bfloat16* dst = o_base + t * o_stride + (size_t)row * D;
-        reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
-        reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
-      }
+      __nv_bfloat16* dst = o_base + cur.t * o_stride + (size_t)row * D;
+      reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
+      reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
     }
+    fresh = nxt.task != cur.task;
+    cur = nxt;
   }
   // this CTA's sums over its rows, in a fixed order
 #pragma unroll
@@ -274,17 +348,17 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_bwd(const QkParams p) {
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < D; i += kWarps * 32) {
+  for (int i = threadIdx.x; i < D; i += kBwdWarps * 32) {
     float v = 0.f;
-    for (int u = 0; u < kWarps; ++u) v += red[u][i];
+    for (int u = 0; u < kBwdWarps; ++u) v += red[u][i];
     p.part[(size_t)blockIdx.x * D + i] = v;
   }
 }
 
-// dwq / dwk from the CTAs' sums: CTA = 32 columns of one of the two, 8 warps over the rows.
-__global__ void __launch_bounds__(256)
+// dwq / dwk from the CTAs' sums: CTA = 32 columns of one of the two, 32 warps over the rows.
+__global__ void __launch_bounds__(1024)
     qk_norm_dw(const float* part, int D, int ctas_q, int ctas, float* dwq, float* dwk) {
-  __shared__ float red[8][32];
+  __shared__ float red[32][33];
   grid_dep_launch();
   grid_dep_wait();
   const int nc = D / 32;
@@ -292,15 +366,16 @@ __global__ void __launch_bounds__(256)
   const int col = (blockIdx.x % nc) * 32 + lane_id();
   const int lo = is_k ? ctas_q : 0, hi = is_k ? ctas : ctas_q;
   float v = 0.f;
-  for (int i = lo + warp_id(); i < hi; i += 8) v += part[(size_t)i * D + col];
+#pragma unroll 4
+  for (int i = lo + warp_id(); i < hi; i += 32) v += part[(size_t)i * D + col];
   red[warp_id()][lane_id()] = v;
   __syncthreads();
-  if (warp_id() == 0) {
-    v = 0.f;
-    for (int u = 0; u < 8; ++u) v += red[u][lane_id()];
-    float* dw = is_k ? dwk : dwq;
-    if (dw) dw[col] = v;
-  }
+  // warp u sums column u
+  v = red[lane_id()][warp_id()];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  float* dw = is_k ? dwk : dwq;
+  if (dw && lane_id() == 0) dw[(blockIdx.x % nc) * 32 + warp_id()] = v;
 }
 
 kvpop_status check_common(const char* what, const void* q, long long q_stride, const void* k, long long k_stride, int b,
@@ -351,11 +426,22 @@ kvpop_status check_common(const char* what, const void* q, long long q_stride, c
   return KVPOP_OK;
 }
 
-// Warps that share one token: as many as it takes to give every resident warp a task,
-// at most one a pass.
-int pick_slices(long long T, int passes, int warps) {
-  const long long want = (warps + T - 1) / T;
-  return (int)(want < passes ? want : passes);
+// Warps that share one token.  A warp's time is its rounds times (passes of a task + the
+// token's angles, worth about kAngleCost passes); shares of a token fill the last round
+// and, with few tokens, the SMs.
+constexpr float kAngleCost = 1.4f;
+int pick_slices(long long T, int passes, long long warps) {
+  int best = 1;
+  float best_cost = 3.0e38f;
+  for (int s = 1; s <= passes; ++s) {
+    const float cost = (float)((T * s + warps - 1) / warps) * ((passes + s - 1) / s + kAngleCost);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+    if (T * s > 16 * warps) break;  // more than 16 rounds: the last one hardly counts
+  }
+  return best;
 }
 
 }  // namespace
@@ -392,7 +478,7 @@ extern "C" kvpop_status kvpop_qk_norm_rope(const void* q, int64_t q_stride, cons
   p.eps = eps;
   const int rpp = 512 / D, passes = (Hq + H + rpp - 1) / rpp;
   const int max_ctas = num_sms() * kCtasPerSm;
-  p.slices = pick_slices(p.T, passes, max_ctas * kWarps);
+  p.slices = pick_slices(p.T, passes, (long long)max_ctas * kWarps);
   const long long ntask = (long long)p.T * p.slices;
   const long long ctas = (ntask + kWarps - 1) / kWarps;
   const dim3 grid((unsigned)(ctas < max_ctas ? ctas : max_ctas));
@@ -464,21 +550,22 @@ extern "C" kvpop_status kvpop_qk_norm_rope_bwd(const void* q, int64_t q_stride, 
   p.nrot = R / 16;
   p.eps = eps;
   const int rpp = 512 / D, pq = (Hq + rpp - 1) / rpp, pk = (H + rpp - 1) / rpp;
-  const int max_ctas = min(num_sms() * kCtasPerSm, kBwdMaxCtas);
-  p.slices = pick_slices(p.T, pq + pk, max_ctas * kWarps);
+  const int max_ctas = min(num_sms() * kBwdCtasPerSm, kBwdMaxCtas);
   // the two kinds of CTAs in proportion to their passes
-  const long long tasks_q = (long long)p.T * min(p.slices, pq), tasks_k = (long long)p.T * min(p.slices, pk);
-  const int share_q = max(1, min(max_ctas - 1, (int)((long long)max_ctas * pq / (pq + pk))));
-  const int ctas_q = (int)min((long long)share_q, (tasks_q + kWarps - 1) / kWarps);
-  const int ctas_k = (int)min((long long)(max_ctas - share_q), (tasks_k + kWarps - 1) / kWarps);
+  const int share_q = max(1, min(max_ctas - 1, (int)(((long long)max_ctas * pq + (pq + pk) / 2) / (pq + pk))));
+  const int share_k = max_ctas - share_q;
+  p.slices = pick_slices(p.T, pq, (long long)share_q * kBwdWarps);
+  p.slices_k = pick_slices(p.T, pk, (long long)share_k * kBwdWarps);
+  const int ctas_q = (int)min((long long)share_q, ((long long)p.T * p.slices + kBwdWarps - 1) / kBwdWarps);
+  const int ctas_k = (int)min((long long)share_k, ((long long)p.T * p.slices_k + kBwdWarps - 1) / kBwdWarps);
   p.ctas_q = ctas_q;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   auto kern = D == 128 ? (interleaved ? qk_norm_bwd<128, true> : qk_norm_bwd<128, false>)
                        : (interleaved ? qk_norm_bwd<64, true> : qk_norm_bwd<64, false>);
-  st = cuda_check(launch_pdl(kern, dim3(ctas_q + ctas_k), dim3(kWarps * 32), 0, cs, p),
+  st = cuda_check(launch_pdl(kern, dim3(ctas_q + ctas_k), dim3(kBwdWarps * 32), 0, cs, p),
                   "kvpop_qk_norm_rope_bwd: launch");
   if (st != KVPOP_OK || (!dwq && !dwk)) return st;
-  return cuda_check(launch_pdl(qk_norm_dw, dim3(2 * D / 32), dim3(256), 0, cs, (const float*)workspace, D, ctas_q,
+  return cuda_check(launch_pdl(qk_norm_dw, dim3(2 * D / 32), dim3(1024), 0, cs, (const float*)workspace, D, ctas_q,
                                ctas_q + ctas_k, dwq, dwk),
                     "kvpop_qk_norm_rope_bwd: weight gradient launch");
 }

@@ -122,12 +122,13 @@ def _check(st: int, what: str):
 
 
 def _p(t):
-    return None if t is None else c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return c_void_p(s.cuda_stream)
+    if stream is None:  # the handle itself: building a torch.cuda.Stream costs several microseconds a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _need(t, dtype, name):
@@ -139,23 +140,36 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _same(ref, *named):
-    """The tensors that are given are on ref's device, and that is the current one."""
-    if ref.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {ref.device}: make it the current device first")
-    for t, name in named:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+def _device(t, name):
+    """Index of the CUDA device that t is on, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}: make it the current device first")
+    return dev
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+def _fit(t, dtype, dev, shape, name):
+    """A contiguous CUDA tensor of this type and shape on device dev."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return
+    _need(t, dtype, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+_here = contextlib.nullcontext()
+
+
+def _empty_as(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _on(stream):
     """Memory that a call allocates belongs to the stream that uses it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _here if stream is None else torch.cuda.stream(stream)
 
 
 def device_status(reset: bool = True):
@@ -346,41 +360,47 @@ def boundary_loss(r_hat, t_bnd, y, w: int, n: int, log_gamma, tau: float, omega=
 # before the attention: per-head norm of q and k with the position rotation
 # ----------------------------------------------------------------------------
 
-def _token_stride(t, name):
+def _token_stride(t, shape, dev, name):
     """Elements between the tokens of a bf16 [b, S, heads, D] view whose heads are contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [b, S, heads, D]")
-    b, S, heads, D = t.shape
-    if (D > 1 and t.stride(3) != 1) or (heads > 1 and t.stride(2) != D):
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype is not torch.bfloat16:
+            raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    b, S, heads, D = shape
+    if t.is_contiguous():
+        return heads * D
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 or (heads > 1 and s2 != D):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if S > 1:
-        if b > 1 and t.stride(0) != S * t.stride(1):
+        if b > 1 and s0 != S * s1:
             raise ValueError(f"{name}: the tokens must be evenly spaced over the batch")
-        return t.stride(1)
-    return t.stride(0) if b > 1 else heads * D
+        return s1
+    return s0 if b > 1 else heads * D
 
 
 def _qk_args(q, k, wq, wk, inv_freq, pos):
-    sq, sk = _token_stride(q, "q"), _token_stride(k, "k")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [b, S, Hq, D] and k [b, S, H, D]")
     b, S, Hq, D = q.shape
-    _shape(k, (b, S, k.shape[2], D), "k")
-    for t, name in ((wq, "wq"), (wk, "wk")):
-        if t is not None:
-            _need(t, torch.float32, name)
-            _shape(t, (D,), name)
+    H = k.shape[2]
+    dev = _device(q, "q")
+    sq, sk = _token_stride(q, (b, S, Hq, D), dev, "q"), _token_stride(k, (b, S, H, D), dev, "k")
+    if wq is not None:
+        _fit(wq, torch.float32, dev, (D,), "wq")
+    if wk is not None:
+        _fit(wk, torch.float32, dev, (D,), "wk")
     R = 0
     if inv_freq is not None:
-        _need(inv_freq, torch.float32, "inv_freq")
         R = 2 * inv_freq.numel()
+        _fit(inv_freq, torch.float32, dev, (R // 2,), "inv_freq")
     if pos is not None:
-        _need(pos, torch.int32, "pos")
-        _shape(pos, (b, S), "pos")
-    _same(q, (k, "k"), (wq, "wq"), (wk, "wk"), (inv_freq, "inv_freq"), (pos, "pos"))
-    return sq, sk, b, S, Hq, k.shape[2], D, R
+        _fit(pos, torch.int32, dev, (b, S), "pos")
+    return dev, sq, sk, b, S, Hq, H, D, R
 
 
 def qk_norm_rope(q, k, wq, wk, eps: float, inv_freq, pos=None, interleaved: bool = False, out=None, stream=None):
@@ -388,19 +408,16 @@ def qk_norm_rope(q, k, wq, wk, eps: float, inv_freq, pos=None, interleaved: bool
     None) and the rotation of the first 2 * len(inv_freq) dims at positions pos (int32
     [b,S]; None: 0..S-1).  q and k may be views of a packed projection.  Returns
     contiguous (q_out, k_out); a decode step's n tokens are [n,1,heads,D]."""
-    sq, sk, b, S, Hq, H, D, R = _qk_args(q, k, wq, wk, inv_freq, pos)
+    dev, sq, sk, b, S, Hq, H, D, R = _qk_args(q, k, wq, wk, inv_freq, pos)
     if out is None:
         with _on(stream):
-            qo = torch.empty((b, S, Hq, D), dtype=torch.bfloat16, device=q.device)
-            ko = torch.empty((b, S, H, D), dtype=torch.bfloat16, device=q.device)
+            qo, ko = _empty_as(q), _empty_as(k)
     else:
         qo, ko = out
-        for t, x, name in ((qo, q, "q_out"), (ko, k, "k_out")):
-            _need(t, torch.bfloat16, name)
-            _shape(t, x.shape, name)
-        _same(q, (qo, "q_out"), (ko, "k_out"))
-    _check(load().kvpop_qk_norm_rope(_p(q), sq, _p(k), sk, b, S, Hq, H, D, _p(wq), _p(wk), float(eps), _p(inv_freq), R,
-                                     int(bool(interleaved)), _p(pos), _p(qo), _p(ko), _stream(stream)),
+        _fit(qo, torch.bfloat16, dev, q.shape, "q_out")
+        _fit(ko, torch.bfloat16, dev, k.shape, "k_out")
+    _check(load().kvpop_qk_norm_rope(_p(q), sq, _p(k), sk, b, S, Hq, H, D, _p(wq), _p(wk), eps, _p(inv_freq), R,
+                                     1 if interleaved else 0, _p(pos), _p(qo), _p(ko), _stream(stream)),
            "kvpop_qk_norm_rope")
     return qo, ko
 
@@ -417,32 +434,28 @@ def qk_norm_rope_bwd(q, k, dq, dk, wq, wk, eps: float, inv_freq, pos=None, inter
     (attn_bwd's): (dq_in, dk_in bf16, dwq, dwk fp32 [D]).  q and k are the forward's
     inputs.  `out` may hold views of a packed projection's gradient, and None for a
     weight gradient that is not wanted."""
-    sq, sk, b, S, Hq, H, D, R = _qk_args(q, k, wq, wk, inv_freq, pos)
-    for t, x, name in ((dq, q, "dq"), (dk, k, "dk")):
-        _need(t, torch.float32, name)
-        _shape(t, x.shape, name)
-    _same(q, (dq, "dq"), (dk, "dk"), (workspace, "workspace"))
+    dev, sq, sk, b, S, Hq, H, D, R = _qk_args(q, k, wq, wk, inv_freq, pos)
+    _fit(dq, torch.float32, dev, q.shape, "dq")
+    _fit(dk, torch.float32, dev, k.shape, "dk")
     with _on(stream):
         if workspace is None:
             workspace = torch.empty(qk_norm_rope_bwd_workspace_size(D), dtype=torch.uint8, device=q.device)
+        else:
+            _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
         if out is None:
-            out = (torch.empty((b, S, Hq, D), dtype=torch.bfloat16, device=q.device),
-                   torch.empty((b, S, H, D), dtype=torch.bfloat16, device=q.device),
-                   torch.empty(D, dtype=torch.float32, device=q.device),
-                   torch.empty(D, dtype=torch.float32, device=q.device))
-    dqi, dki, dwq, dwk = out
-    _shape(dqi, q.shape, "dq_in")
-    _shape(dki, k.shape, "dk_in")
-    for t, name in ((dwq, "dwq"), (dwk, "dwk")):
-        if t is not None:
-            _need(t, torch.float32, name)
-            _shape(t, (D,), name)
-    _same(q, (dqi, "dq_in"), (dki, "dk_in"), (dwq, "dwq"), (dwk, "dwk"))
-    _need(workspace, torch.uint8, "workspace")
-    _check(load().kvpop_qk_norm_rope_bwd(_p(q), sq, _p(k), sk, _p(dq), _p(dk), b, S, Hq, H, D, _p(wq), _p(wk), float(eps),
-                                         _p(inv_freq), R, int(bool(interleaved)), _p(pos), _p(dqi),
-                                         _token_stride(dqi, "dq_in"), _p(dki), _token_stride(dki, "dk_in"), _p(dwq),
-                                         _p(dwk), _p(workspace), workspace.numel(), _stream(stream)),
+            dqi, dki = _empty_as(q), _empty_as(k)
+            dwq, dwk = (torch.empty(D, dtype=torch.float32, device=q.device) for _ in range(2))
+            so, sp = Hq * D, H * D
+        else:
+            dqi, dki, dwq, dwk = out
+            so, sp = _token_stride(dqi, q.shape, dev, "dq_in"), _token_stride(dki, k.shape, dev, "dk_in")
+            if dwq is not None:
+                _fit(dwq, torch.float32, dev, (D,), "dwq")
+            if dwk is not None:
+                _fit(dwk, torch.float32, dev, (D,), "dwk")
+    _check(load().kvpop_qk_norm_rope_bwd(_p(q), sq, _p(k), sk, _p(dq), _p(dk), b, S, Hq, H, D, _p(wq), _p(wk), eps,
+                                         _p(inv_freq), R, 1 if interleaved else 0, _p(pos), _p(dqi), so, _p(dki), sp,
+                                         _p(dwq), _p(dwk), _p(workspace), workspace.numel(), _stream(stream)),
            "kvpop_qk_norm_rope_bwd")
     return dqi, dki, dwq, dwk
 
@@ -463,40 +476,35 @@ def prefix_attn(q, pk, pv, cu=None, lens=None, join=None, scale: float = 0.0, wo
     one prefix) and sees the first lens[j] keys (int32 [m]; None: all P).  `join` =
     (O2 [n,Hq,D] bf16, lse2 [n,Hq] fp32), the rows' attention over other keys such as
     Cache.step's, makes the result the attention over both.  Returns (O, lse)."""
-    for t, name in ((q, "q"), (pk, "pk"), (pv, "pv")):
-        _need(t, torch.bfloat16, name)
     if q.dim() != 3 or pk.dim() != 4:
         raise ValueError("q must be [n, Hq, D] and pk [m, P, H, D]")
-    n, Hq, D = q.shape
+    n, Hq, D = rows = q.shape
     m, P, H, _ = pk.shape
-    _shape(pk, (m, P, H, D), "pk")
-    _shape(pv, (m, P, H, D), "pv")
-    for t, size, name in ((cu, m + 1, "cu"), (lens, m, "lens")):
-        if t is not None:
-            _need(t, torch.int32, name)
-            _shape(t, (size,), name)
-    O2, lse2 = (None, None) if join is None else join
+    dev = _device(q, "q")
+    _fit(q, torch.bfloat16, dev, rows, "q")
+    _fit(pk, torch.bfloat16, dev, (m, P, H, D), "pk")
+    _fit(pv, torch.bfloat16, dev, (m, P, H, D), "pv")
+    if cu is not None:
+        _fit(cu, torch.int32, dev, (m + 1,), "cu")
+    if lens is not None:
+        _fit(lens, torch.int32, dev, (m,), "lens")
+    O2 = lse2 = None
     if join is not None:
-        _need(O2, torch.bfloat16, "O2")
-        _need(lse2, torch.float32, "lse2")
-        _shape(O2, (n, Hq, D), "O2")
-        _shape(lse2, (n, Hq), "lse2")
+        O2, lse2 = join
+        _fit(O2, torch.bfloat16, dev, rows, "O2")
+        _fit(lse2, torch.float32, dev, (n, Hq), "lse2")
     with _on(stream):
         if out is None:
-            O = torch.empty_like(q)
-            lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+            O, lse = torch.empty_like(q), torch.empty((n, Hq), dtype=torch.float32, device=q.device)
         else:
             O, lse = out
-            _need(O, torch.bfloat16, "O")
-            _need(lse, torch.float32, "lse")
-            _shape(O, (n, Hq, D), "O")
-            _shape(lse, (n, Hq), "lse")
+            _fit(O, torch.bfloat16, dev, rows, "O")
+            _fit(lse, torch.float32, dev, (n, Hq), "lse")
         if workspace is None:
             workspace = torch.empty(prefix_attn_workspace_size(n, m, P, Hq, H, D), dtype=torch.uint8, device=q.device)
-    _need(workspace, torch.uint8, "workspace")
-    _same(q, (pk, "pk"), (pv, "pv"), (cu, "cu"), (lens, "lens"), (O2, "O2"), (lse2, "lse2"), (O, "O"), (lse, "lse"),
-          (workspace, "workspace"))
-    _check(load().kvpop_prefix_attn(_p(q), _p(pk), _p(pv), n, m, P, Hq, H, D, float(scale), _p(cu), _p(lens), _p(O2),
+        else:
+            _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
+    _check(load().kvpop_prefix_attn(_p(q), _p(pk), _p(pv), n, m, P, Hq, H, D, scale, _p(cu), _p(lens), _p(O2),
                                     _p(lse2), _p(O), _p(lse), _p(workspace), workspace.numel(), _stream(stream)),
            "kvpop_prefix_attn")
     return O, lse
