@@ -24,7 +24,7 @@ namespace kvpop {
 namespace {
 
 constexpr int kWarps = 4;          // per CTA
-constexpr int kCtasPerSm = 6;      // grid limit: resident CTAs
+constexpr int kCtasPerSm = 5;      // grid limit: resident CTAs
 constexpr int kBwdWarps = 8;
 constexpr int kBwdCtasPerSm = 2;
 constexpr int kBwdMaxCtas = 1024;  // rows of the weight gradients' workspace
@@ -63,18 +63,43 @@ __device__ __forceinline__ void pieces(int j, int nrot, int& a, int& b) {
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+// Eight bf16 values as four pairs of fp32, and back with one rounding.
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t (&x)[4]) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const uint64_t (&x)[4]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(x[i], lo, hi);
+    u[i] = pack_bf16x2(lo, hi);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return lo + hi;
+}
+
+// Eight floats of shared memory as four pairs.
+__device__ __forceinline__ void lds8(const float* s, uint64_t (&x)[4]) {
+  const float4 u = reinterpret_cast<const float4*>(s)[0], v = reinterpret_cast<const float4*>(s)[1];
+  x[0] = pack2(u.x, u.y);
+  x[1] = pack2(u.z, u.w);
+  x[2] = pack2(v.x, v.y);
+  x[3] = pack2(v.z, v.w);
 }
 
 // Turns per position as a fraction of 2^64, whole turns dropped: the 24-bit
@@ -98,7 +123,7 @@ template <int LPR>
 struct Angles {
   static constexpr int RPP = 32 / LPR, MINE = 8 / RPP;
   unsigned long long turn[MINE];
-  float c[8], s[8];
+  uint64_t c[4], s[4], ns[4];  // cos, sin and -sin of angles (2 i, 2 i + 1)
 
   __device__ __forceinline__ void init(const float* inv_freq, int j, int rg, int nrot) {
 #pragma unroll
@@ -111,35 +136,51 @@ struct Angles {
       const unsigned long long a = turn[i] * (unsigned long long)(long long)pos;
       sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &ms[i], &mc[i]);  // half turns in [-1, 1]
     }
+    float cc[8], ss[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int src = (e / MINE) * LPR + j;
-      c[e] = __shfl_sync(0xffffffffu, mc[e % MINE], src);
-      s[e] = __shfl_sync(0xffffffffu, ms[e % MINE], src);
+      cc[e] = __shfl_sync(0xffffffffu, mc[e % MINE], src);
+      ss[e] = __shfl_sync(0xffffffffu, ms[e % MINE], src);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = pack2(cc[2 * i], cc[2 * i + 1]);
+      s[i] = pack2(ss[2 * i], ss[2 * i + 1]);
+      ns[i] = pack2(-ss[2 * i], -ss[2 * i + 1]);
+    }
+  }
+  // Half-split pairs sit at the same place of the two pieces, adjacent pairs next to each
+  // other in one of them.  BACK turns the other way.
+  template <bool INTER, bool BACK>
+  __device__ __forceinline__ void rotate(uint64_t (&a)[4], uint64_t (&b)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!INTER) {
+        const uint64_t u = fma2(b[i], BACK ? s[i] : ns[i], mul2(a[i], c[i]));
+        b[i] = fma2(a[i], BACK ? ns[i] : s[i], mul2(b[i], c[i]));
+        a[i] = u;
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // angle e = 2 i + h: pair e of a, or e - 4 of b
+          const int e = 2 * i + h;
+          uint64_t& y = e < 4 ? a[e & 3] : b[e & 3];
+          float u, v, c0, c1, s0, s1;
+          unpack2(y, u, v);
+          unpack2(c[i], c0, c1);
+          unpack2(s[i], s0, s1);
+          const float cs = h ? c1 : c0, sn = BACK ? -(h ? s1 : s0) : (h ? s1 : s0);
+          y = pack2(u * cs - v * sn, v * cs + u * sn);
+        }
+      }
     }
   }
 };
 
-// Pair e of a lane: half-split pairs sit at the same place of the two pieces,
-// adjacent pairs next to each other in one of them.
-template <bool INTER>
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8],
-                                       float sign) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float& u = INTER ? (e < 4 ? a[2 * e] : b[2 * e - 8]) : a[e];
-    float& v = INTER ? (e < 4 ? a[2 * e + 1] : b[2 * e - 7]) : b[e];
-    const float sn = sign * s[e];
-    const float u2 = u * c[e] - v * sn, v2 = v * c[e] + u * sn;
-    u = u2;
-    v = v2;
-  }
-}
-
 // The passes of a warp's tasks, one after the other: pass ps of token t takes head
-// rows ps * RPP .. of the Hq + H rows.  Loads run one pass ahead, into the next task.
+// rows ps * RPP .. of the token.  Loads run ahead, into the next task.
 struct Passes {
-  long long task, ntask, step;
+  uint32_t task, ntask, step;
   int t, ps, p1;
 
   __device__ __forceinline__ void enter(int slices, int passes) {
@@ -147,89 +188,110 @@ struct Passes {
     int sl = 0;
     t = (int)task;
     if (slices > 1) {
-      t = (int)(task / slices);
-      sl = (int)(task - (long long)t * slices);
+      t = (int)(task / (uint32_t)slices);
+      sl = (int)task - t * slices;
     }
     ps = passes * sl / slices;
     p1 = passes * (sl + 1) / slices;
   }
   __device__ __forceinline__ bool live() const { return task < ntask; }
-  __device__ __forceinline__ void next(int slices, int passes) {
-    if (++ps < p1) return;
+  __device__ __forceinline__ bool next(int slices, int passes) {  // true: entered another task
+    if (++ps < p1) return false;
     task += step;
     enter(slices, passes);
+    return true;
   }
 };
 
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) qk_norm_fwd(const QkParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;
-  __shared__ __align__(16) float w_s[2][D];
+  __shared__ __align__(16) float w_s[2 * D];
   const int lane = lane_id(), j = lane % LPR, rg = lane / LPR;
   grid_dep_launch();
   grid_dep_wait();  // the projections, positions and weights come from earlier kernels
   int pa, pb;
   pieces<INTER>(j, p.nrot, pa, pb);
   const int rows = p.Hq + p.H, passes = (rows + RPP - 1) / RPP;
-  Passes cur;
-  cur.task = (long long)blockIdx.x * kWarps + warp_id();
-  cur.ntask = (long long)p.T * p.slices;
-  cur.step = (long long)gridDim.x * kWarps;
+  // two cursors over this warp's passes: the one being computed and the next one to load
+  Passes cur, ahead;
+  cur.task = blockIdx.x * kWarps + warp_id();
+  cur.ntask = (uint32_t)p.T * p.slices;
+  cur.step = gridDim.x * kWarps;
   cur.enter(p.slices, passes);
-  auto load = [&](const Passes& c, uint4& a, uint4& b) {
-    const int row = c.ps * RPP + rg;
-    if (!c.live() || row >= rows) return;
-    const __nv_bfloat16* src = row >= p.Hq ? p.k + c.t * p.k_stride + (size_t)(row - p.Hq) * D
-                                           : p.q + c.t * p.q_stride + (size_t)row * D;
-    a = reinterpret_cast<const uint4*>(src)[pa];
-    b = reinterpret_cast<const uint4*>(src)[pb];
+  ahead = cur;
+  const uint4 *q_t, *k_t;  // row 0 of the token being loaded; key rows count on from the query rows
+  auto token = [&]() {
+    q_t = reinterpret_cast<const uint4*>(p.q + ahead.t * p.q_stride);
+    k_t = reinterpret_cast<const uint4*>(p.k + ahead.t * p.k_stride) - (long long)p.Hq * (D / 8);
   };
-  uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
-  load(cur, ra, rb);
+  if (cur.live()) token();
+  auto load = [&](uint4& a, uint4& b) {
+    if (!ahead.live()) return;
+    const int row = ahead.ps * RPP + rg;
+    if (row < rows) {
+      const uint4* src = (row >= p.Hq ? k_t : q_t) + row * (D / 8);
+      a = src[pa];
+      b = src[pb];
+    }
+    if (ahead.next(p.slices, passes) && ahead.live()) token();
+  };
+  uint4 r0[2], r1[2];
+  r0[0] = r0[1] = r1[0] = r1[1] = make_uint4(0, 0, 0, 0);
+  load(r0[0], r0[1]);
+  load(r1[0], r1[1]);
   for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
     const float* w = i < D ? p.wq : p.wk;
-    w_s[i / D][i % D] = w ? w[i % D] : 1.0f;
+    w_s[i] = w ? w[i % D] : 1.0f;
   }
   Angles<LPR> ang;
   if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
   __syncthreads();
+  uint4 *qo_t, *ko_t;
   bool fresh = true;
-#pragma unroll 1
-  while (cur.live()) {
-    Passes nxt = cur;
-    nxt.next(p.slices, passes);
-    uint4 na = make_uint4(0, 0, 0, 0), nb = na;
-    load(nxt, na, nb);
-    if (fresh && p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j);
+  auto pass = [&](uint4 (&raw)[2]) {
+    uint64_t a[4], b[4], wt[4];
+    unpack8(raw[0], a);
+    unpack8(raw[1], b);
+    load(raw[0], raw[1]);  // two passes ahead
+    if (fresh) {
+      qo_t = reinterpret_cast<uint4*>(p.q_out + cur.t * p.qo_stride);
+      ko_t = reinterpret_cast<uint4*>(p.k_out + cur.t * p.ko_stride) - (long long)p.Hq * (D / 8);
+      if (p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j);
+    }
     const int row = cur.ps * RPP + rg;
     const bool is_k = row >= p.Hq;
-    float a[8], b[8];
-    unpack8(ra, a);
-    unpack8(rb, b);
-    float ss = 0.f;
+    uint64_t sq = mul2(a[0], a[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
+    for (int i = 0; i < 4; ++i) {
+      if (i) sq = fma2(a[i], a[i], sq);
+      sq = fma2(b[i], b[i], sq);
+    }
+    float ss = sum2(sq);
 #pragma unroll
     for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-    const float* wa = &w_s[is_k][8 * pa];
-    const float* wb = &w_s[is_k][8 * pb];
+    const uint64_t r2 = pack2(r, r);
+    const float* w = w_s + (is_k ? D : 0);
+    lds8(w + 8 * pa, wt);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] = a[e] * r * wa[e];
-      b[e] = b[e] * r * wb[e];
-    }
-    if (j < p.nrot) rotate<INTER>(a, b, ang.c, ang.s, 1.0f);
+    for (int i = 0; i < 4; ++i) a[i] = mul2(mul2(a[i], r2), wt[i]);
+    lds8(w + 8 * pb, wt);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = mul2(mul2(b[i], r2), wt[i]);
+    if (j < p.nrot) ang.template rotate<INTER, false>(a, b);
     if (row < rows) {
-      __nv_bfloat16* dst = is_k ? p.k_out + cur.t * p.ko_stride + (size_t)(row - p.Hq) * D
-                                : p.q_out + cur.t * p.qo_stride + (size_t)row * D;
-      reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
-      reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
+      uint4* dst = (is_k ? ko_t : qo_t) + row * (D / 8);
+      dst[pa] = pack8(a);
+      dst[pb] = pack8(b);
     }
-    fresh = nxt.task != cur.task;
-    cur = nxt;
-    ra = na;
-    rb = nb;
+    fresh = cur.next(p.slices, passes);
+  };
+#pragma unroll 1
+  while (cur.live()) {
+    pass(r0);
+    if (!cur.live()) break;
+    pass(r1);
   }
 }
 
@@ -256,9 +318,9 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
   pieces<INTER>(j, p.nrot, pa, pb);
   const int passes = (heads + RPP - 1) / RPP, slices = is_k ? p.slices_k : p.slices;
   Passes cur;
-  cur.task = (long long)cta * kBwdWarps + warp;
-  cur.ntask = (long long)p.T * slices;
-  cur.step = (long long)ctas * kBwdWarps;
+  cur.task = cta * kBwdWarps + warp;
+  cur.ntask = (uint32_t)p.T * slices;
+  cur.step = ctas * kBwdWarps;
   cur.enter(slices, passes);
   struct Raw {
     uint4 xa, xb;
@@ -281,10 +343,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
   };
   Raw raw;
   load(cur, raw);
-  float da[8] = {}, db[8] = {};
+  uint64_t da[4] = {}, db[4] = {};
   for (int i = threadIdx.x; i < D; i += kBwdWarps * 32) w_s[i] = w ? w[i] : 1.0f;
-  const float* wa = &w_s[8 * pa];
-  const float* wb = &w_s[8 * pb];
   Angles<LPR> ang;
   if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
   __syncthreads();
@@ -292,59 +352,78 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
 #pragma unroll 1
   while (cur.live()) {
     Passes nxt = cur;
-    nxt.next(slices, passes);
-    float a[8], b[8], ga[8], gb[8];
+    const bool entered = nxt.next(slices, passes);
+    uint64_t a[4], b[4], ga[4], gb[4], wt[4];
     unpack8(raw.xa, a);
     unpack8(raw.xb, b);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      ga[4 * i] = raw.g[i].x, ga[4 * i + 1] = raw.g[i].y, ga[4 * i + 2] = raw.g[i].z, ga[4 * i + 3] = raw.g[i].w;
-      gb[4 * i] = raw.g[2 + i].x, gb[4 * i + 1] = raw.g[2 + i].y, gb[4 * i + 2] = raw.g[2 + i].z,
-             gb[4 * i + 3] = raw.g[2 + i].w;
+      ga[2 * i] = pack2(raw.g[i].x, raw.g[i].y);
+      ga[2 * i + 1] = pack2(raw.g[i].z, raw.g[i].w);
+      gb[2 * i] = pack2(raw.g[2 + i].x, raw.g[2 + i].y);
+      gb[2 * i + 1] = pack2(raw.g[2 + i].z, raw.g[2 + i].w);
     }
     load(nxt, raw);
     if (fresh && p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j);
-    if (j < p.nrot) rotate<INTER>(ga, gb, ang.c, ang.s, -1.0f);  // g is now dL/dy
-    float ss = 0.f, ex = 0.f;
+    if (j < p.nrot) ang.template rotate<INTER, true>(ga, gb);  // g is now dL/dy
+    uint64_t sq = 0, ex = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      ss += a[e] * a[e] + b[e] * b[e];
-      ex += ga[e] * wa[e] * a[e] + gb[e] * wb[e] * b[e];
+    for (int i = 0; i < 4; ++i) {
+      sq = fma2(a[i], a[i], sq);
+      sq = fma2(b[i], b[i], sq);
     }
+    // a weight piece at a time, twice: the registers are short
+    lds8(w_s + 8 * pa, wt);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ex = fma2(mul2(ga[i], wt[i]), a[i], ex);
+    lds8(w_s + 8 * pb, wt);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ex = fma2(mul2(gb[i], wt[i]), b[i], ex);
+    float ss = sum2(sq), es = sum2(ex);
 #pragma unroll
     for (int o = 1; o < LPR; o <<= 1) {
       ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      ex += __shfl_xor_sync(0xffffffffu, ex, o);
+      es += __shfl_xor_sync(0xffffffffu, es, o);
     }
     const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-    const float back = r * r * (ex * (1.0f / D));
+    const float back = -r * r * (es * (1.0f / D));
+    const uint64_t r2 = pack2(r, r), back2 = pack2(back, back);
     const int row = cur.ps * RPP + rg;
     if (row < heads) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        da[e] += ga[e] * (a[e] * r);
-        db[e] += gb[e] * (b[e] * r);
-        a[e] = r * (ga[e] * wa[e] - a[e] * back);
-        b[e] = r * (gb[e] * wb[e] - b[e] * back);
-      }
       __nv_bfloat16* dst = o_base + cur.t * o_stride + (size_t)row * D;
-      reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        da[i] = fma2(ga[i], mul2(a[i], r2), da[i]);
+        db[i] = fma2(gb[i], mul2(b[i], r2), db[i]);
+      }
+      lds8(w_s + 8 * pb, wt);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = mul2(fma2(b[i], back2, mul2(gb[i], wt[i])), r2);
       reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
+      lds8(w_s + 8 * pa, wt);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = mul2(fma2(a[i], back2, mul2(ga[i], wt[i])), r2);
+      reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
     }
-    fresh = nxt.task != cur.task;
+    fresh = entered;
     cur = nxt;
   }
   // this CTA's sums over its rows, in a fixed order
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
+    float lo, hi, va, vb;
+    unpack2(da[e >> 1], lo, hi);
+    va = e & 1 ? hi : lo;
+    unpack2(db[e >> 1], lo, hi);
+    vb = e & 1 ? hi : lo;
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1) {
-      da[e] += __shfl_xor_sync(0xffffffffu, da[e], o);
-      db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+      va += __shfl_xor_sync(0xffffffffu, va, o);
+      vb += __shfl_xor_sync(0xffffffffu, vb, o);
     }
     if (rg == 0) {
-      red[warp][8 * pa + e] = da[e];
-      red[warp][8 * pb + e] = db[e];
+      red[warp][8 * pa + e] = va;
+      red[warp][8 * pb + e] = vb;
     }
   }
   __syncthreads();
