@@ -10,14 +10,14 @@
 // once, so a prefix is read from memory once per 256 rows; the arithmetic is
 // rows flop a byte, memory-bound up to about that many rows.
 //
-// Work split: a unit is (group, 256-row block, KV head, 128-key tile), numbered in
-// that order, and CTA c takes the units [c U / C, (c + 1) U / C) -- one CTA an SM,
-// every SM the same number of key tiles however ragged the groups and lengths.
-// A CTA's units fall into segments of one (group, block, head) each.  A segment
+// Work split: an item is one (group, 256-row block, KV head), in that order, and has
+// kSetup units of setup and then a unit for each 128-key tile.  CTA c takes the c-th
+// part of all units, one CTA an SM, so that every SM has the same work however ragged
+// the groups and lengths.  A CTA's key tiles fall into segments of one item each.  A segment
 // that covers all key tiles is finished by its CTA; of the others a CTA has at
 // most two (it begins inside one and ends inside another), whose running
 // maximum, sum and unnormalised O go to two slots of the workspace, and
-// prefix_merge joins the slots of a row in the order of the CTAs.  No atomics:
+// prefix_merge joins the slots of an item in the order of the CTAs.  No atomics:
 // the same call gives the same bits.
 //
 // Warp roles of prefix_kernel (384 threads):
@@ -46,12 +46,19 @@ constexpr int kKeys = 128;
 constexpr int kBlockRows = 256;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
+// Time between the last tile of a segment and the first of the next, in key tiles.
+constexpr int kSetup = 4;
 constexpr int kSegs = 4;  // segments between the walker and the last reader
 // Register split: warps 0-3 drop to kRegsIo, the softmax warpgroups rise to kRegsSoftmax.
 constexpr int kRegsIo = 64;
 constexpr int kRegsSoftmax = 216;
 constexpr int kRegsNeeded = (128 * kRegsIo + 256 * kRegsSoftmax + kThreads - 1) / kThreads;
+
+// An item that several CTAs share: rows, and its CTAs c0 .. c1.  nrow = 0: none.
+struct __align__(16) Split {
+  int seq0, h, nrow, c1;
+};
 
 struct PrefixParams {
   CUtensorMap tq, tk, tv;
@@ -61,9 +68,9 @@ struct PrefixParams {
   const float* lse2;
   __nv_bfloat16* O;
   float* lse;
-  long long* unit0;  // [m + 1] first unit of each group
+  Split* split;      // [CTA] the item that the CTA is the second to work on
   float2* part_ml;   // [CTA, 2 slots, 256 rows] (maximum in log2 units, sum)
-  float4* part_o;    // [CTA, 2 slots, 2 row tiles, D / 4, 128 rows]
+  float4* part_o;    // [CTA, 2 slots, 2 row tiles, D / 4, 128 rows]: a warp's store is contiguous
   int* status;
   int n, m, P, Hq, H, G, seqs;  // seqs = 256 / G sequences of a row block
   float scale_log2;
@@ -71,10 +78,10 @@ struct PrefixParams {
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
-// Group j: its sequences [lo, hi), rows, key tiles and units.
+// Group j: its sequences [lo, hi), keys, key tiles and units (the host bounds the sum
+// of all units by 2^31).
 struct Group {
-  int lo, hi, len, nt;
-  long long rows, units;
+  int lo, hi, len, nt, units;
 };
 __device__ __forceinline__ Group group_of(const PrefixParams& p, int j) {
   Group g;
@@ -82,8 +89,7 @@ __device__ __forceinline__ Group group_of(const PrefixParams& p, int j) {
   g.hi = p.cu ? max(g.lo, min(p.cu[j + 1], p.n)) : p.n;
   g.len = p.lens ? max(0, min(p.lens[j], p.P)) : p.P;
   g.nt = (g.len + kKeys - 1) / kKeys;
-  g.rows = (long long)(g.hi - g.lo) * p.G;
-  g.units = (g.rows + kBlockRows - 1) / kBlockRows * p.H * g.nt;
+  g.units = g.nt ? (g.hi - g.lo + p.seqs - 1) / p.seqs * p.H * (g.nt + kSetup) : 0;
   return g;
 }
 
@@ -96,11 +102,18 @@ __device__ __forceinline__ long long scan_incl(long long x) {
   return x;
 }
 
-// CTA c's first unit, and the CTA that holds unit u, for U units over C CTAs.
-__device__ __forceinline__ long long first_unit(long long U, int C, int c) { return U * c / C; }
-__device__ __forceinline__ int cta_of(long long U, int C, long long u) { return (int)(((u + 1) * C + U - 1) / U) - 1; }
+// U units over C CTAs: the first U mod C of them take one more.
+struct Share {
+  int q, r;
+  __device__ __forceinline__ Share(int U, int C) : q(U / C), r(U - U / C * C) {}
+  __device__ __forceinline__ int first(int c) const { return q * c + min(c, r); }
+  __device__ __forceinline__ int cta_of(int u) const {
+    const int big = r * (q + 1);
+    return u < big ? u / (q + 1) : r + (u - big) / q;
+  }
+};
 
-// One segment: key tiles [kt0, kt0 + NT) of a row block of (group j, head h).
+// One segment: key tiles [kt0, kt0 + NT) of an item of group j, head h.
 struct __align__(16) Seg {
   int j, h, seq0, nrow;  // first sequence and rows (up to 256) of the block
   int kt0, NT, len, flags;
@@ -110,33 +123,6 @@ struct __align__(16) Seg {
   __device__ __forceinline__ bool whole() const { return flags & 2; }
   // otherwise: 0 when an earlier CTA began the block, 1 when this one did
   __device__ __forceinline__ int slot() const { return flags >> 2; }
-};
-
-// Walks the segments of units [u, end) starting in group j (first unit base).
-struct Walk {
-  long long u, end, base;
-  int j;
-  __device__ __forceinline__ Seg next(const PrefixParams& p) {
-    Seg s = {};
-    if (u >= end) return s;  // NT = 0 ends the CTA's work
-    Group g = group_of(p, j);
-    while (u >= base + g.units) {
-      base += g.units;
-      g = group_of(p, ++j);
-    }
-    const long long item = (u - base) / g.nt;
-    s.kt0 = (int)((u - base) - item * g.nt);
-    s.NT = (int)min((long long)(g.nt - s.kt0), end - u);
-    s.j = j;
-    const long long rb = item / p.H;
-    s.h = (int)(item - rb * p.H);
-    s.seq0 = g.lo + (int)rb * p.seqs;
-    s.nrow = (int)min((long long)kBlockRows, g.rows - rb * kBlockRows);
-    s.len = g.len;
-    s.flags = (s.nrow > 128 ? 1 : 0) | (s.NT == g.nt ? 2 : 0) | (s.kt0 == 0 ? 4 : 0);
-    u += s.NT;
-    return s;
-  }
 };
 
 // Place of a key tile's K and V among the segment's 2 NT loads: the order in which
@@ -319,12 +305,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const int seq = a.sb + pos_k(two, t), st = seq % NS;
         if (a.e == 0 && !(ok = wait_bar(&bars->q_full, a.n & 1, 1))) return;
         if (!(ok = wait_bar(&bars->kv_full[st], (seq / NS) & 1, 2))) return;
+        const uint32_t qlo = desc_lo(q_addr + qt * L::kTile, 16), klo = desc_lo(kv_addr + st * L::kTile, 16);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const int dh = ks >> 2;
           const uint32_t w32 = (uint32_t)(ks & 3) * 32;
-          mma_ss(tbase + 128 * w, smem_desc_sw128(q_addr + (qt * DH + dh) * kBlockBytes + w32, 16, 1024),
-                 smem_desc_sw128(kv_addr + st * L::kTile + dh * kBlockBytes + w32, 16, 1024), idesc_qk,
+          mma_ss_lo(tbase + 128 * w, qlo + (dh * kBlockBytes + w32) / 16, klo + (dh * kBlockBytes + w32) / 16, idesc_qk,
                  ks > 0 ? 1u : 0u);
         }
         mma_commit(&bars->s_full[w]);
@@ -341,11 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         np ^= 1u << w;
         if (!(ok = wait_bar(&bars->kv_full[st], (seq / NS) & 1, 4))) break;
         if (b.e == 0 && !(ok = wait_bar(&bars->o_empty, (b.n & 1) ^ 1, 5))) break;
+        const uint32_t vlo = desc_lo(kv_addr + st * L::kTile, DH > 1 ? kBlockBytes : 16);
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_ts(tbase + 256 + 128 * w, tbase + 128 * w + ks * 8,
-                 smem_desc_sw128(kv_addr + st * L::kTile + ks * 2048, DH > 1 ? kBlockBytes : 16, 1024), idesc_pv,
-                 (b.e > 1 || ks > 0) ? 1u : 0u);
+          mma_ts_lo(tbase + 256 + 128 * w, tbase + 128 * w + ks * 8, vlo + ks * (2048 / 16), idesc_pv,
+                    (b.e > 1 || ks > 0) ? 1u : 0u);
         if (!two || (b.e & 1)) mma_commit(&bars->kv_empty[st]);
         if (b.e == (two ? 2 * b.NT : b.NT) - 1) mma_commit(&bars->o_full);
         step(b, true);
@@ -372,43 +358,77 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       }
     } else if (warp == 3) {
       // ------------------------------------------------------------ the CTA's share
-      // all units, then the group in which this CTA's share begins
-      long long U = 0;
-      for (int j0 = 0; j0 < p.m; j0 += 32) {
-        const long long x = j0 + lane < p.m ? group_of(p, j0 + lane).units : 0, incl = scan_incl(x);
-        if (blockIdx.x == 0 && j0 + lane < p.m) p.unit0[j0 + lane] = U + incl - x;
-        U += __shfl_sync(0xffffffffu, incl, 31);
-      }
-      if (blockIdx.x == 0 && lane == 0) p.unit0[p.m] = U;
-      const int C = (int)min((long long)gridDim.x, U);
-      Walk walk = {0, 0, 0, 0};
+      // lane l holds group j0 + l of a window of 32 groups, and its first unit
+      long long all = 0;
+      int j0 = 0, base = 0;
+      Group g = {0, 0, 0, 0, 0};
+      auto window = [&](int w0, long long at) {  // groups w0 .., the first of them at unit `at`; returns the unit after
+        g = w0 + lane < p.m ? group_of(p, w0 + lane) : Group{0, 0, 0, 0, 0};
+        const long long incl = scan_incl(g.units);
+        j0 = w0;
+        base = (int)(at + incl - g.units);
+        return at + __shfl_sync(0xffffffffu, incl, 31);
+      };
+      for (int w0 = 0; w0 < p.m; w0 += 32) all = window(w0, all);
+      // groups that overlap, which the interface rules out, could exceed the host's bound: no work then
+      const int U = all <= 0x7fffffffll ? (int)all : 0;
+      if (blockIdx.x == 0 && lane == 0 && all != U)
+        report_error(p.status, KVPOP_ERR_INVALID_ARG, SITE_PREFIX_PRODUCER, 5);
+      const int C = min((int)gridDim.x, U);
+      const Share sh(U, max(C, 1));
+      int u = 0, end = 0;
       if ((int)blockIdx.x < C) {
-        walk.u = first_unit(U, C, blockIdx.x);
-        walk.end = first_unit(U, C, blockIdx.x + 1);
-        long long base = 0;
-        for (int j0 = 0; j0 < p.m; j0 += 32) {
-          const long long x = j0 + lane < p.m ? group_of(p, j0 + lane).units : 0, incl = scan_incl(x);
-          const unsigned past = __ballot_sync(0xffffffffu, base + incl > walk.u);
-          if (past) {
-            const int l = __ffs(past) - 1;
-            walk.j = j0 + l;
-            walk.base = base + __shfl_sync(0xffffffffu, incl - x, l);
-            break;
-          }
-          base += __shfl_sync(0xffffffffu, incl, 31);
+        u = sh.first(blockIdx.x);
+        end = sh.first(blockIdx.x + 1);
+      }
+      if (p.m > 32 && u < end) {  // back to the window in which the share begins
+        long long at = 0;
+        for (int w0 = 0;; w0 += 32) {
+          at = window(w0, at);
+          if (u < at) break;
         }
       }
-      if (lane == 0) {
-        for (int n = 0;; ++n) {
-          const Seg s = walk.next(p);
-          if (!mbar_wait(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag)) {
-            fail(SITE_PREFIX_PRODUCER, 4);
-            break;
+      Split split = {0, 0, 0, 0};
+      for (int n = 0;; ++n) {
+        Seg s = {0, 0, 0, 0, 0, 0, 0, 0};  // NT = 0 ends the work
+        while (u < end && s.NT == 0) {
+          // the group that holds unit u: the last of the window that begins at or before it
+          unsigned at = __ballot_sync(0xffffffffu, g.units > 0 && base <= u && u < base + g.units);
+          if (at == 0) {
+            window(j0 + 32, u);  // u is the window's end
+            continue;
           }
+          const int l = __ffs(at) - 1;
+          const int b = __shfl_sync(0xffffffffu, base, l), lo = __shfl_sync(0xffffffffu, g.lo, l),
+                    hi = __shfl_sync(0xffffffffu, g.hi, l), nt = __shfl_sync(0xffffffffu, g.nt, l);
+          s.len = __shfl_sync(0xffffffffu, g.len, l);
+          const int per = nt + kSetup, item = (u - b) / per, off = (u - b) - item * per;
+          const int stop = min(per, off + (end - u));  // this CTA's units of the item: [off, stop)
+          s.kt0 = max(off - kSetup, 0);
+          s.NT = max(stop - kSetup, 0) - s.kt0;
+          const int rb = item / p.H;
+          s.j = j0 + l;
+          s.h = item - rb * p.H;
+          s.seq0 = lo + rb * p.seqs;
+          s.nrow = min(p.seqs, hi - s.seq0) * p.G;
+          s.flags = (s.nrow > 128 ? 1 : 0) | (s.NT == nt ? 2 : 0) | (s.kt0 == 0 ? 4 : 0);
+          if (n == 0 && s.kt0 > 0) {
+            // the work begins inside an item; the second of its CTAs leaves word of it
+            const int first = b + item * per + kSetup;
+            split = {s.seq0, s.h, sh.cta_of(first) + 1 == (int)blockIdx.x ? s.nrow : 0, sh.cta_of(first + nt - 1)};
+          }
+          u += stop - off;
+        }
+        if (n == 0 && lane == 0) p.split[blockIdx.x] = split;
+        if (!warp_wait(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag)) {
+          if (lane == 0) fail(SITE_PREFIX_PRODUCER, 4);
+          break;
+        }
+        if (lane == 0) {
           segs[n % kSegs] = s;
           mbar_arrive(&bars->seg_full[n % kSegs]);
-          if (s.NT == 0) break;
         }
+        if (s.NT == 0) break;
       }
     }
   } else {
@@ -646,91 +666,135 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   }
 }
 
-// One CTA per (sequence, KV head): joins the slots of its G rows and (O2, lse2).
-// Rows that prefix_kernel finished, and rows outside the groups, are left alone.
+// A row's result from (maximum, sum, unnormalised O) of its four columns and the join.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge(const __grid_constant__ PrefixParams p, int ctas) {
+__device__ __forceinline__ void finish_row(const PrefixParams& p, size_t orow, int c4, float j2, float M, float l,
+                                           float4 o) {
+  const float T = fmaxf(M, j2);
+  const float w = M != neg_inf() ? ex2_approx(M - T) : 0.0f, wj = j2 != neg_inf() ? ex2_approx(j2 - T) : 0.0f;
+  l = l * w + wj;
+  o = M != neg_inf() ? make_float4(o.x * w, o.y * w, o.z * w, o.w * w) : make_float4(0.f, 0.f, 0.f, 0.f);
+  if (wj != 0.0f) {
+    const uint2 y = *reinterpret_cast<const uint2*>(p.o2 + orow * D + 4 * c4);
+    o.x += wj * __uint_as_float(y.x << 16);
+    o.y += wj * __uint_as_float(y.x & 0xffff0000u);
+    o.z += wj * __uint_as_float(y.y << 16);
+    o.w += wj * __uint_as_float(y.y & 0xffff0000u);
+  }
+  const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+  *reinterpret_cast<uint2*>(p.O + orow * D + 4 * c4) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (c4 == 0) p.lse[orow] = l != 0.0f ? (T + __log2f(l)) * 0.69314718055994531f : neg_inf();
+}
+
+// The items that several of prefix_kernel's CTAs shared, each joined from the slots of its
+// CTAs in their order: CTA (x, y < chunks) takes rows y of those whose second CTA is in the
+// x-th part of the CTAs.  Thread (part, c4, row) takes four columns and every parts-th slot;
+// the parts are joined through shared memory.
+// CTAs (x, chunks): the rows of groups without keys, which get what they join or nothing.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) prefix_merge(const __grid_constant__ PrefixParams p, int ctas, int parts,
+                                                              int chunks) {
+  constexpr int kBatch = 4;
+  __shared__ float2 ml_s[kMergeThreads];
+  __shared__ float4 o_s[kMergeThreads];
   grid_dep_launch();
   grid_dep_wait();
-  const int i = blockIdx.x / p.H, h = blockIdx.x - i * p.H;
-  int j = 0;  // the last group that begins at or before sequence i
-  if (p.cu) {
-    int hi = p.m;
-    while (hi - j > 1) {
-      const int mid = (j + hi) >> 1;
-      if (p.cu[mid] <= i) j = mid;
-      else hi = mid;
-    }
-  }
-  const Group g = group_of(p, j);
-  if (i < g.lo || i >= g.hi) return;
-  const int row0 = (i - g.lo) % p.seqs * p.G, rb = (i - g.lo) / p.seqs;
-  int c0 = 0, c1 = -1, first_slot = 0;  // the CTAs that had key tiles of this row block
-  if (g.nt > 0) {
-    const long long U = p.unit0[p.m], u0 = p.unit0[j] + ((long long)rb * p.H + h) * g.nt;
-    const int C = (int)min((long long)ctas, U);
-    c0 = cta_of(U, C, u0);
-    c1 = cta_of(U, C, u0 + g.nt - 1);
-    if (c0 == c1) return;  // one CTA had them all, and finished the rows
-    first_slot = 1;        // the block begins in c0's share; it reaches into the others'
-  }
-  const int G = p.G;
-  for (int x0 = 0; x0 < G * (D / 4); x0 += kMergeThreads) {
-    const int x = x0 + threadIdx.x;
-    const bool on = x < G * (D / 4);
-    const int r = row0 + x % G, c4 = x / G;
-    const size_t orow = (size_t)i * p.Hq + h * G + x % G;
-    float j2 = neg_inf(), M = neg_inf(), l = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on) {
-      if (p.o2) j2 = p.lse2[orow] * 1.4426950408889634f;
-      M = j2;
-      for (int c = c0; c <= c1; ++c) {
-        const size_t slot = (size_t)c * 2 + (c == c0 ? first_slot : 0);
-        M = fmaxf(M, p.part_ml[slot * kBlockRows + r].x);
+  if ((int)blockIdx.y == chunks) {
+    const int c4 = threadIdx.x % (D / 4);
+    for (int j = blockIdx.x; j < p.m; j += gridDim.x) {
+      const Group g = group_of(p, j);
+      if (g.nt > 0) continue;
+      const size_t end = (size_t)g.hi * p.Hq;
+      for (size_t o0 = (size_t)g.lo * p.Hq; o0 < end; o0 += kMergeThreads / (D / 4)) {
+        const size_t orow = o0 + threadIdx.x / (D / 4);
+        const float j2 = orow < end && p.o2 ? p.lse2[orow] * 1.4426950408889634f : neg_inf();
+        __syncthreads();  // lse, which may be lse2, is written after every thread has read it
+        if (orow < end) finish_row<D>(p, orow, c4, j2, neg_inf(), 0.0f, make_float4(0.f, 0.f, 0.f, 0.f));
       }
-      for (int c = c0; c <= c1; ++c) {
-        const size_t slot = (size_t)c * 2 + (c == c0 ? first_slot : 0);
-        const float2 ml = p.part_ml[slot * kBlockRows + r];
-        const float4 y = p.part_o[((slot * 2 + (r >> 7)) * (D / 4) + c4) * 128 + (r & 127)];
-        const float f = ml.x != neg_inf() ? ex2_approx(ml.x - M) : 0.0f;
+    }
+    return;
+  }
+  const int wide = kMergeThreads / parts, rows = wide / (D / 4);
+  const int part = threadIdx.x / wide, x = threadIdx.x - part * wide, c4 = x / rows, r = blockIdx.y * rows + x - c4 * rows;
+  const int lo = (int)((long long)ctas * blockIdx.x / gridDim.x), hi = (int)((long long)ctas * (blockIdx.x + 1) / gridDim.x);
+  for (int w0 = lo; w0 < hi; w0 += 32) {
+    const Split mine = w0 + lane_id() < hi ? p.split[w0 + lane_id()] : Split{0, 0, 0, 0};
+    unsigned todo = __ballot_sync(0xffffffffu, (int)blockIdx.y * rows < mine.nrow);
+    while (todo) {  // the same in every warp
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int seq0 = __shfl_sync(0xffffffffu, mine.seq0, src), h = __shfl_sync(0xffffffffu, mine.h, src),
+                nrow = __shfl_sync(0xffffffffu, mine.nrow, src), c1 = __shfl_sync(0xffffffffu, mine.c1, src);
+      const int c0 = w0 + src - 1;
+      const bool on = r < nrow;
+      const size_t orow = on ? (size_t)(seq0 + r / p.G) * p.Hq + h * p.G + r % p.G : 0;
+      const float j2 = on && p.o2 ? p.lse2[orow] * 1.4426950408889634f : neg_inf();
+      float M = neg_inf(), l = 0.0f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](const float2& ml, const float4& y, float m) {
+        const float f = ml.x != neg_inf() ? ex2_approx(ml.x - m) : 0.0f;
         l += f * ml.y;
-        if (f != 0.0f) {
+        if (ml.x != neg_inf()) {
           o.x += f * y.x;
           o.y += f * y.y;
           o.z += f * y.z;
           o.w += f * y.w;
         }
-      }
-      if (j2 != neg_inf()) {
-        const float f = ex2_approx(j2 - M);
-        l += f;
-        if (f != 0.0f) {
-          const uint2 y = *reinterpret_cast<const uint2*>(p.o2 + orow * D + 4 * c4);
-          o.x += f * __uint_as_float(y.x << 16);
-          o.y += f * __uint_as_float(y.x & 0xffff0000u);
-          o.z += f * __uint_as_float(y.y << 16);
-          o.w += f * __uint_as_float(y.y & 0xffff0000u);
+      };
+      for (int c = c0 + part; on && c <= c1; c += kBatch * parts) {
+        float2 ml[kBatch];
+        float4 y[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int cc = c + k * parts;
+          ml[k] = make_float2(neg_inf(), 0.0f);
+          y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (cc <= c1) {
+            const size_t slot = (size_t)cc * 2 + (cc == c0 ? 1 : 0);  // the item begins in c0's share
+            ml[k] = p.part_ml[slot * kBlockRows + r];
+            y[k] = p.part_o[((slot * 2 + (r >> 7)) * (D / 4) + c4) * 128 + (r & 127)];
+          }
+        }
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) m = fmaxf(m, ml[k].x);
+        if (m != neg_inf()) {
+          const float f = M != neg_inf() ? ex2_approx(M - m) : 0.0f;
+          l *= f;
+          o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+          M = m;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) add(ml[k], y[k], m);
         }
       }
-    }
-    __syncthreads();  // lse, which may be lse2, is written after every thread has read it
-    if (on) {
-      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-      *reinterpret_cast<uint2*>(p.O + orow * D + 4 * c4) =
-          make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-      if (c4 == 0) p.lse[orow] = l != 0.0f ? (M + __log2f(l)) * 0.69314718055994531f : neg_inf();
+      ml_s[threadIdx.x] = make_float2(M, l);
+      o_s[threadIdx.x] = o;
+      __syncthreads();  // also: lse, which may be lse2, is written after every thread has read it
+      if (on && part == 0) {
+        if (parts > 1) {
+          for (int k = 1; k < parts; ++k) M = fmaxf(M, ml_s[x + k * wide].x);
+          l = 0.0f;
+          o = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; M != neg_inf() && k < parts; ++k) add(ml_s[x + k * wide], o_s[x + k * wide], M);
+        }
+        finish_row<D>(p, orow, c4, j2, M, l, o);
+      }
+      __syncthreads();
     }
   }
 }
 
+// A bound on the units of a call, and the CTAs of prefix_kernel.
+long long max_units(int n, int m, int P, int H, int G) {
+  return (m + (long long)n * G / kBlockRows) * H * ((P + kKeys - 1ll) / kKeys + kSetup);
+}
 int max_ctas(int n, int m, int P, int H, int G) {
-  const long long units = (m + (long long)n * G / kBlockRows) * H * ((P + kKeys - 1ll) / kKeys);
-  return (int)min((long long)num_sms(), units);
+  return (int)min((long long)num_sms(), max_units(n, m, P, H, G));
 }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
-size_t ml_offset(int m) { return round256((size_t)(m + 1) * 8); }
-size_t o_offset(int m, int ctas) { return ml_offset(m) + (size_t)ctas * 2 * kBlockRows * 8; }
+size_t ml_offset(int ctas) { return round256((size_t)ctas * sizeof(Split)); }
+size_t o_offset(int ctas) { return ml_offset(ctas) + (size_t)ctas * 2 * kBlockRows * 8; }
 
 template <int D>
 kvpop_status launch(PrefixParams& prm, int ctas, cudaStream_t cs) {
@@ -755,8 +819,18 @@ kvpop_status launch(PrefixParams& prm, int ctas, cudaStream_t cs) {
   }
   st = cuda_check(launch_pdl(kern, dim3(ctas), dim3(kThreads), L::total, cs, prm), "kvpop_prefix_attn: launch");
   if (st != KVPOP_OK) return st;
-  return cuda_check(launch_pdl(prefix_merge<D>, dim3((unsigned)((long long)prm.n * prm.H)), dim3(kMergeThreads), 0, cs,
-                               prm, ctas),
+  // A thread of the merge takes about four slots of a row, a CTA at least four rows (two
+  // sectors of a slot's columns).  There are at most `items` items, and at most one a CTA
+  // that several CTAs share.
+  const long long rows_all = (long long)prm.n * prm.G;
+  const int items = prm.H * (prm.m == 1 ? (int)((rows_all + kBlockRows - 1) / kBlockRows)
+                                        : prm.m + (int)(rows_all / kBlockRows));
+  int parts = 1;
+  while (kMergeThreads / (D / 4) / parts > 4 && ctas / items > 4 * parts) parts *= 2;
+  const int rows = kMergeThreads / (D / 4) / parts;
+  const int chunks = ((int)min((long long)kBlockRows, rows_all) + rows - 1) / rows;
+  return cuda_check(launch_pdl(prefix_merge<D>, dim3(min(ctas, items), chunks + 1), dim3(kMergeThreads), 0, cs, prm, ctas,
+                               parts, chunks),
                     "kvpop_prefix_attn: merge launch");
 }
 
@@ -774,8 +848,12 @@ extern "C" kvpop_status kvpop_prefix_attn_workspace_size(int n, int m, int P, in
     set_last_error("kvpop_prefix_attn_workspace_size: D=%d (64 or 128), G=%d (dividing 128) unsupported", D, Hq / H);
     return KVPOP_ERR_UNSUPPORTED;
   }
+  if (max_units(n, m, P, H, Hq / H) > 0x7fffffffll) {
+    set_last_error("kvpop_prefix_attn_workspace_size: more than 2^31 - 1 tiles of rows and keys");
+    return KVPOP_ERR_UNSUPPORTED;
+  }
   const int ctas = max_ctas(n, m, P, H, Hq / H);
-  *bytes = o_offset(m, ctas) + (size_t)ctas * 2 * kBlockRows * D * 4;
+  *bytes = o_offset(ctas) + (size_t)ctas * 2 * kBlockRows * D * 4;
   return KVPOP_OK;
 }
 
@@ -809,8 +887,8 @@ extern "C" kvpop_status kvpop_prefix_attn(const void* q, const void* pk, const v
     set_last_error("kvpop_prefix_attn: q, pk, pv, O, O2 must be 16-byte, workspace 256-byte aligned");
     return KVPOP_ERR_UNSUPPORTED;
   }
-  if (H > 65535 || Hq > 65535 || m > 65535 || n > (1 << 24) || (long long)n * H > 0x7fffffffll) {
-    set_last_error("kvpop_prefix_attn: at most 65535 heads and prefixes, 2^24 sequences and 2^31 - 1 sequence heads");
+  if (H > 65535 || Hq > 65535 || m > 65535 || n > (1 << 24) || (long long)n * Hq > 0x7fffffffll) {
+    set_last_error("kvpop_prefix_attn: at most 65535 heads and prefixes, 2^24 sequences and 2^31 - 1 rows");
     return KVPOP_ERR_UNSUPPORTED;
   }
   const int G = Hq / H;
@@ -833,9 +911,9 @@ extern "C" kvpop_status kvpop_prefix_attn(const void* q, const void* pk, const v
   prm.lse2 = lse2;
   prm.O = (__nv_bfloat16*)O;
   prm.lse = lse;
-  prm.unit0 = reinterpret_cast<long long*>(ws);
-  prm.part_ml = reinterpret_cast<float2*>(ws + ml_offset(m));
-  prm.part_o = reinterpret_cast<float4*>(ws + o_offset(m, ctas));
+  prm.split = reinterpret_cast<Split*>(ws);
+  prm.part_ml = reinterpret_cast<float2*>(ws + ml_offset(ctas));
+  prm.part_o = reinterpret_cast<float4*>(ws + o_offset(ctas));
   prm.status = device_status_ptr();
   prm.n = n;
   prm.m = m;

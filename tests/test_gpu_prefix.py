@@ -161,6 +161,31 @@ def test_in_place_join_and_rows_outside():
     assert torch.isfinite(full[0].float()).all()
 
 
+@pytest.mark.parametrize("G", [1, 64, 128])
+def test_in_place_join_of_split_rows(G):
+    """The same where several CTAs share a row and a row's outputs take several rounds."""
+    q, k, v, j = make([4], 5000, 1, G, 128, seed=G, join=True)
+    ref = kvpop.prefix_attn(q, k, v, None, None, j)
+    check(*ref, q, k, v, [0, 4], [5000], j)
+    O, lse = j[0].clone(), j[1].clone()
+    kvpop.prefix_attn(q, k, v, None, None, (O, lse), out=(O, lse))
+    assert torch.equal(O, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_nan_in_a_query_stays_in_its_row():
+    q, k, v, j = make([6], 2000, 2, 4, 128, seed=11, join=True)
+    clean = kvpop.prefix_attn(q, k, v, None, None, j)
+    q[2, 3, 7] = float("nan")
+    for lens in ([2000], [100]):
+        O, lse = kvpop.prefix_attn(q, k, v, None, i32(lens), j)
+        assert torch.isnan(O[2, 3]).all() and torch.isnan(lse[2, 3])
+        assert int(torch.isnan(O.float()).any(-1).sum()) == 1
+    O, lse = kvpop.prefix_attn(q, k, v, None, None, j)
+    keep = torch.ones(6, 8, dtype=torch.bool, device="cuda")
+    keep[2, 3] = False
+    assert torch.equal(O[keep], clean[0][keep]) and torch.equal(lse[keep], clean[1][keep])
+
+
 def test_out_of_range_groups_and_lengths_are_clamped():
     q, k, v, _ = make([5, 5], 150, 1, 2, 64, seed=5)
     want = kvpop.prefix_attn(q, k, v, i32([0, 5, 10]), i32([150, 0]))
