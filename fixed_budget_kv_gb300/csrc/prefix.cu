@@ -30,8 +30,9 @@
 // core works on one while the other is in its softmax.  A segment of more than
 // 128 rows gives each its own row tile; a smaller one gives both the same rows
 // and every other key tile, and joins the two in the epilogue.  S = Q K^T lands in
-// TMEM (fp32), becomes bf16 P in place, and O += P V reads P from TMEM.  Running
-// maxima are moved lazily, when they grow by more than 2^8.
+// TMEM (fp32), becomes bf16 P in place, and O += P V reads P from TMEM.  A row's
+// reference is the maximum of its first tile; it moves (with O and the sum) only when a
+// tile's weights against it sum to more than 2^20.
 #include <string.h>
 
 #include <atomic>
@@ -45,7 +46,7 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 128;
 constexpr int kBlockRows = 256;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
-constexpr float kRescaleLog2 = 8.0f;
+constexpr float kDirectMax = 1048576.0f;  // 2^20: leaves V all but 2^20 of its range
 constexpr int kMergeThreads = 256;
 // Time between the last tile of a segment and the first of the next, in key tiles.
 constexpr int kSetup = 4;
@@ -76,6 +77,12 @@ struct PrefixParams {
   float scale_log2;
 };
 
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return lo + hi;
+}
+
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
 // Group j: its sequences [lo, hi), keys, key tiles and units (the host bounds the sum
@@ -93,10 +100,10 @@ __device__ __forceinline__ Group group_of(const PrefixParams& p, int j) {
   return g;
 }
 
-__device__ __forceinline__ long long scan_incl(long long x) {
+__device__ __forceinline__ int scan_incl(int x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane_id() >= o) x += y;
   }
   return x;
@@ -359,21 +366,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     } else if (warp == 3) {
       // ------------------------------------------------------------ the CTA's share
       // lane l holds group j0 + l of a window of 32 groups, and its first unit
-      long long all = 0;
-      int j0 = 0, base = 0;
-      Group g = {0, 0, 0, 0, 0};
-      auto window = [&](int w0, long long at) {  // groups w0 .., the first of them at unit `at`; returns the unit after
+      int U = 0, members = 0, j0 = 0, base = 0;
+      Group g;
+      auto window = [&](int w0, int at) {  // groups w0 .., the first of them at unit `at`; returns the unit after
         g = w0 + lane < p.m ? group_of(p, w0 + lane) : Group{0, 0, 0, 0, 0};
-        const long long incl = scan_incl(g.units);
+        const int incl = scan_incl(g.units);
         j0 = w0;
-        base = (int)(at + incl - g.units);
+        base = at + incl - g.units;
         return at + __shfl_sync(0xffffffffu, incl, 31);
       };
-      for (int w0 = 0; w0 < p.m; w0 += 32) all = window(w0, all);
-      // groups that overlap, which the interface rules out, could exceed the host's bound: no work then
-      const int U = all <= 0x7fffffffll ? (int)all : 0;
-      if (blockIdx.x == 0 && lane == 0 && all != U)
-        report_error(p.status, KVPOP_ERR_INVALID_ARG, SITE_PREFIX_PRODUCER, 5);
+#pragma unroll 1
+      for (int w0 = 0; w0 < p.m; w0 += 32) {
+        U = window(w0, U);
+        members = min(members, p.n + 1) + __reduce_add_sync(0xffffffffu, min(g.hi - g.lo, p.n));
+      }
+      if (members > p.n) {
+        // groups that overlap, which the interface rules out, could pass the host's bound on U: no work
+        U = 0;
+        if (blockIdx.x == 0 && lane == 0) report_error(p.status, KVPOP_ERR_INVALID_ARG, SITE_PREFIX_PRODUCER, 5);
+      }
       const int C = min((int)gridDim.x, U);
       const Share sh(U, max(C, 1));
       int u = 0, end = 0;
@@ -382,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         end = sh.first(blockIdx.x + 1);
       }
       if (p.m > 32 && u < end) {  // back to the window in which the share begins
-        long long at = 0;
+        int at = 0;
+#pragma unroll 1
         for (int w0 = 0;; w0 += 32) {
           at = window(w0, at);
           if (u < at) break;
@@ -469,47 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (warp_on) {
           // the whole S row of this thread (128 fp32) in registers; keys past the length -> -inf
           uint32_t sr[4][32];
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) tmem_ld32(tl + s_col + ch * 32, sr[ch]);
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) tmem_wait_ld_dep(sr[ch]);
-          float mt = neg_inf();
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            if (left < ch * 32 + 32) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (ch * 32 + c >= left) sr[ch][c] = 0xff800000u;
-            }
-            mt = fmaxf(mt, max32(sr[ch]));
-          }
-          const float m_new = fmaxf(m_ref, mt);
-          const bool need = (m_new - m_ref) * sl2 > kRescaleLog2;  // true when m_ref == -inf and mt finite
-          float alpha = 1.0f;
-          if (need) {
-            alpha = ex2_approx((m_ref - m_new) * sl2);
-            l *= alpha;
-            m_ref = m_new;
-          }
-          if (__any_sync(0xffffffffu, need) && i > 0) {
-            // O of this stream's last event is complete: S of this one was issued after it
-#pragma unroll
-            for (int cd = 0; cd < D / 32; ++cd) {
-              uint32_t r[32];
-              tmem_ld32(tl + o_col + cd * 32, r);
-              tmem_wait_ld_dep(r);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
-              tmem_st32(tl + o_col + cd * 32, r);
-            }
-            tmem_wait_st();
-          }
-          // P = exp2(s * scale_log2 - m) as bf16, written over S
-          const float nm = (m_ref == neg_inf()) ? 0.0f : -m_ref * sl2;
-          const uint64_t n2 = pack2(nm, nm);
+          tmem_ld32(tl + s_col, sr[0]);
           uint64_t lacc = 0;
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
+          // P = exp2(s * scale_log2 - m) as bf16, written over S
+          auto weights = [&](int ch, uint64_t n2) {
             uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
@@ -521,10 +496,67 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
               pk[c >> 1] = pack_bf16x2(p0, p1);
             }
             tmem_st16(tl + s_col + ch * 16, pk);
+          };
+          auto mask = [&](int ch) {
+            if (left < ch * 32 + 32) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (ch * 32 + c >= left) sr[ch][c] = 0xff800000u;
+            }
+          };
+          // The direct way: weights against the reference that the row has.  It is kept as long
+          // as no weight is near overflow; their precision does not depend on their size.
+          bool direct = i > 0;
+          if (direct) {
+            const float nm = (m_ref == neg_inf()) ? 0.0f : -m_ref * sl2;
+            const uint64_t n2 = pack2(nm, nm);
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              tmem_wait_ld_dep(sr[ch]);
+              if (ch < 3) tmem_ld32(tl + s_col + (ch + 1) * 32, sr[ch + 1]);
+              mask(ch);
+              weights(ch, n2);
+            }
+            const float sum = sum2(lacc);
+            direct = __all_sync(0xffffffffu, !row_on || (m_ref != neg_inf() && sum < kDirectMax));
+            if (direct) l += sum;
+          } else {
+#pragma unroll
+            for (int ch = 1; ch < 4; ++ch) tmem_ld32(tl + s_col + ch * 32, sr[ch]);
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              tmem_wait_ld_dep(sr[ch]);
+              mask(ch);
+            }
           }
-          float l0, l1;
-          unpack2(lacc, l0, l1);
-          l += l0 + l1;
+          if (!direct) {
+            float mt = neg_inf();
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) mt = fmaxf(mt, max32(sr[ch]));
+            const float m_new = fmaxf(m_ref, mt);
+            if (i > 0) {
+              // O of this stream's last event is complete: S of this one was issued after it
+              const float alpha = m_new > m_ref ? ex2_approx((m_ref - m_new) * sl2) : 1.0f;
+              l *= alpha;
+#pragma unroll
+              for (int cd = 0; cd < D / 32; ++cd) {
+                uint32_t r[32];
+                tmem_ld32(tl + o_col + cd * 32, r);
+                tmem_wait_ld_dep(r);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
+                tmem_st32(tl + o_col + cd * 32, r);
+              }
+            }
+            m_ref = m_new;
+            const float nm = (m_ref == neg_inf()) ? 0.0f : -m_ref * sl2;
+            const uint64_t n2 = pack2(nm, nm);
+            lacc = 0;
+            tmem_wait_st();  // the weights of the direct way, which these replace
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) weights(ch, n2);
+            l += sum2(lacc);
+          }
           tmem_wait_st();
         }
         if (left < kKeys && s.len < p.P) {

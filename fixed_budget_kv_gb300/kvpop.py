@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 
@@ -164,7 +165,7 @@ _here = contextlib.nullcontext()
 
 
 def _empty_as(t):
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _on(stream):
@@ -422,6 +423,7 @@ def qk_norm_rope(q, k, wq, wk, eps: float, inv_freq, pos=None, interleaved: bool
     return qo, ko
 
 
+@functools.lru_cache(maxsize=None)
 def qk_norm_rope_bwd_workspace_size(D: int) -> int:
     n = c_size()
     _check(load().kvpop_qk_norm_rope_bwd_workspace_size(D, ctypes.byref(n)), "qk_norm_rope_bwd_workspace_size")
@@ -465,6 +467,12 @@ def qk_norm_rope_bwd(q, k, dq, dk, wq, wk, eps: float, inv_freq, pos=None, inter
 # ----------------------------------------------------------------------------
 
 def prefix_attn_workspace_size(n, m, P, Hq, H, D) -> int:
+    return _prefix_workspace(torch.cuda.current_device() if torch.cuda.is_available() else -1, n, m, P, Hq, H, D)
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_workspace(dev, n, m, P, Hq, H, D) -> int:
+    """Bytes on device dev: a function of the sizes and of the device's number of SMs."""
     nb = c_size()
     _check(load().kvpop_prefix_attn_workspace_size(n, m, P, Hq, H, D, ctypes.byref(nb)), "prefix_attn_workspace_size")
     return nb.value
@@ -501,7 +509,7 @@ def prefix_attn(q, pk, pv, cu=None, lens=None, join=None, scale: float = 0.0, wo
             _fit(O, torch.bfloat16, dev, rows, "O")
             _fit(lse, torch.float32, dev, (n, Hq), "lse")
         if workspace is None:
-            workspace = torch.empty(prefix_attn_workspace_size(n, m, P, Hq, H, D), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(_prefix_workspace(dev, n, m, P, Hq, H, D), dtype=torch.uint8, device=q.device)
         else:
             _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
     _check(load().kvpop_prefix_attn(_p(q), _p(pk), _p(pv), n, m, P, Hq, H, D, scale, _p(cu), _p(lens), _p(O2),
