@@ -21,9 +21,9 @@
 // the same call gives the same bits.
 //
 // Warp roles of prefix_kernel (384 threads):
-//   warp 0      TMA producer: one ring of K and V tiles in the order of their use
+//   warp 0      TMA producer of the query tiles and the ring of K tiles
 //   warp 1      TMEM allocation and the single-thread tcgen05.mma issuer
-//   warp 2      query tiles of each segment
+//   warp 2      TMA producer of the ring of V tiles
 //   warp 3      the CTA's share of the units, handed to the others segment by segment
 //   warps 4-7, 8-11  softmax, one thread a row (TMEM lane)
 // The two softmax warpgroups are two streams that alternate, so that the tensor
@@ -132,15 +132,23 @@ struct __align__(16) Seg {
   __device__ __forceinline__ int slot() const { return flags >> 2; }
 };
 
-// Place of a key tile's K and V among the segment's 2 NT loads: the order in which
-// the MMA warp uses them (S runs two events ahead of P V).
-__device__ __forceinline__ int pos_k(bool two, int t) { return two ? 2 * t : (t < 2 ? t : 2 * t - 1); }
-__device__ __forceinline__ int pos_v(bool two, int NT, int t) { return two ? 2 * t + 1 : min(NT, t + 2) + t; }
+// A place in a ring of N stages and the parity of its use.
+template <int N>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
 
-template <int NS>
+template <int NK, int NV>
 struct Bars {
   uint64_t q_full, q_empty;
-  uint64_t kv_full[NS], kv_empty[NS];
+  uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV];
   uint64_t s_full[2], p_full[2];
   uint64_t o_full, o_empty;
   uint64_t ml_full;
@@ -151,12 +159,13 @@ struct Bars {
 template <int D>
 struct Layout {
   static constexpr int DH = D / 64;
-  static constexpr int NS = D == 128 ? 5 : 10;  // 32 KB or 16 KB tiles
+  static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? 2 : 5;  // 32 KB or 16 KB tiles
   static constexpr int kTile = DH * kBlockBytes;
   static constexpr int q_off = 0;
-  static constexpr int kv_off = q_off + 2 * kTile;
-  static constexpr int bar_off = kv_off + NS * kTile;
-  static constexpr int seg_off = bar_off + ((int)sizeof(Bars<NS>) + 15) / 16 * 16;
+  static constexpr int k_off = q_off + 2 * kTile;
+  static constexpr int v_off = k_off + NK * kTile;
+  static constexpr int bar_off = v_off + NV * kTile;
+  static constexpr int seg_off = bar_off + ((int)sizeof(Bars<NK, NV>) + 15) / 16 * 16;
   static constexpr int ml_off = seg_off + kSegs * (int)sizeof(Seg);  // [stream][row] (maximum, sum)
   static constexpr int misc_off = ml_off + 2 * 128 * 8;
   static constexpr int total = misc_off + 16;
@@ -166,13 +175,13 @@ struct Layout {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
   using L = Layout<D>;
-  constexpr int DH = L::DH, NS = L::NS;
+  constexpr int DH = L::DH, NK = L::NK, NV = L::NV;
   extern __shared__ __align__(1024) uint8_t smem[];  // no slack left to align by hand: checked
   if (smem_u32(smem) & 1023) {
     if (threadIdx.x == 0) report_error(p.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 50);
     return;
   }
-  Bars<NS>* bars = reinterpret_cast<Bars<NS>*>(smem + L::bar_off);
+  Bars<NK, NV>* bars = reinterpret_cast<Bars<NK, NV>*>(smem + L::bar_off);
   Seg* segs = reinterpret_cast<Seg*>(smem + L::seg_off);
   float2* ml_s = reinterpret_cast<float2*>(smem + L::ml_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::misc_off);
@@ -183,9 +192,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&bars->kv_full[i], 1);
-      mbar_init(&bars->kv_empty[i], 1);
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&bars->v_full[i], 1);
+      mbar_init(&bars->v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
@@ -196,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     mbar_init(&bars->ml_full, 8);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bars->seg_full[i], 1);
-      mbar_init(&bars->seg_empty[i], 11);  // producer, query tiles, MMA, 8 softmax warps
+      mbar_init(&bars->seg_empty[i], 11);  // two producers, MMA, 8 softmax warps
     }
     mbar_init(&bars->drain, 1);
     *abort_flag = 0;
@@ -233,135 +246,151 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (warp < 4) {
     setmaxnreg_dec<kRegsIo>();
     if (warp == 0 && lane == 0) {
-      // ------------------------------------------------------------ K / V producer
+      // ------------------------------------------------------------ query and K producer
       tma_prefetch_desc(&p.tk);
-      tma_prefetch_desc(&p.tv);
+      tma_prefetch_desc(&p.tq);
       Seg s;
-      int seq = 0;
+      Ring<NK> k;
       bool ok = true;
-      auto load = [&](const CUtensorMap* map, int t) {
-        const int st = seq % NS;
-        if (!mbar_wait(&bars->kv_empty[st], ((seq / NS) & 1) ^ 1, abort_flag)) {
-          fail(SITE_PREFIX_PRODUCER, 1);
-          ok = false;
-          return;
-        }
-        mbar_arrive_expect_tx(&bars->kv_full[st], L::kTile);
-        for (int dh = 0; dh < DH; ++dh)
-          tma_load_4d(smem + L::kv_off + st * L::kTile + dh * kBlockBytes, map, &bars->kv_full[st], dh * 64, s.h,
-                      (s.kt0 + t) * kKeys, s.j);
-        ++seq;
-      };
       for (int n = 0; ok && get_seg(n, s); ++n) {
-        const int ahead = s.two() ? 1 : 2;  // K tiles before the first V
-        for (int t = 0; ok && t < min(ahead, s.NT); ++t) load(&p.tk, t);
-        for (int t = 0; ok && t < s.NT; ++t) {
-          load(&p.tv, t);
-          if (ok && t + ahead < s.NT) load(&p.tk, t + ahead);
+        for (int t = 0; t < s.NT; ++t) {
+          if (!mbar_wait(&bars->k_empty[k.st], k.ph ^ 1, abort_flag)) {
+            fail(SITE_PREFIX_PRODUCER, 1);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&bars->k_full[k.st], L::kTile);
+          for (int dh = 0; dh < DH; ++dh)
+            tma_load_4d(smem + L::k_off + k.st * L::kTile + dh * kBlockBytes, &p.tk, &bars->k_full[k.st], dh * 64, s.h,
+                        (s.kt0 + t) * kKeys, s.j);
+          k.next();
+          if (t == 0) {
+            if (!mbar_wait(&bars->q_empty, (n & 1) ^ 1, abort_flag)) {
+              fail(SITE_PREFIX_PRODUCER, 2);
+              ok = false;
+              break;
+            }
+            const int tiles = s.two() ? 2 : 1;
+            mbar_arrive_expect_tx(&bars->q_full, tiles * L::kTile);
+            for (int i = 0; i < tiles; ++i)
+              for (int dh = 0; dh < DH; ++dh)
+                tma_load_4d(smem + L::q_off + i * L::kTile + dh * kBlockBytes, &p.tq, &bars->q_full, dh * 64, s.h * p.G,
+                            s.seq0 + i * (p.seqs / 2), 0);
+          }
         }
       }
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------------ MMA issuer
-      // Event e of a segment is stream w = (e & 1) ^ par and key tile e (or e / 2 with two
-      // row tiles).  S runs two events ahead of P V, into the next segment, so S of a
-      // stream always follows P V of the stream's event before.
-      // TMEM: S / P of stream w at column 128 w, O at 256 + 128 w.
+      // A segment's events alternate between the streams: event e takes key tile e, or with
+      // two row tiles row tile e & 1 and key tile e / 2.  S runs two events ahead of P V, into
+      // the next segment, so S of a stream always follows P V of the stream's event before.
+      // TMEM: S / P of stream w at column 128 w, O at 256 + 128 w.  The issuing thread is a
+      // third of its scheduler's warps and its bookkeeping is in the way of every MMA: places
+      // in the rings are counted on, operands stepped from descriptor low words.
       constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0);
       constexpr uint32_t idesc_pv = idesc_bf16(128, D, 1);
-      const uint32_t q_addr = sbase + L::q_off, kv_addr = sbase + L::kv_off;
-      struct Ev {
-        int NT, flags;  // of its segment; NT = 0 at the end
-        int e, n, sb;   // event, segment number, loads before the segment
-        uint32_t par;
-      };
-      Ev a = {0, 0, 0, 0, 0, 0}, b = a;  // next S, next P V
-      auto fetch = [&](Ev& x, bool last_reader) {
-        x.NT = 0;
-        if (!mbar_wait(&bars->seg_full[x.n % kSegs], (x.n / kSegs) & 1, abort_flag)) {
-          fail(SITE_PREFIX_MMA, 6);
-          return;
-        }
-        x.NT = segs[x.n % kSegs].NT;
-        x.flags = segs[x.n % kSegs].flags;
-        if (last_reader) mbar_arrive(&bars->seg_empty[x.n % kSegs]);
-      };
-      auto step = [&](Ev& x, bool last_reader) {
-        const int events = (x.flags & 1) ? 2 * x.NT : x.NT;
-        if (++x.e < events) return;
-        x.par ^= events & 1;
-        x.sb += 2 * x.NT;
-        ++x.n;
-        x.e = 0;
-        fetch(x, last_reader);
-      };
-      fetch(a, false);
-      fetch(b, true);
-      uint32_t np = 0;  // bit w: parity of stream w's next P
+      const uint32_t q_lo = desc_lo(sbase + L::q_off, 16), k_lo = desc_lo(sbase + L::k_off, 16),
+                     v_lo = desc_lo(sbase + L::v_off, DH > 1 ? kBlockBytes : 16);
+      Ring<NK> k;
+      Ring<NV> v;
+      int an = 0, a_left = 0, bn = 0, b_left = 0;  // segment and events left of it, for S and for P V
+      bool a_two = false, b_two = false;
+      uint32_t a_sub = 0, b_sub = 0, aw = 0, bw = 0;  // row tile; stream
+      uint32_t a_new = 1, b_new = 2;                  // first event of a segment; first event of each stream in it
+      uint32_t np = 0;                                // bit w: parity of stream w's next P
       bool ok = true;
       auto wait_bar = [&](uint64_t* bar, uint32_t ph, int detail) -> bool {
         if (!mbar_wait(bar, ph, abort_flag)) {
           fail(SITE_PREFIX_MMA, detail);
+          ok = false;
           return false;
         }
-        tc_fence_after();
         return true;
       };
+      // events and mode of segment n; no events at the end of the work
+      auto fetch = [&](int n, int& left, bool& two, bool last_reader) {
+        left = 0;
+        if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, 6)) return;
+        const int NT = segs[n % kSegs].NT;
+        two = segs[n % kSegs].two();
+        left = two ? 2 * NT : NT;
+        if (last_reader) mbar_arrive(&bars->seg_empty[n % kSegs]);
+      };
       auto issue_s = [&]() {
-        const bool two = a.flags & 1;
-        const int w = (a.e & 1) ^ a.par, t = two ? a.e >> 1 : a.e, qt = two ? a.e & 1 : 0;
-        const int seq = a.sb + pos_k(two, t), st = seq % NS;
-        if (a.e == 0 && !(ok = wait_bar(&bars->q_full, a.n & 1, 1))) return;
-        if (!(ok = wait_bar(&bars->kv_full[st], (seq / NS) & 1, 2))) return;
-        const uint32_t qlo = desc_lo(q_addr + qt * L::kTile, 16), klo = desc_lo(kv_addr + st * L::kTile, 16);
+        if (a_new) {
+          if (!wait_bar(&bars->q_full, an & 1, 1)) return;
+          a_new = 0;
+        }
+        if (!a_sub && !wait_bar(&bars->k_full[k.st], k.ph, 2)) return;
+        tc_fence_after();
+        const uint32_t d = tbase + 128 * aw, a0 = q_lo + a_sub * (L::kTile / 16), b0 = k_lo + k.st * (L::kTile / 16);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const int dh = ks >> 2;
-          const uint32_t w32 = (uint32_t)(ks & 3) * 32;
-          mma_ss_lo(tbase + 128 * w, qlo + (dh * kBlockBytes + w32) / 16, klo + (dh * kBlockBytes + w32) / 16, idesc_qk,
-                 ks > 0 ? 1u : 0u);
+          const uint32_t off = ((ks >> 2) * kBlockBytes + (ks & 3) * 32) / 16;
+          mma_ss_lo(d, a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
         }
-        mma_commit(&bars->s_full[w]);
-        if (!two || (a.e & 1)) mma_commit(&bars->kv_empty[st]);
-        if (a.e == (two ? 2 * a.NT : a.NT) - 1) mma_commit(&bars->q_empty);
-        step(a, false);
+        mma_commit(&bars->s_full[aw]);
+        if (!a_two || a_sub) {
+          mma_commit(&bars->k_empty[k.st]);
+          k.next();
+        }
+        if (a_two) a_sub ^= 1;
+        aw ^= 1;
+        if (--a_left == 0) {
+          mma_commit(&bars->q_empty);
+          a_new = 1;
+          fetch(++an, a_left, a_two, false);
+        }
       };
-      for (int i = 0; i < 2 && ok && a.NT; ++i) issue_s();
-      while (ok && b.NT) {
-        const bool two = b.flags & 1;
-        const int w = (b.e & 1) ^ b.par, t = two ? b.e >> 1 : b.e;
-        const int seq = b.sb + pos_v(two, b.NT, t), st = seq % NS;
-        if (!(ok = wait_bar(&bars->p_full[w], (np >> w) & 1, 3))) break;
-        np ^= 1u << w;
-        if (!(ok = wait_bar(&bars->kv_full[st], (seq / NS) & 1, 4))) break;
-        if (b.e == 0 && !(ok = wait_bar(&bars->o_empty, (b.n & 1) ^ 1, 5))) break;
-        const uint32_t vlo = desc_lo(kv_addr + st * L::kTile, DH > 1 ? kBlockBytes : 16);
+      fetch(0, a_left, a_two, false);
+      fetch(0, b_left, b_two, true);
+      for (int i = 0; i < 2 && ok && a_left; ++i) issue_s();
+      while (ok && b_left) {
+        if (!wait_bar(&bars->p_full[bw], (np >> bw) & 1, 3)) break;
+        np ^= 1u << bw;
+        if (!b_sub && !wait_bar(&bars->v_full[v.st], v.ph, 4)) break;
+        if (b_new == 2 && !wait_bar(&bars->o_empty, (bn & 1) ^ 1, 5)) break;
+        tc_fence_after();
+        const uint32_t d = tbase + 256 + 128 * bw, a0 = tbase + 128 * bw, b0 = v_lo + v.st * (L::kTile / 16);
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_ts_lo(tbase + 256 + 128 * w, tbase + 128 * w + ks * 8, vlo + ks * (2048 / 16), idesc_pv,
-                    (b.e > 1 || ks > 0) ? 1u : 0u);
-        if (!two || (b.e & 1)) mma_commit(&bars->kv_empty[st]);
-        if (b.e == (two ? 2 * b.NT : b.NT) - 1) mma_commit(&bars->o_full);
-        step(b, true);
-        if (a.NT) issue_s();
+          mma_ts_lo(d, a0 + ks * 8, b0 + ks * (2048 / 16), idesc_pv, (b_new == 0 || ks > 0) ? 1u : 0u);
+        if (!b_two || b_sub) {
+          mma_commit(&bars->v_empty[v.st]);
+          v.next();
+        }
+        if (b_new) --b_new;
+        if (b_two) b_sub ^= 1;
+        bw ^= 1;
+        if (--b_left == 0) {
+          mma_commit(&bars->o_full);
+          b_new = 2;
+          fetch(++bn, b_left, b_two, true);
+        }
+        if (a_left && ok) issue_s();
       }
       // drain every issued MMA before teardown
       mma_commit(&bars->drain);
       mbar_wait(&bars->drain, 0, nullptr);
     } else if (warp == 2 && lane == 0) {
-      // ------------------------------------------------------------ query tiles
-      tma_prefetch_desc(&p.tq);
+      // ------------------------------------------------------------ V producer
+      tma_prefetch_desc(&p.tv);
       Seg s;
-      for (int n = 0; get_seg(n, s); ++n) {
-        if (!mbar_wait(&bars->q_empty, (n & 1) ^ 1, abort_flag)) {
-          fail(SITE_PREFIX_PRODUCER, 2);
-          break;
-        }
-        const int tiles = s.two() ? 2 : 1;
-        mbar_arrive_expect_tx(&bars->q_full, tiles * L::kTile);
-        for (int i = 0; i < tiles; ++i)
+      Ring<NV> v;
+      bool ok = true;
+      for (int n = 0; ok && get_seg(n, s); ++n) {
+        for (int t = 0; t < s.NT; ++t) {
+          if (!mbar_wait(&bars->v_empty[v.st], v.ph ^ 1, abort_flag)) {
+            fail(SITE_PREFIX_PRODUCER, 6);
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&bars->v_full[v.st], L::kTile);
           for (int dh = 0; dh < DH; ++dh)
-            tma_load_4d(smem + L::q_off + i * L::kTile + dh * kBlockBytes, &p.tq, &bars->q_full, dh * 64, s.h * p.G,
-                        s.seq0 + i * (p.seqs / 2), 0);
+            tma_load_4d(smem + L::v_off + v.st * L::kTile + dh * kBlockBytes, &p.tv, &bars->v_full[v.st], dh * 64, s.h,
+                        (s.kt0 + t) * kKeys, s.j);
+          v.next();
+        }
       }
     } else if (warp == 3) {
       // ------------------------------------------------------------ the CTA's share
@@ -561,8 +590,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         }
         if (left < kKeys && s.len < p.P) {
           // V rows past the length hold anything, and 0 * NaN would be NaN: zero them
-          const int seq = sb + pos_v(two, s.NT, t), st = seq % NS;
-          if (!warp_wait(&bars->kv_full[st], (seq / NS) & 1, abort_flag)) {
+          const int seq = sb + t, st = seq % NV;
+          if (!warp_wait(&bars->v_full[st], (seq / NV) & 1, abort_flag)) {
             if (lane == 0) fail(SITE_PREFIX_SOFTMAX, 2);
             ok = false;
             break;
@@ -570,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           if (row >= left) {
 #pragma unroll
             for (int dh = 0; dh < DH; ++dh) {
-              uint4* r = reinterpret_cast<uint4*>(smem + L::kv_off + st * L::kTile + dh * kBlockBytes + row * 128);
+              uint4* r = reinterpret_cast<uint4*>(smem + L::v_off + st * L::kTile + dh * kBlockBytes + row * 128);
 #pragma unroll
               for (int u = 0; u < 8; ++u) r[u] = make_uint4(0, 0, 0, 0);
             }
@@ -679,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       }
       tc_fence_before();
       par ^= (two ? 2 * s.NT : s.NT) & 1;
-      sb += 2 * s.NT;
+      sb += s.NT;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bars->o_empty);
