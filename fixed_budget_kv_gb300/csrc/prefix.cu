@@ -22,7 +22,7 @@
 //
 // Warp roles of prefix_kernel (384 threads):
 //   warp 0      TMA producer of the query tiles and the ring of K tiles
-//   warp 1      TMEM allocation and the single-thread tcgen05.mma issuer
+//   warp 1      TMEM allocation; issues tcgen05.mma
 //   warp 2      TMA producer of the ring of V tiles
 //   warp 3      the CTA's share of the units, handed to the others segment by segment
 //   warps 4-7, 8-11  softmax, one thread a row (TMEM lane)
@@ -132,6 +132,38 @@ struct __align__(16) Seg {
   __device__ __forceinline__ int slot() const { return flags >> 2; }
 };
 
+// The MMA wrappers for a whole warp: one elected lane issues.
+__device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 // A place in a ring of N stages and the parity of its use.
 template <int N>
 struct Ring {
@@ -178,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   constexpr int DH = L::DH, NK = L::NK, NV = L::NV;
   extern __shared__ __align__(1024) uint8_t smem[];  // no slack left to align by hand: checked
   if (smem_u32(smem) & 1023) {
+    grid_dep_wait();
     if (threadIdx.x == 0) report_error(p.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 50);
     return;
   }
@@ -279,14 +312,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           }
         }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
       // A segment's events alternate between the streams: event e takes key tile e, or with
       // two row tiles row tile e & 1 and key tile e / 2.  S runs two events ahead of P V, into
       // the next segment, so S of a stream always follows P V of the stream's event before.
-      // TMEM: S / P of stream w at column 128 w, O at 256 + 128 w.  The issuing thread is a
-      // third of its scheduler's warps and its bookkeeping is in the way of every MMA: places
-      // in the rings are counted on, operands stepped from descriptor low words.
+      // TMEM: S / P of stream w at column 128 w, O at 256 + 128 w.
+      // The bookkeeping is in the way of every MMA.  The whole warp runs it, in step, and one
+      // elected lane issues: the operands then live in uniform registers (256 x 8k keys: 77 us
+      // against 84 with a single thread here).  Places in the rings are counted on.
       constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0);
       constexpr uint32_t idesc_pv = idesc_bf16(128, D, 1);
       const uint32_t q_lo = desc_lo(sbase + L::q_off, 16), k_lo = desc_lo(sbase + L::k_off, 16),
@@ -300,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       uint32_t np = 0;                                // bit w: parity of stream w's next P
       bool ok = true;
       auto wait_bar = [&](uint64_t* bar, uint32_t ph, int detail) -> bool {
-        if (!mbar_wait(bar, ph, abort_flag)) {
-          fail(SITE_PREFIX_MMA, detail);
+        if (!warp_wait(bar, ph, abort_flag)) {
+          if (lane == 0) fail(SITE_PREFIX_MMA, detail);
           ok = false;
           return false;
         }
@@ -311,10 +345,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       auto fetch = [&](int n, int& left, bool& two, bool last_reader) {
         left = 0;
         if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, 6)) return;
-        const int NT = segs[n % kSegs].NT;
-        two = segs[n % kSegs].two();
+        // warp reductions of equal values: the results are known to be uniform
+        const int NT = __reduce_max_sync(0xffffffffu, segs[n % kSegs].NT);
+        two = __reduce_max_sync(0xffffffffu, segs[n % kSegs].flags) & 1;
         left = two ? 2 * NT : NT;
-        if (last_reader) mbar_arrive(&bars->seg_empty[n % kSegs]);
+        if (last_reader && lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
       };
       auto issue_s = [&]() {
         if (a_new) {
@@ -327,17 +362,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t off = ((ks >> 2) * kBlockBytes + (ks & 3) * 32) / 16;
-          mma_ss_lo(d, a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
+          mma_ss_elect(d, a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
         }
-        mma_commit(&bars->s_full[aw]);
+        mma_commit_elect(&bars->s_full[aw]);
         if (!a_two || a_sub) {
-          mma_commit(&bars->k_empty[k.st]);
+          mma_commit_elect(&bars->k_empty[k.st]);
           k.next();
         }
         if (a_two) a_sub ^= 1;
         aw ^= 1;
         if (--a_left == 0) {
-          mma_commit(&bars->q_empty);
+          mma_commit_elect(&bars->q_empty);
           a_new = 1;
           fetch(++an, a_left, a_two, false);
         }
@@ -354,24 +389,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const uint32_t d = tbase + 256 + 128 * bw, a0 = tbase + 128 * bw, b0 = v_lo + v.st * (L::kTile / 16);
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_ts_lo(d, a0 + ks * 8, b0 + ks * (2048 / 16), idesc_pv, (b_new == 0 || ks > 0) ? 1u : 0u);
+          mma_ts_elect(d, a0 + ks * 8, b0 + ks * (2048 / 16), idesc_pv, (b_new == 0 || ks > 0) ? 1u : 0u);
         if (!b_two || b_sub) {
-          mma_commit(&bars->v_empty[v.st]);
+          mma_commit_elect(&bars->v_empty[v.st]);
           v.next();
         }
         if (b_new) --b_new;
         if (b_two) b_sub ^= 1;
         bw ^= 1;
         if (--b_left == 0) {
-          mma_commit(&bars->o_full);
+          mma_commit_elect(&bars->o_full);
           b_new = 2;
           fetch(++bn, b_left, b_two, true);
         }
         if (a_left && ok) issue_s();
       }
       // drain every issued MMA before teardown
-      mma_commit(&bars->drain);
-      mbar_wait(&bars->drain, 0, nullptr);
+      mma_commit_elect(&bars->drain);
+      warp_wait(&bars->drain, 0, nullptr);
     } else if (warp == 2 && lane == 0) {
       // ------------------------------------------------------------ V producer
       tma_prefetch_desc(&p.tv);

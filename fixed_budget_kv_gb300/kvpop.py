@@ -483,7 +483,8 @@ def prefix_attn(q, pk, pv, cu=None, lens=None, join=None, scale: float = 0.0, wo
     sequences share: group j is the sequences cu[j]..cu[j+1]-1 (int32 [m+1]; None with
     one prefix) and sees the first lens[j] keys (int32 [m]; None: all P).  `join` =
     (O2 [n,Hq,D] bf16, lse2 [n,Hq] fp32), the rows' attention over other keys such as
-    Cache.step's, makes the result the attention over both.  Returns (O, lse)."""
+    Cache.step's, makes the result the attention over both.  Returns (O, lse), [n,Hq,D]
+    bf16 and [n,Hq] fp32; rows outside the groups are not written."""
     if q.dim() != 3 or pk.dim() != 4:
         raise ValueError("q must be [n, Hq, D] and pk [m, P, H, D]")
     n, Hq, D = rows = q.shape

@@ -268,7 +268,8 @@ kvpop_status kvpop_boundary_loss(const float* r_hat, const int32_t* t_bnd, const
  *            q_stride elements apart (Hq * D, or the packed projection's width);
  *            likewise k [b, S, H, D] with k_stride
  *   wq, wk   [D] fp32, nullable (all 1)
- *   inv_freq [R/2] fp32; angles are taken from its exact values at any int32 position
+ *   inv_freq [R/2] fp32, finite; angles are taken from its exact values at any int32
+ *            position
  *   pos      [b, S] int32, nullable: the position of token s is s
  *   q_out    [b, S, Hq, D], k_out [b, S, H, D] bf16, contiguous.  q_out may be q
  *            (and k_out k) when the strides are equal too; no other overlap.
@@ -370,7 +371,10 @@ kvpop_status kvpop_cache_position(const kvpop_cache* cache, int32_t* q_next);
  *   pk, pv [m, P, H, D] bf16 (the K and V of a prompt batch as kvpop_attn_fwd
  *          takes them); keys at or past lens[j] are never used, whatever they hold
  *   cu     [m + 1] int32 device, non-decreasing in [0, n]; NULL with m = 1: all n.
- *          Rows of O and lse outside cu[0] .. cu[m]-1 are left as they were.
+ *          Rows of O and lse outside cu[0] .. cu[m]-1 are left as they were.  (A
+ *          sequence without a prefix can be in a group of length 0.)  Groups that
+ *          overlap to more than n sequences in all record KVPOP_ERR_INVALID_ARG in
+ *          the device status words, and nothing is computed.
  *   lens   [m] int32 device in [0, P]; NULL: all P.  A row without any key (and
  *          with lse2 = -inf, if given) gets O = 0 and lse = -inf.
  *          Out-of-range values of cu and lens are clamped.

@@ -88,6 +88,30 @@ def test_prefix_attention(case):
     check(O, lse, q, k, v, cu, lens, j)
 
 
+def test_many_groups():
+    """More groups than a warp takes at a time, whole windows of them without work, and
+    a share that begins in a later window."""
+    groups, lens = [], []
+    for j in range(300):
+        groups.append([0, 1, 2, 5][j % 4] if not 64 <= j < 140 else (3 if j % 2 else 0))
+        lens.append((j * 37) % 400 if not 64 <= j < 140 else (0 if j % 2 else 200))
+    q, k, v, j2 = make(groups, 400, 1, 4, 64, seed=12, join=True)
+    cu = [0] + np.cumsum(groups).tolist()
+    O, lse = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), j2)
+    check(O, lse, q, k, v, cu, lens, j2)
+
+
+def test_overlapping_groups_are_reported():
+    """Groups that cover more than n sequences: the status says so and nothing is written."""
+    q, k, v, _ = make([5, 5], 150, 1, 2, 64, seed=13)
+    k3, v3 = torch.cat([k, k[:1]]), torch.cat([v, v[:1]])
+    O, lse = torch.full_like(q, 3.0), torch.full((10, 2), 3.0, device="cuda")
+    kvpop.prefix_attn(q, k3, v3, i32([0, 8, 2, 10]), i32([150, 150, 150]), out=(O, lse))
+    st, words = kvpop.device_status(reset=True)
+    assert st == 1, words
+    assert (O == 3.0).all() and (lse == 3.0).all()
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_defaults_and_scale(D):
     """One prefix without cu and lens; a scale of the caller's; peaked and flat rows."""
@@ -159,6 +183,18 @@ def test_in_place_join_and_rows_outside():
     kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), None, out=tuple(full))
     assert all((t[:3] == 5).all() and (t[9:] == 5).all() for t in full)
     assert torch.isfinite(full[0].float()).all()
+
+
+def test_moving_reference():
+    """Scores whose maximum rises by far more than 2^20 between the tiles of a row, in both
+    streams and for one row among many; and values large enough that a weight of 2^20 counts."""
+    q, k, v, _ = make([40], 1100, 1, 4, 128, seed=14)
+    k *= 0.02
+    for t, f in ((140, 3.0), (300, 6.0), (650, 9.0), (900, 12.0)):
+        k[0, t, 0] = (q[7, 1].float() * f / 12.0).bfloat16()
+    v *= 1e30
+    O, lse = kvpop.prefix_attn(q, k, v, scale=0.5)
+    check(O, lse, q, k, v, [0, 40], [1100], scale=0.5)
 
 
 @pytest.mark.parametrize("G", [1, 64, 128])
