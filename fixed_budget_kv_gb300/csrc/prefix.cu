@@ -21,9 +21,9 @@
 // the same call gives the same bits.
 //
 // Warp roles of prefix_kernel (384 threads):
-//   warp 0      TMA producer of the query tiles and the ring of K tiles
+//   warp 0      TMA producer: one ring of K and V tiles in the order of their use
 //   warp 1      TMEM allocation; issues tcgen05.mma
-//   warp 2      TMA producer of the ring of V tiles
+//   warp 2      query tiles of each segment
 //   warp 3      the CTA's share of the units, handed to the others segment by segment
 //   warps 4-7, 8-11  softmax, one thread a row (TMEM lane)
 // The two softmax warpgroups are two streams that alternate, so that the tensor
@@ -164,23 +164,32 @@ __device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
       : "memory");
 }
 
+// Place of a key tile's K and V among the segment's 2 NT loads: the order in which
+// the MMA warp uses them (S runs two events ahead of P V).
+__device__ __forceinline__ int pos_v(bool two, int NT, int t) { return two ? 2 * t + 1 : min(NT, t + 2) + t; }
+
 // A place in a ring of N stages and the parity of its use.
 template <int N>
 struct Ring {
   int st = 0;
   uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++st == N) {
-      st = 0;
+  __device__ __forceinline__ void skip(int d) {  // d < N
+    st += d;
+    if (st >= N) {
+      st -= N;
       ph ^= 1;
     }
   }
+  __device__ __forceinline__ void jump(int d) {
+    ph ^= d / N & 1;
+    skip(d % N);
+  }
 };
 
-template <int NK, int NV>
+template <int NS>
 struct Bars {
   uint64_t q_full, q_empty;
-  uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV];
+  uint64_t kv_full[NS], kv_empty[NS];
   uint64_t s_full[2], p_full[2];
   uint64_t o_full, o_empty;
   uint64_t ml_full;
@@ -191,13 +200,12 @@ struct Bars {
 template <int D>
 struct Layout {
   static constexpr int DH = D / 64;
-  static constexpr int NK = D == 128 ? 3 : 5, NV = D == 128 ? 2 : 5;  // 32 KB or 16 KB tiles
+  static constexpr int NS = D == 128 ? 5 : 10;  // 32 KB or 16 KB tiles
   static constexpr int kTile = DH * kBlockBytes;
   static constexpr int q_off = 0;
-  static constexpr int k_off = q_off + 2 * kTile;
-  static constexpr int v_off = k_off + NK * kTile;
-  static constexpr int bar_off = v_off + NV * kTile;
-  static constexpr int seg_off = bar_off + ((int)sizeof(Bars<NK, NV>) + 15) / 16 * 16;
+  static constexpr int kv_off = q_off + 2 * kTile;
+  static constexpr int bar_off = kv_off + NS * kTile;
+  static constexpr int seg_off = bar_off + ((int)sizeof(Bars<NS>) + 15) / 16 * 16;
   static constexpr int ml_off = seg_off + kSegs * (int)sizeof(Seg);  // [stream][row] (maximum, sum)
   static constexpr int misc_off = ml_off + 2 * 128 * 8;
   static constexpr int total = misc_off + 16;
@@ -207,14 +215,14 @@ struct Layout {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
   using L = Layout<D>;
-  constexpr int DH = L::DH, NK = L::NK, NV = L::NV;
+  constexpr int DH = L::DH, NS = L::NS;
   extern __shared__ __align__(1024) uint8_t smem[];  // no slack left to align by hand: checked
   if (smem_u32(smem) & 1023) {
     grid_dep_wait();
     if (threadIdx.x == 0) report_error(p.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 50);
     return;
   }
-  Bars<NK, NV>* bars = reinterpret_cast<Bars<NK, NV>*>(smem + L::bar_off);
+  Bars<NS>* bars = reinterpret_cast<Bars<NS>*>(smem + L::bar_off);
   Seg* segs = reinterpret_cast<Seg*>(smem + L::seg_off);
   float2* ml_s = reinterpret_cast<float2*>(smem + L::ml_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::misc_off);
@@ -225,13 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
-    for (int i = 0; i < NK; ++i) {
-      mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 1);
-    }
-    for (int i = 0; i < NV; ++i) {
-      mbar_init(&bars->v_full[i], 1);
-      mbar_init(&bars->v_empty[i], 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bars->kv_full[i], 1);
+      mbar_init(&bars->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     mbar_init(&bars->ml_full, 8);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bars->seg_full[i], 1);
-      mbar_init(&bars->seg_empty[i], 11);  // two producers, MMA, 8 softmax warps
+      mbar_init(&bars->seg_empty[i], 11);  // producer, query tiles, MMA, 8 softmax warps
     }
     mbar_init(&bars->drain, 1);
     *abort_flag = 0;
@@ -279,37 +283,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
   if (warp < 4) {
     setmaxnreg_dec<kRegsIo>();
     if (warp == 0 && lane == 0) {
-      // ------------------------------------------------------------ query and K producer
+      // ------------------------------------------------------------ K / V producer
       tma_prefetch_desc(&p.tk);
-      tma_prefetch_desc(&p.tq);
+      tma_prefetch_desc(&p.tv);
       Seg s;
-      Ring<NK> k;
+      Ring<NS> r;
       bool ok = true;
+      auto load = [&](const CUtensorMap* map, int t) {
+        if (!mbar_wait(&bars->kv_empty[r.st], r.ph ^ 1, abort_flag)) {
+          fail(SITE_PREFIX_PRODUCER, 1);
+          ok = false;
+          return;
+        }
+        mbar_arrive_expect_tx(&bars->kv_full[r.st], L::kTile);
+        for (int dh = 0; dh < DH; ++dh)
+          tma_load_4d(smem + L::kv_off + r.st * L::kTile + dh * kBlockBytes, map, &bars->kv_full[r.st], dh * 64, s.h,
+                      (s.kt0 + t) * kKeys, s.j);
+        r.skip(1);
+      };
       for (int n = 0; ok && get_seg(n, s); ++n) {
-        for (int t = 0; t < s.NT; ++t) {
-          if (!mbar_wait(&bars->k_empty[k.st], k.ph ^ 1, abort_flag)) {
-            fail(SITE_PREFIX_PRODUCER, 1);
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&bars->k_full[k.st], L::kTile);
-          for (int dh = 0; dh < DH; ++dh)
-            tma_load_4d(smem + L::k_off + k.st * L::kTile + dh * kBlockBytes, &p.tk, &bars->k_full[k.st], dh * 64, s.h,
-                        (s.kt0 + t) * kKeys, s.j);
-          k.next();
-          if (t == 0) {
-            if (!mbar_wait(&bars->q_empty, (n & 1) ^ 1, abort_flag)) {
-              fail(SITE_PREFIX_PRODUCER, 2);
-              ok = false;
-              break;
-            }
-            const int tiles = s.two() ? 2 : 1;
-            mbar_arrive_expect_tx(&bars->q_full, tiles * L::kTile);
-            for (int i = 0; i < tiles; ++i)
-              for (int dh = 0; dh < DH; ++dh)
-                tma_load_4d(smem + L::q_off + i * L::kTile + dh * kBlockBytes, &p.tq, &bars->q_full, dh * 64, s.h * p.G,
-                            s.seq0 + i * (p.seqs / 2), 0);
-          }
+        const int ahead = s.two() ? 1 : 2;  // K tiles before the first V
+        for (int t = 0; ok && t < min(ahead, s.NT); ++t) load(&p.tk, t);
+        for (int t = 0; ok && t < s.NT; ++t) {
+          load(&p.tv, t);
+          if (ok && t + ahead < s.NT) load(&p.tk, t + ahead);
         }
       }
     } else if (warp == 1) {
@@ -323,11 +320,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       // against 84 with a single thread here).  Places in the rings are counted on.
       constexpr uint32_t idesc_qk = idesc_bf16(128, 128, 0);
       constexpr uint32_t idesc_pv = idesc_bf16(128, D, 1);
-      const uint32_t q_lo = desc_lo(sbase + L::q_off, 16), k_lo = desc_lo(sbase + L::k_off, 16),
-                     v_lo = desc_lo(sbase + L::v_off, DH > 1 ? kBlockBytes : 16);
-      Ring<NK> k;
-      Ring<NV> v;
-      int an = 0, a_left = 0, bn = 0, b_left = 0;  // segment and events left of it, for S and for P V
+      const uint32_t q_lo = desc_lo(sbase + L::q_off, 16), k_lo = desc_lo(sbase + L::kv_off, 16),
+                     v_lo = desc_lo(sbase + L::kv_off, DH > 1 ? kBlockBytes : 16);
+      Ring<NS> k, v, base;  // the next K and V tile; the first load of the segment that K is in
+      int an = 0, a_left = 0, a_NT = 0, bn = 0, b_left = 0;  // segment and events left of it, for S and for P V
+      int b_rem = 0;                                         // key tiles left of b's segment
       bool a_two = false, b_two = false;
       uint32_t a_sub = 0, b_sub = 0, aw = 0, bw = 0;  // row tile; stream
       uint32_t a_new = 1, b_new = 2;                  // first event of a segment; first event of each stream in it
@@ -341,22 +338,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         }
         return true;
       };
-      // events and mode of segment n; no events at the end of the work
-      auto fetch = [&](int n, int& left, bool& two, bool last_reader) {
+      // key tiles and mode of segment n; none at the end of the work
+      auto fetch = [&](int n, int& NT, int& left, bool& two, bool last_reader) {
         left = 0;
         if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, 6)) return;
         // warp reductions of equal values: the results are known to be uniform
-        const int NT = __reduce_max_sync(0xffffffffu, segs[n % kSegs].NT);
+        NT = __reduce_max_sync(0xffffffffu, segs[n % kSegs].NT);
         two = __reduce_max_sync(0xffffffffu, segs[n % kSegs].flags) & 1;
         left = two ? 2 * NT : NT;
         if (last_reader && lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
+      };
+      // V of a segment comes after its first K tiles
+      auto enter_v = [&](Ring<NS> at) {
+        v = at;
+        v.skip(b_two ? 1 : min(b_rem, 2));
       };
       auto issue_s = [&]() {
         if (a_new) {
           if (!wait_bar(&bars->q_full, an & 1, 1)) return;
           a_new = 0;
         }
-        if (!a_sub && !wait_bar(&bars->k_full[k.st], k.ph, 2)) return;
+        if (!a_sub && !wait_bar(&bars->kv_full[k.st], k.ph, 2)) return;
         tc_fence_after();
         const uint32_t d = tbase + 128 * aw, a0 = q_lo + a_sub * (L::kTile / 16), b0 = k_lo + k.st * (L::kTile / 16);
 #pragma unroll
@@ -366,24 +368,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         }
         mma_commit_elect(&bars->s_full[aw]);
         if (!a_two || a_sub) {
-          mma_commit_elect(&bars->k_empty[k.st]);
-          k.next();
+          mma_commit_elect(&bars->kv_empty[k.st]);
+          k.skip(!a_two && a_left == a_NT ? 1 : 2);
         }
         if (a_two) a_sub ^= 1;
         aw ^= 1;
         if (--a_left == 0) {
           mma_commit_elect(&bars->q_empty);
           a_new = 1;
-          fetch(++an, a_left, a_two, false);
+          base.jump(2 * a_NT);
+          k = base;
+          fetch(++an, a_NT, a_left, a_two, false);
         }
       };
-      fetch(0, a_left, a_two, false);
-      fetch(0, b_left, b_two, true);
+      Ring<NS> b_base;
+      int b_NT = 0;
+      fetch(0, a_NT, a_left, a_two, false);
+      fetch(0, b_NT, b_left, b_two, true);
+      b_rem = b_NT;
+      enter_v(b_base);
       for (int i = 0; i < 2 && ok && a_left; ++i) issue_s();
       while (ok && b_left) {
         if (!wait_bar(&bars->p_full[bw], (np >> bw) & 1, 3)) break;
         np ^= 1u << bw;
-        if (!b_sub && !wait_bar(&bars->v_full[v.st], v.ph, 4)) break;
+        if (!b_sub && !wait_bar(&bars->kv_full[v.st], v.ph, 4)) break;
         if (b_new == 2 && !wait_bar(&bars->o_empty, (bn & 1) ^ 1, 5)) break;
         tc_fence_after();
         const uint32_t d = tbase + 256 + 128 * bw, a0 = tbase + 128 * bw, b0 = v_lo + v.st * (L::kTile / 16);
@@ -391,8 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         for (int ks = 0; ks < kKeys / 16; ++ks)
           mma_ts_elect(d, a0 + ks * 8, b0 + ks * (2048 / 16), idesc_pv, (b_new == 0 || ks > 0) ? 1u : 0u);
         if (!b_two || b_sub) {
-          mma_commit_elect(&bars->v_empty[v.st]);
-          v.next();
+          mma_commit_elect(&bars->kv_empty[v.st]);
+          --b_rem;
+          v.skip(b_two || b_rem >= 2 ? 2 : 1);
         }
         if (b_new) --b_new;
         if (b_two) b_sub ^= 1;
@@ -400,7 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (--b_left == 0) {
           mma_commit_elect(&bars->o_full);
           b_new = 2;
-          fetch(++bn, b_left, b_two, true);
+          b_base.jump(2 * b_NT);
+          fetch(++bn, b_NT, b_left, b_two, true);
+          b_rem = b_NT;
+          enter_v(b_base);
         }
         if (a_left && ok) issue_s();
       }
@@ -408,24 +420,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       mma_commit_elect(&bars->drain);
       warp_wait(&bars->drain, 0, nullptr);
     } else if (warp == 2 && lane == 0) {
-      // ------------------------------------------------------------ V producer
-      tma_prefetch_desc(&p.tv);
+      // ------------------------------------------------------------ query tiles
+      tma_prefetch_desc(&p.tq);
       Seg s;
-      Ring<NV> v;
-      bool ok = true;
-      for (int n = 0; ok && get_seg(n, s); ++n) {
-        for (int t = 0; t < s.NT; ++t) {
-          if (!mbar_wait(&bars->v_empty[v.st], v.ph ^ 1, abort_flag)) {
-            fail(SITE_PREFIX_PRODUCER, 6);
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&bars->v_full[v.st], L::kTile);
-          for (int dh = 0; dh < DH; ++dh)
-            tma_load_4d(smem + L::v_off + v.st * L::kTile + dh * kBlockBytes, &p.tv, &bars->v_full[v.st], dh * 64, s.h,
-                        (s.kt0 + t) * kKeys, s.j);
-          v.next();
+      for (int n = 0; get_seg(n, s); ++n) {
+        if (!mbar_wait(&bars->q_empty, (n & 1) ^ 1, abort_flag)) {
+          fail(SITE_PREFIX_PRODUCER, 2);
+          break;
         }
+        const int tiles = s.two() ? 2 : 1;
+        mbar_arrive_expect_tx(&bars->q_full, tiles * L::kTile);
+        for (int i = 0; i < tiles; ++i)
+          for (int dh = 0; dh < DH; ++dh)
+            tma_load_4d(smem + L::q_off + i * L::kTile + dh * kBlockBytes, &p.tq, &bars->q_full, dh * 64, s.h * p.G,
+                        s.seq0 + i * (p.seqs / 2), 0);
       }
     } else if (warp == 3) {
       // ------------------------------------------------------------ the CTA's share
@@ -625,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         }
         if (left < kKeys && s.len < p.P) {
           // V rows past the length hold anything, and 0 * NaN would be NaN: zero them
-          const int seq = sb + t, st = seq % NV;
-          if (!warp_wait(&bars->v_full[st], (seq / NV) & 1, abort_flag)) {
+          const int seq = sb + pos_v(two, s.NT, t), st = seq % NS;
+          if (!warp_wait(&bars->kv_full[st], (seq / NS) & 1, abort_flag)) {
             if (lane == 0) fail(SITE_PREFIX_SOFTMAX, 2);
             ok = false;
             break;
@@ -634,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           if (row >= left) {
 #pragma unroll
             for (int dh = 0; dh < DH; ++dh) {
-              uint4* r = reinterpret_cast<uint4*>(smem + L::v_off + st * L::kTile + dh * kBlockBytes + row * 128);
+              uint4* r = reinterpret_cast<uint4*>(smem + L::kv_off + st * L::kTile + dh * kBlockBytes + row * 128);
 #pragma unroll
               for (int u = 0; u < 8; ++u) r[u] = make_uint4(0, 0, 0, 0);
             }
@@ -743,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       }
       tc_fence_before();
       par ^= (two ? 2 * s.NT : s.NT) & 1;
-      sb += s.NT;
+      sb += 2 * s.NT;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&bars->o_empty);
