@@ -30,9 +30,8 @@
 // core works on one while the other is in its softmax.  A segment of more than
 // 128 rows gives each its own row tile; a smaller one gives both the same rows
 // and every other key tile, and joins the two in the epilogue.  S = Q K^T lands in
-// TMEM (fp32), becomes bf16 P in place, and O += P V reads P from TMEM.  A row's
-// reference is the maximum of its first tile; it moves (with O and the sum) only when a
-// tile's weights against it sum to more than 2^20.
+// TMEM (fp32), becomes bf16 P in place, and O += P V reads P from TMEM.  Running
+// maxima are moved lazily, when they grow by more than 2^8.
 #include <string.h>
 
 #include <atomic>
@@ -46,7 +45,7 @@ constexpr int kThreads = 384;
 constexpr int kKeys = 128;
 constexpr int kBlockRows = 256;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
-constexpr float kDirectMax = 1048576.0f;  // 2^20: leaves V all but 2^20 of its range
+constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMergeThreads = 256;
 // Time between the last tile of a segment and the first of the next, in key tiles.
 constexpr int kSetup = 4;
@@ -76,12 +75,6 @@ struct PrefixParams {
   int n, m, P, Hq, H, G, seqs;  // seqs = 256 / G sequences of a row block
   float scale_log2;
 };
-
-__device__ __forceinline__ float sum2(uint64_t v) {
-  float lo, hi;
-  unpack2(v, lo, hi);
-  return lo + hi;
-}
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
@@ -553,10 +546,46 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         if (warp_on) {
           // the whole S row of this thread (128 fp32) in registers; keys past the length -> -inf
           uint32_t sr[4][32];
-          tmem_ld32(tl + s_col, sr[0]);
-          uint64_t lacc = 0;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) tmem_ld32(tl + s_col + ch * 32, sr[ch]);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) tmem_wait_ld_dep(sr[ch]);
+          float mt = neg_inf();
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            if (left < ch * 32 + 32) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (ch * 32 + c >= left) sr[ch][c] = 0xff800000u;
+            }
+            mt = fmaxf(mt, max32(sr[ch]));
+          }
+          const float m_new = fmaxf(m_ref, mt);
+          const bool need = (m_new - m_ref) * sl2 > kRescaleLog2;  // true when m_ref == -inf and mt finite
+          float alpha = 1.0f;
+          if (need) {
+            alpha = ex2_approx((m_ref - m_new) * sl2);
+            l *= alpha;
+            m_ref = m_new;
+          }
+          if (__any_sync(0xffffffffu, need) && i > 0) {
+            // O of this stream's last event is complete: S of this one was issued after it
+#pragma unroll 1
+            for (int cd = 0; cd < D / 32; ++cd) {
+              uint32_t r[32];
+              tmem_ld32(tl + o_col + cd * 32, r);
+              tmem_wait_ld_dep(r);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
+              tmem_st32(tl + o_col + cd * 32, r);
+            }
+          }
           // P = exp2(s * scale_log2 - m) as bf16, written over S
-          auto weights = [&](int ch, uint64_t n2) {
+          const float nm = (m_ref == neg_inf()) ? 0.0f : -m_ref * sl2;
+          const uint64_t n2 = pack2(nm, nm);
+          uint64_t lacc = 0;
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
             uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
@@ -568,67 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
               pk[c >> 1] = pack_bf16x2(p0, p1);
             }
             tmem_st16(tl + s_col + ch * 16, pk);
-          };
-          auto mask = [&](int ch) {
-            if (left < ch * 32 + 32) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (ch * 32 + c >= left) sr[ch][c] = 0xff800000u;
-            }
-          };
-          // The direct way: weights against the reference that the row has.  It is kept as long
-          // as no weight is near overflow; their precision does not depend on their size.
-          bool direct = i > 0;
-          if (direct) {
-            const float nm = (m_ref == neg_inf()) ? 0.0f : -m_ref * sl2;
-            const uint64_t n2 = pack2(nm, nm);
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              tmem_wait_ld_dep(sr[ch]);
-              if (ch < 3) tmem_ld32(tl + s_col + (ch + 1) * 32, sr[ch + 1]);
-              mask(ch);
-              weights(ch, n2);
-            }
-            const float sum = sum2(lacc);
-            direct = __all_sync(0xffffffffu, !row_on || (m_ref != neg_inf() && sum < kDirectMax));
-            if (direct) l += sum;
-          } else {
-#pragma unroll
-            for (int ch = 1; ch < 4; ++ch) tmem_ld32(tl + s_col + ch * 32, sr[ch]);
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              tmem_wait_ld_dep(sr[ch]);
-              mask(ch);
-            }
           }
-          if (!direct) {
-            float mt = neg_inf();
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) mt = fmaxf(mt, max32(sr[ch]));
-            const float m_new = fmaxf(m_ref, mt);
-            if (i > 0) {
-              // O of this stream's last event is complete: S of this one was issued after it
-              const float alpha = m_new > m_ref ? ex2_approx((m_ref - m_new) * sl2) : 1.0f;
-              l *= alpha;
-#pragma unroll
-              for (int cd = 0; cd < D / 32; ++cd) {
-                uint32_t r[32];
-                tmem_ld32(tl + o_col + cd * 32, r);
-                tmem_wait_ld_dep(r);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
-                tmem_st32(tl + o_col + cd * 32, r);
-              }
-            }
-            m_ref = m_new;
-            const float nm = (m_ref == neg_inf()) ? 0.0f : -m_ref * sl2;
-            const uint64_t n2 = pack2(nm, nm);
-            lacc = 0;
-            tmem_wait_st();  // the weights of the direct way, which these replace
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) weights(ch, n2);
-            l += sum2(lacc);
-          }
+          float l0, l1;
+          unpack2(lacc, l0, l1);
+          l += l0 + l1;
           tmem_wait_st();
         }
         if (left < kKeys && s.len < p.P) {
