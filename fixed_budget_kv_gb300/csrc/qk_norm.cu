@@ -12,7 +12,10 @@
 // row, D/16 lanes to a row -- so the rotation needs no exchange and a row's sum
 // takes log2(D/16) shuffles.  A warp takes one token: its lanes compute the
 // token's R/2 angles once (shared out over the row groups) and use them for
-// every head.  HBM-bound: 4 bytes a value forward, 8 backward.
+// every head; with few tokens, or to fill the last round, several warps share one.
+// HBM-bound: 4 bytes a value forward, 8 backward.  Measured (Hq 32, H 8, D 128, q and k
+// from a packed projection, one GB300): 16 384 tokens 60 us forward (82% of the copy rate)
+// and 118 us backward (83%), 131 072 tokens 421 us forward (94%).
 //
 // Angles: f / 2 pi becomes a 64-bit fixed-point fraction of a turn, so the
 // product with an integer position wraps at whole turns without any loss; the
@@ -24,7 +27,10 @@ namespace kvpop {
 namespace {
 
 constexpr int kWarps = 4;          // per CTA
-constexpr int kCtasPerSm = 5;      // grid limit: resident CTAs
+// Resident CTAs an SM, the grid's limit.  16 384 tokens forward: 71 us with 3, 61 with 4,
+// 60 with 5, 70 with 6; backward, warps x CTAs: 118 us with 8 x 2, 126 with 4 x 3, 120 with
+// 16 x 1.
+constexpr int kCtasPerSm = 5;
 constexpr int kBwdWarps = 8;
 constexpr int kBwdCtasPerSm = 2;
 constexpr int kBwdMaxCtas = 1024;  // rows of the weight gradients' workspace

@@ -380,9 +380,10 @@ kvpop_status kvpop_cache_position(const kvpop_cache* cache, int32_t* q_next);
  *          Out-of-range values of cu and lens are clamped.
  *   O2     [n, Hq, D] bf16, lse2 [n, Hq] fp32, both or neither; a row with
  *          lse2 = -inf contributes nothing, whatever O2 holds
- *   O      [n, Hq, D] bf16, lse [n, Hq] fp32 natural log; O may be O2 and lse lse2
+ *   O      [n, Hq, D] bf16, lse [n, Hq] fp32 natural log; O may be O2 and lse lse2,
+ *          no other overlap
  * scale <= 0 selects 1/sqrt(D).  D 64 or 128, G dividing 128, H, Hq and m up to
- * 65535, n up to 2^24, tensors 16-byte aligned.  bf16 operands (the softmax
+ * 65535, n up to 2^24, P up to 2^30, tensors 16-byte aligned.  bf16 operands (the softmax
  * weights rounded to bf16 before their product with V), fp32 accumulation.
  * workspace: kvpop_prefix_attn_workspace_size() bytes, 256-byte aligned; contents
  * undefined between calls, so calls that overlap in time need one each.

@@ -164,6 +164,8 @@ def test_join_edges():
     check(O, lse, q, k, v, cu, lens, (O2, l2))
     assert torch.equal(O[5:], O2[5:]) and torch.equal(O[1], O2[1])
     assert (O[4] == 0).all() and (lse[4] == -math.inf).all()
+    empty, el = kvpop.prefix_attn(q, k, v, i32(cu), i32([0, 0]), (O2, l2))
+    check(empty, el, q, k, v, cu, [0, 0], (O2, l2))
     alone, al = kvpop.prefix_attn(q, k, v, i32(cu), i32(lens))
     assert torch.equal(alone[0], O[0]) and torch.equal(alone[2], O[2])
     assert (alone[4:] == 0).all() and (al[4:] == -math.inf).all()

@@ -79,6 +79,7 @@ def prefix(lib, q=P, k=P, n=4, m=1, L=100, Hq=8, H=2, D=64, cu=P, lens=P, O2=Non
     (dict(nb=16), 1),
     (dict(q=ctypes.c_void_p(264)), 2), (dict(O=ctypes.c_void_p(258)), 2), (dict(O2=ctypes.c_void_p(264), lse2=P), 2),
     (dict(ws=ctypes.c_void_p(272)), 2), (dict(m=70000), 2), (dict(n=(1 << 24) + 1), 2), (dict(H=70000, Hq=70000), 2),
+    (dict(L=(1 << 30) + 1), 2), (dict(n=1 << 24, H=64, Hq=4096, L=1 << 20), 2),   # more tiles than 2^31
 ], ids=lambda x: str(x))
 def test_prefix_refusals(lib, kw, code):
     assert prefix(lib, **kw) == code
