@@ -14,8 +14,10 @@
 // token's R/2 angles once (shared out over the row groups) and use them for
 // every head; with few tokens, or to fill the last round, several warps share one.
 // HBM-bound: 4 bytes a value forward, 8 backward.  Measured (Hq 32, H 8, D 128, q and k
-// from a packed projection, one GB300): 16 384 tokens 60 us forward (82% of the copy rate)
-// and 118 us backward (83%), 131 072 tokens 421 us forward (94%).
+// from a packed projection, one GB300): 16 384 tokens 57 us forward (87% of the copy rate)
+// and 111 us backward (89%), 131 072 tokens 402 us forward (98%).  Angles and weights stay
+// in shared memory, in the order in which the lanes read them: the registers that this
+// frees are worth more as further warps (421 -> 402 us, 118 -> 111 us).
 //
 // Angles: f / 2 pi becomes a 64-bit fixed-point fraction of a turn, so the
 // product with an integer position wraps at whole turns without any loss; the
@@ -27,12 +29,13 @@ namespace kvpop {
 namespace {
 
 constexpr int kWarps = 4;          // per CTA
-// Resident CTAs an SM, the grid's limit.  16 384 tokens forward: 71 us with 3, 61 with 4,
-// 60 with 5, 70 with 6; backward, warps x CTAs: 118 us with 8 x 2, 126 with 4 x 3, 120 with
-// 16 x 1.
-constexpr int kCtasPerSm = 5;
-constexpr int kBwdWarps = 8;
-constexpr int kBwdCtasPerSm = 2;
+// Resident CTAs an SM, the grid's limit: as many warps as the registers allow without
+// spills.  16 384 tokens forward (loads two passes ahead): 58.7 us with 5, 56.8 with 6, 57.0
+// with 7; backward (no loads ahead, more warps instead): 111 us with 5, 132 with 6, and 115
+// with 4 and loads one pass ahead.
+constexpr int kCtasPerSm = 6;
+constexpr int kBwdWarps = 4;
+constexpr int kBwdCtasPerSm = 5;
 constexpr int kBwdMaxCtas = 1024;  // rows of the weight gradients' workspace
 
 struct QkParams {
@@ -99,13 +102,26 @@ __device__ __forceinline__ float sum2(uint64_t v) {
   return lo + hi;
 }
 
-// Eight floats of shared memory as four pairs.
-__device__ __forceinline__ void lds8(const float* s, uint64_t (&x)[4]) {
-  const float4 u = reinterpret_cast<const float4*>(s)[0], v = reinterpret_cast<const float4*>(s)[1];
+// Eight floats of lane j: float4 j of two consecutive rows of LPR float4 (no bank conflicts).
+template <int LPR>
+__device__ __forceinline__ void lds8(const float4* s, int j, uint64_t (&x)[4]) {
+  const float4 u = s[j], v = s[LPR + j];
   x[0] = pack2(u.x, u.y);
   x[1] = pack2(u.z, u.w);
   x[2] = pack2(v.x, v.y);
   x[3] = pack2(v.z, v.w);
+}
+
+// Weights in that order: rows 0, 1 for piece a of each lane, 2, 3 for piece b.
+template <int D, bool INTER>
+__device__ __forceinline__ void stage_weights(float4* dst, const float* w, int nrot, int thread, int threads) {
+  constexpr int LPR = D / 16;
+  for (int i = thread; i < 4 * LPR; i += threads) {
+    int a, b;
+    pieces<INTER>(i % LPR, nrot, a, b);
+    const int col = 8 * (i < 2 * LPR ? a : b) + 4 * (i / LPR & 1);
+    dst[i] = w ? make_float4(w[col], w[col + 1], w[col + 2], w[col + 3]) : make_float4(1.f, 1.f, 1.f, 1.f);
+  }
 }
 
 // Turns per position as a fraction of 2^64, whole turns dropped: the 24-bit
@@ -123,48 +139,46 @@ __device__ __forceinline__ unsigned long long turns64(float f) {
   return u >> 31 ? 0ull - r : r;
 }
 
-// The eight angles of lane j = lane % LPR: each of the 32 / LPR row groups computes
-// its share and the lanes of equal j exchange them.
+// The eight angles of each lane j = lane % LPR: the 32 / LPR row groups compute a share
+// each, into the warp's shared memory -- cos in rows 0, 1, sin in rows 2, 3 of LPR float4.
 template <int LPR>
 struct Angles {
   static constexpr int RPP = 32 / LPR, MINE = 8 / RPP;
   unsigned long long turn[MINE];
-  uint64_t c[4], s[4], ns[4];  // cos, sin and -sin of angles (2 i, 2 i + 1)
+  float4* s;
 
-  __device__ __forceinline__ void init(const float* inv_freq, int j, int rg, int nrot) {
+  __device__ __forceinline__ void init(float4* smem, const float* inv_freq, int j, int rg, int nrot) {
+    s = smem;
 #pragma unroll
     for (int i = 0; i < MINE; ++i) turn[i] = j < nrot ? turns64(inv_freq[8 * j + rg * MINE + i]) : 0ull;
   }
-  __device__ __forceinline__ void at(int pos, int j) {
-    float mc[MINE], ms[MINE];
+  __device__ __forceinline__ void at(int pos, int j, int rg) {
+    __syncwarp();  // every lane has read the angles of the token before
 #pragma unroll
     for (int i = 0; i < MINE; ++i) {
       const unsigned long long a = turn[i] * (unsigned long long)(long long)pos;
-      sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &ms[i], &mc[i]);  // half turns in [-1, 1]
+      float sn, cs;
+      sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &sn, &cs);  // half turns in [-1, 1]
+      const int e = rg * MINE + i;
+      float* dst = reinterpret_cast<float*>(s + (e >> 2) * LPR + j) + (e & 3);
+      dst[0] = cs;
+      dst[8 * LPR] = sn;
     }
-    float cc[8], ss[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int src = (e / MINE) * LPR + j;
-      cc[e] = __shfl_sync(0xffffffffu, mc[e % MINE], src);
-      ss[e] = __shfl_sync(0xffffffffu, ms[e % MINE], src);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = pack2(cc[2 * i], cc[2 * i + 1]);
-      s[i] = pack2(ss[2 * i], ss[2 * i + 1]);
-      ns[i] = pack2(-ss[2 * i], -ss[2 * i + 1]);
-    }
+    __syncwarp();
   }
   // Half-split pairs sit at the same place of the two pieces, adjacent pairs next to each
   // other in one of them.  BACK turns the other way.
   template <bool INTER, bool BACK>
-  __device__ __forceinline__ void rotate(uint64_t (&a)[4], uint64_t (&b)[4]) const {
+  __device__ __forceinline__ void rotate(uint64_t (&a)[4], uint64_t (&b)[4], int j) const {
+    uint64_t c[4], sn[4];
+    lds8<LPR>(s, j, c);
+    lds8<LPR>(s + 2 * LPR, j, sn);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!INTER) {
-        const uint64_t u = fma2(b[i], BACK ? s[i] : ns[i], mul2(a[i], c[i]));
-        b[i] = fma2(a[i], BACK ? ns[i] : s[i], mul2(b[i], c[i]));
+        const uint64_t ns = sn[i] ^ 0x8000000080000000ull;
+        const uint64_t u = fma2(b[i], BACK ? sn[i] : ns, mul2(a[i], c[i]));
+        b[i] = fma2(a[i], BACK ? ns : sn[i], mul2(b[i], c[i]));
         a[i] = u;
       } else {
 #pragma unroll
@@ -174,9 +188,9 @@ struct Angles {
           float u, v, c0, c1, s0, s1;
           unpack2(y, u, v);
           unpack2(c[i], c0, c1);
-          unpack2(s[i], s0, s1);
-          const float cs = h ? c1 : c0, sn = BACK ? -(h ? s1 : s0) : (h ? s1 : s0);
-          y = pack2(u * cs - v * sn, v * cs + u * sn);
+          unpack2(sn[i], s0, s1);
+          const float cs = h ? c1 : c0, sg = BACK ? -(h ? s1 : s0) : (h ? s1 : s0);
+          y = pack2(u * cs - v * sg, v * cs + u * sg);
         }
       }
     }
@@ -184,7 +198,7 @@ struct Angles {
 };
 
 // The passes of a warp's tasks, one after the other: pass ps of token t takes head
-// rows ps * RPP .. of the token.  Loads run ahead, into the next task.
+// rows ps * RPP .. of the token.  The forward's loads run ahead, into the next task.
 struct Passes {
   uint32_t task, ntask, step;
   int t, ps, p1;
@@ -212,7 +226,8 @@ struct Passes {
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) qk_norm_fwd(const QkParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;
-  __shared__ __align__(16) float w_s[2 * D];
+  __shared__ float4 w_s[2 * 4 * LPR];  // q, k
+  __shared__ float4 ang_s[kWarps][4 * LPR];
   const int lane = lane_id(), j = lane % LPR, rg = lane / LPR;
   grid_dep_launch();
   grid_dep_wait();  // the projections, positions and weights come from earlier kernels
@@ -246,12 +261,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) qk_norm_fwd(const QkP
   r0[0] = r0[1] = r1[0] = r1[1] = make_uint4(0, 0, 0, 0);
   load(r0[0], r0[1]);
   load(r1[0], r1[1]);
-  for (int i = threadIdx.x; i < 2 * D; i += kWarps * 32) {
-    const float* w = i < D ? p.wq : p.wk;
-    w_s[i] = w ? w[i % D] : 1.0f;
-  }
+  stage_weights<D, INTER>(w_s, p.wq, p.nrot, threadIdx.x, kWarps * 32);
+  stage_weights<D, INTER>(w_s + 4 * LPR, p.wk, p.nrot, threadIdx.x, kWarps * 32);
   Angles<LPR> ang;
-  if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
+  if (p.nrot) ang.init(ang_s[warp_id()], p.inv_freq, j, rg, p.nrot);
   __syncthreads();
   uint4 *qo_t, *ko_t;
   bool fresh = true;
@@ -263,7 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) qk_norm_fwd(const QkP
     if (fresh) {
       qo_t = reinterpret_cast<uint4*>(p.q_out + cur.t * p.qo_stride);
       ko_t = reinterpret_cast<uint4*>(p.k_out + cur.t * p.ko_stride) - (long long)p.Hq * (D / 8);
-      if (p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j);
+      if (p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j, rg);
     }
     const int row = cur.ps * RPP + rg;
     const bool is_k = row >= p.Hq;
@@ -278,14 +291,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) qk_norm_fwd(const QkP
     for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = rsqrtf(ss * (1.0f / D) + p.eps);
     const uint64_t r2 = pack2(r, r);
-    const float* w = w_s + (is_k ? D : 0);
-    lds8(w + 8 * pa, wt);
+    const float4* w = w_s + (is_k ? 4 * LPR : 0);
+    lds8<LPR>(w, j, wt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = mul2(mul2(a[i], r2), wt[i]);
-    lds8(w + 8 * pb, wt);
+    lds8<LPR>(w + 2 * LPR, j, wt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = mul2(mul2(b[i], r2), wt[i]);
-    if (j < p.nrot) ang.template rotate<INTER, false>(a, b);
+    if (j < p.nrot) ang.template rotate<INTER, false>(a, b, j);
     if (row < rows) {
       uint4* dst = (is_k ? ko_t : qo_t) + row * (D / 8);
       dst[pa] = pack8(a);
@@ -307,7 +320,8 @@ template <int D, bool INTER>
 __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(const QkParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR;
   __shared__ float red[kBwdWarps][D];
-  __shared__ __align__(16) float w_s[D];
+  __shared__ float4 w_s[4 * LPR];
+  __shared__ float4 ang_s[kBwdWarps][4 * LPR];
   const int lane = lane_id(), warp = warp_id(), j = lane % LPR, rg = lane / LPR;
   grid_dep_launch();
   grid_dep_wait();
@@ -328,50 +342,34 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
   cur.ntask = (uint32_t)p.T * slices;
   cur.step = ctas * kBwdWarps;
   cur.enter(slices, passes);
-  struct Raw {
-    uint4 xa, xb;
-    float4 g[4];
-  };
-  auto load = [&](const Passes& c, Raw& v) {
-    const int row = c.ps * RPP + rg;
-    v.xa = v.xb = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v.g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!c.live() || row >= heads) return;
-    const __nv_bfloat16* src = x_base + c.t * x_stride + (size_t)row * D;
-    v.xa = reinterpret_cast<const uint4*>(src)[pa];
-    v.xb = reinterpret_cast<const uint4*>(src)[pb];
-    const float4* g = reinterpret_cast<const float4*>(g_base + ((size_t)c.t * heads + row) * D);
-    v.g[0] = g[2 * pa];
-    v.g[1] = g[2 * pa + 1];
-    v.g[2] = g[2 * pb];
-    v.g[3] = g[2 * pb + 1];
-  };
-  Raw raw;
-  load(cur, raw);
   uint64_t da[4] = {}, db[4] = {};
-  for (int i = threadIdx.x; i < D; i += kBwdWarps * 32) w_s[i] = w ? w[i] : 1.0f;
+  stage_weights<D, INTER>(w_s, w, p.nrot, threadIdx.x, kBwdWarps * 32);
   Angles<LPR> ang;
-  if (p.nrot) ang.init(p.inv_freq, j, rg, p.nrot);
+  if (p.nrot) ang.init(ang_s[warp], p.inv_freq, j, rg, p.nrot);
   __syncthreads();
   bool fresh = true;
 #pragma unroll 1
   while (cur.live()) {
-    Passes nxt = cur;
-    const bool entered = nxt.next(slices, passes);
-    uint64_t a[4], b[4], ga[4], gb[4], wt[4];
-    unpack8(raw.xa, a);
-    unpack8(raw.xb, b);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ga[2 * i] = pack2(raw.g[i].x, raw.g[i].y);
-      ga[2 * i + 1] = pack2(raw.g[i].z, raw.g[i].w);
-      gb[2 * i] = pack2(raw.g[2 + i].x, raw.g[2 + i].y);
-      gb[2 * i + 1] = pack2(raw.g[2 + i].z, raw.g[2 + i].w);
+    const int row = cur.ps * RPP + rg;
+    uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
+    float4 g0 = make_float4(0.f, 0.f, 0.f, 0.f), g1 = g0, g2 = g0, g3 = g0;
+    if (row < heads) {
+      const uint4* x = reinterpret_cast<const uint4*>(x_base + cur.t * x_stride + (size_t)row * D);
+      const float4* g = reinterpret_cast<const float4*>(g_base + ((size_t)cur.t * heads + row) * D);
+      xa = x[pa];
+      xb = x[pb];
+      g0 = g[2 * pa];
+      g1 = g[2 * pa + 1];
+      g2 = g[2 * pb];
+      g3 = g[2 * pb + 1];
     }
-    load(nxt, raw);
-    if (fresh && p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j);
-    if (j < p.nrot) ang.template rotate<INTER, true>(ga, gb);  // g is now dL/dy
+    if (fresh && p.nrot) ang.at(p.pos ? p.pos[cur.t] : cur.t % p.S, j, rg);
+    uint64_t a[4], b[4], wt[4];
+    uint64_t ga[4] = {pack2(g0.x, g0.y), pack2(g0.z, g0.w), pack2(g1.x, g1.y), pack2(g1.z, g1.w)};
+    uint64_t gb[4] = {pack2(g2.x, g2.y), pack2(g2.z, g2.w), pack2(g3.x, g3.y), pack2(g3.z, g3.w)};
+    unpack8(xa, a);
+    unpack8(xb, b);
+    if (j < p.nrot) ang.template rotate<INTER, true>(ga, gb, j);  // g is now dL/dy
     uint64_t sq = 0, ex = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -379,10 +377,10 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
       sq = fma2(b[i], b[i], sq);
     }
     // a weight piece at a time, twice: the registers are short
-    lds8(w_s + 8 * pa, wt);
+    lds8<LPR>(w_s, j, wt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) ex = fma2(mul2(ga[i], wt[i]), a[i], ex);
-    lds8(w_s + 8 * pb, wt);
+    lds8<LPR>(w_s + 2 * LPR, j, wt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) ex = fma2(mul2(gb[i], wt[i]), b[i], ex);
     float ss = sum2(sq), es = sum2(ex);
@@ -394,7 +392,6 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
     const float r = rsqrtf(ss * (1.0f / D) + p.eps);
     const float back = -r * r * (es * (1.0f / D));
     const uint64_t r2 = pack2(r, r), back2 = pack2(back, back);
-    const int row = cur.ps * RPP + rg;
     if (row < heads) {
       __nv_bfloat16* dst = o_base + cur.t * o_stride + (size_t)row * D;
 #pragma unroll
@@ -402,17 +399,16 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
         da[i] = fma2(ga[i], mul2(a[i], r2), da[i]);
         db[i] = fma2(gb[i], mul2(b[i], r2), db[i]);
       }
-      lds8(w_s + 8 * pb, wt);
+      lds8<LPR>(w_s + 2 * LPR, j, wt);
 #pragma unroll
       for (int i = 0; i < 4; ++i) b[i] = mul2(fma2(b[i], back2, mul2(gb[i], wt[i])), r2);
       reinterpret_cast<uint4*>(dst)[pb] = pack8(b);
-      lds8(w_s + 8 * pa, wt);
+      lds8<LPR>(w_s, j, wt);
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = mul2(fma2(a[i], back2, mul2(ga[i], wt[i])), r2);
       reinterpret_cast<uint4*>(dst)[pa] = pack8(a);
     }
-    fresh = entered;
-    cur = nxt;
+    fresh = cur.next(slices, passes);
   }
   // this CTA's sums over its rows, in a fixed order
 #pragma unroll

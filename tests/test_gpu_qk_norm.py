@@ -235,3 +235,15 @@ def test_binding_refusals():
     with pytest.raises(ValueError, match="dwk"):
         kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f,
                                out=(torch.empty_like(q), torch.empty_like(k), wq, wq.double()))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_gradients_in_place(packed):
+    """The gradients may replace q and k, contiguous or as parts of the packed projection."""
+    q, k, wq, wk, gq, gk = make(3, 90, 6, 2, 64, seed=13, packed=packed)
+    f = freqs(32)
+    ref = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f, interleaved=True)
+    got = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f, interleaved=True,
+                                 out=(q, k, torch.empty_like(wq), torch.empty_like(wk)))
+    for a, r in zip(got, ref):
+        assert torch.equal(a, r)
