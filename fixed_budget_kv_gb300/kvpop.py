@@ -152,11 +152,9 @@ def _device(t, name):
 
 
 def _fit(t, dtype, dev, shape, name):
-    """The address of a contiguous CUDA tensor of this type and shape on device dev; None for None."""
-    if t is None:
-        return None
+    """A contiguous CUDA tensor of this type and shape on device dev."""
     if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+        return
     _need(t, dtype, name)
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
@@ -167,7 +165,8 @@ _here = contextlib.nullcontext()
 
 
 def _empty_as(t):
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    # torch.empty alone: every further torch function next to a launch costs the host about a microsecond
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _on(stream):
@@ -387,17 +386,23 @@ def _token_stride(t, shape, dev, name):
 
 
 def _qk_args(q, k, wq, wk, inv_freq, pos):
-    """(device, shapes, token strides, R) and the addresses of the optional inputs."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [b, S, Hq, D] and k [b, S, H, D]")
-    b, S, Hq, D = qs = q.shape
+    b, S, Hq, D = q.shape
     H = k.shape[2]
     dev = _device(q, "q")
-    sq, sk = _token_stride(q, qs, dev, "q"), _token_stride(k, (b, S, H, D), dev, "k")
-    half = 0 if inv_freq is None else inv_freq.numel()
-    return (dev, b, S, Hq, H, D, sq, sk, 2 * half, _fit(wq, torch.float32, dev, (D,), "wq"),
-            _fit(wk, torch.float32, dev, (D,), "wk"), _fit(inv_freq, torch.float32, dev, (half,), "inv_freq"),
-            _fit(pos, torch.int32, dev, (b, S), "pos"))
+    sq, sk = _token_stride(q, (b, S, Hq, D), dev, "q"), _token_stride(k, (b, S, H, D), dev, "k")
+    if wq is not None:
+        _fit(wq, torch.float32, dev, (D,), "wq")
+    if wk is not None:
+        _fit(wk, torch.float32, dev, (D,), "wk")
+    R = 0
+    if inv_freq is not None:
+        R = 2 * inv_freq.numel()
+        _fit(inv_freq, torch.float32, dev, (R // 2,), "inv_freq")
+    if pos is not None:
+        _fit(pos, torch.int32, dev, (b, S), "pos")
+    return dev, sq, sk, b, S, Hq, H, D, R
 
 
 def qk_norm_rope(q, k, wq, wk, eps: float, inv_freq, pos=None, interleaved: bool = False, out=None, stream=None):
@@ -405,16 +410,16 @@ def qk_norm_rope(q, k, wq, wk, eps: float, inv_freq, pos=None, interleaved: bool
     None) and the rotation of the first 2 * len(inv_freq) dims at positions pos (int32
     [b,S]; None: 0..S-1).  q and k may be views of a packed projection.  Returns
     contiguous (q_out, k_out); a decode step's n tokens are [n,1,heads,D]."""
-    dev, b, S, Hq, H, D, sq, sk, R, pwq, pwk, pf, ppos = _qk_args(q, k, wq, wk, inv_freq, pos)
+    dev, sq, sk, b, S, Hq, H, D, R = _qk_args(q, k, wq, wk, inv_freq, pos)
     if out is None:
         with _on(stream):
             qo, ko = _empty_as(q), _empty_as(k)
-        pq, pk = qo.data_ptr(), ko.data_ptr()
     else:
         qo, ko = out
-        pq, pk = _fit(qo, torch.bfloat16, dev, q.shape, "q_out"), _fit(ko, torch.bfloat16, dev, k.shape, "k_out")
-    st = load().kvpop_qk_norm_rope(q.data_ptr(), sq, k.data_ptr(), sk, b, S, Hq, H, D, pwq, pwk, eps, pf, R,
-                                   1 if interleaved else 0, ppos, pq, pk, _stream(stream))
+        _fit(qo, torch.bfloat16, dev, q.shape, "q_out")
+        _fit(ko, torch.bfloat16, dev, k.shape, "k_out")
+    st = load().kvpop_qk_norm_rope(_p(q), sq, _p(k), sk, b, S, Hq, H, D, _p(wq), _p(wk), eps, _p(inv_freq), R,
+                                   1 if interleaved else 0, _p(pos), _p(qo), _p(ko), _stream(stream))
     if st:
         _check(st, "kvpop_qk_norm_rope")
     return qo, ko
@@ -433,24 +438,29 @@ def qk_norm_rope_bwd(q, k, dq, dk, wq, wk, eps: float, inv_freq, pos=None, inter
     (attn_bwd's): (dq_in, dk_in bf16, dwq, dwk fp32 [D]).  q and k are the forward's
     inputs.  `out` may hold views of a packed projection's gradient, and None for a
     weight gradient that is not wanted."""
-    dev, b, S, Hq, H, D, sq, sk, R, pwq, pwk, pf, ppos = _qk_args(q, k, wq, wk, inv_freq, pos)
-    pdq, pdk = _fit(dq, torch.float32, dev, q.shape, "dq"), _fit(dk, torch.float32, dev, k.shape, "dk")
+    dev, sq, sk, b, S, Hq, H, D, R = _qk_args(q, k, wq, wk, inv_freq, pos)
+    _fit(dq, torch.float32, dev, q.shape, "dq")
+    _fit(dk, torch.float32, dev, k.shape, "dk")
     with _on(stream):
         if workspace is None:
             workspace = torch.empty(qk_norm_rope_bwd_workspace_size(D), dtype=torch.uint8, device=q.device)
+        else:
+            _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
         if out is None:
-            out = (_empty_as(q), _empty_as(k), torch.empty(D, dtype=torch.float32, device=q.device),
-                   torch.empty(D, dtype=torch.float32, device=q.device))
-    dqi, dki, dwq, dwk = out
-    so, sp = _token_stride(dqi, q.shape, dev, "dq_in"), _token_stride(dki, k.shape, dev, "dk_in")
-    st = load().kvpop_qk_norm_rope_bwd(q.data_ptr(), sq, k.data_ptr(), sk, pdq, pdk, b, S, Hq, H, D, pwq, pwk, eps, pf, R,
-                                       1 if interleaved else 0, ppos, dqi.data_ptr(), so, dki.data_ptr(), sp,
-                                       _fit(dwq, torch.float32, dev, (D,), "dwq"),
-                                       _fit(dwk, torch.float32, dev, (D,), "dwk"),
-                                       _fit(workspace, torch.uint8, dev, workspace.shape, "workspace"),
-                                       workspace.numel(), _stream(stream))
-    if st:
-        _check(st, "kvpop_qk_norm_rope_bwd")
+            dqi, dki = _empty_as(q), _empty_as(k)
+            dwq, dwk = (torch.empty(D, dtype=torch.float32, device=q.device) for _ in range(2))
+            so, sp = Hq * D, H * D
+        else:
+            dqi, dki, dwq, dwk = out
+            so, sp = _token_stride(dqi, q.shape, dev, "dq_in"), _token_stride(dki, k.shape, dev, "dk_in")
+            if dwq is not None:
+                _fit(dwq, torch.float32, dev, (D,), "dwq")
+            if dwk is not None:
+                _fit(dwk, torch.float32, dev, (D,), "dwk")
+    _check(load().kvpop_qk_norm_rope_bwd(_p(q), sq, _p(k), sk, _p(dq), _p(dk), b, S, Hq, H, D, _p(wq), _p(wk), eps,
+                                         _p(inv_freq), R, 1 if interleaved else 0, _p(pos), _p(dqi), so, _p(dki), sp,
+                                         _p(dwq), _p(dwk), _p(workspace), workspace.numel(), _stream(stream)),
+           "kvpop_qk_norm_rope_bwd")
     return dqi, dki, dwq, dwk
 
 
@@ -482,22 +492,32 @@ def prefix_attn(q, pk, pv, cu=None, lens=None, join=None, scale: float = 0.0, wo
     n, Hq, D = rows = q.shape
     m, P, H, _ = pk.shape
     dev = _device(q, "q")
-    keys = (m, P, H, D)
-    aq = _fit(q, torch.bfloat16, dev, rows, "q")
-    ak, av = _fit(pk, torch.bfloat16, dev, keys, "pk"), _fit(pv, torch.bfloat16, dev, keys, "pv")
-    acu, alens = _fit(cu, torch.int32, dev, (m + 1,), "cu"), _fit(lens, torch.int32, dev, (m,), "lens")
-    O2, lse2 = (None, None) if join is None else join
-    aO2, alse2 = _fit(O2, torch.bfloat16, dev, rows, "O2"), _fit(lse2, torch.float32, dev, (n, Hq), "lse2")
+    _fit(q, torch.bfloat16, dev, rows, "q")
+    _fit(pk, torch.bfloat16, dev, (m, P, H, D), "pk")
+    _fit(pv, torch.bfloat16, dev, (m, P, H, D), "pv")
+    if cu is not None:
+        _fit(cu, torch.int32, dev, (m + 1,), "cu")
+    if lens is not None:
+        _fit(lens, torch.int32, dev, (m,), "lens")
+    O2 = lse2 = None
+    if join is not None:
+        O2, lse2 = join
+        _fit(O2, torch.bfloat16, dev, rows, "O2")
+        _fit(lse2, torch.float32, dev, (n, Hq), "lse2")
     with _on(stream):
-        O, lse = out if out is not None else (torch.empty_like(q), torch.empty((n, Hq), dtype=torch.float32, device=q.device))
+        if out is None:
+            O, lse = _empty_as(q), torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+        else:
+            O, lse = out
+            _fit(O, torch.bfloat16, dev, rows, "O")
+            _fit(lse, torch.float32, dev, (n, Hq), "lse")
         if workspace is None:
             workspace = torch.empty(_prefix_workspace(dev, n, m, P, Hq, H, D), dtype=torch.uint8, device=q.device)
-    st = load().kvpop_prefix_attn(aq, ak, av, n, m, P, Hq, H, D, scale, acu, alens, aO2, alse2,
-                                  _fit(O, torch.bfloat16, dev, rows, "O"), _fit(lse, torch.float32, dev, (n, Hq), "lse"),
-                                  _fit(workspace, torch.uint8, dev, workspace.shape, "workspace"), workspace.numel(),
-                                  _stream(stream))
-    if st:
-        _check(st, "kvpop_prefix_attn")
+        else:
+            _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
+    _check(load().kvpop_prefix_attn(_p(q), _p(pk), _p(pv), n, m, P, Hq, H, D, scale, _p(cu), _p(lens), _p(O2),
+                                    _p(lse2), _p(O), _p(lse), _p(workspace), workspace.numel(), _stream(stream)),
+           "kvpop_prefix_attn")
     return O, lse
 
 
