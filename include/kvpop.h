@@ -287,8 +287,8 @@ kvpop_status kvpop_boundary_loss(const float* r_hat, const int32_t* t_bnd, const
  *   dwq, dwk      [D] fp32, nullable: gradients of the weights, summed over all
  *                 tokens and heads in a fixed order (the same bits every run)
  * All overwritten.  dq_in may be q and dk_in k when the strides are equal too.
- * workspace: kvpop_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned,
- * contents undefined between calls.
+ * workspace: kvpop_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned;
+ * contents undefined between calls, so calls that overlap in time need one each.
  * ---------------------------------------------------------------------- */
 kvpop_status kvpop_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int b, int S,
                                 int Hq, int H, int D, const float* wq, const float* wk, float eps,

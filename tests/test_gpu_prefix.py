@@ -188,8 +188,8 @@ def test_in_place_join_and_rows_outside():
 
 
 def test_moving_reference():
-    """Scores whose maximum rises by far more than 2^20 between the tiles of a row, in both
-    streams and for one row among many; and values large enough that a weight of 2^20 counts."""
+    """Scores whose maximum rises steeply between the tiles of a row, in both streams and for
+    one row among many, with values near the end of their range."""
     q, k, v, _ = make([40], 1100, 1, 4, 128, seed=14)
     k *= 0.02
     for t, f in ((140, 3.0), (300, 6.0), (650, 9.0), (900, 12.0)):
