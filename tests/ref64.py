@@ -39,18 +39,23 @@ def norm_rope(x, w, eps, inv_freq, pos=None, interleaved=False):
 
 
 def norm_rope_bwd(x, g, w, eps, inv_freq, pos=None, interleaved=False):
-    """(dx, dw, scale of dx's terms [.., 1], sum of |dw's terms| [D])."""
+    """(dx, dw, scale of dx's terms [.., 1], bound on the fp32 error of dw [D]): 512 * 2^-24
+    of the sum of its terms' magnitudes for the additions, and for the terms themselves, which
+    turn g back and may cancel there, 2^-20 of the row's largest |g| (angles within 2^-22 and
+    three roundings of 2^-24, each relative to |g_a| + |g_b|)."""
     x, g = x.double(), g.double()
     w = torch.ones(x.shape[-1], dtype=torch.float64, device=x.device) if w is None else w.double()
     r = ((x * x).mean(-1, keepdim=True) + eps) ** -0.5
     xh = x * r
+    turned = (g.abs().amax(-1, keepdim=True) * xh.abs()).sum((0, 1, 2))
     if inv_freq is not None:
         cos, sin = angles(_pos(x, pos), inv_freq)
         g = _turn(g, cos, -sin, interleaved)
     e = g * w
     dx = r * (e - xh * (e * xh).mean(-1, keepdim=True))
     size = r * (e.abs().amax(-1, keepdim=True) + xh.abs().amax(-1, keepdim=True) * (e * xh).abs().mean(-1, keepdim=True))
-    return dx, (g * xh).sum((0, 1, 2)), size, (g * xh).abs().sum((0, 1, 2))
+    bound = 512 * 2.0 ** -24 * (g * xh).abs().sum((0, 1, 2)) + 2.0 ** -20 * turned
+    return dx, (g * xh).sum((0, 1, 2)), size, bound
 
 
 def prefix_attn(q, k, v, cu, lens, scale=None, join=None):
