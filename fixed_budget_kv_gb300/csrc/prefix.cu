@@ -216,12 +216,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_constant__ PrefixParams p) {
   using L = Layout<D>;
   constexpr int DH = L::DH, NS = L::NS;
-  extern __shared__ __align__(1024) uint8_t smem[];  // no slack left to align by hand: checked
-  if (smem_u32(smem) & 1023) {
-    grid_dep_wait();
-    if (threadIdx.x == 0) report_error(p.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 50);
-    return;
-  }
+  extern __shared__ __align__(1024) uint8_t smem[];  // no slack left to align by hand: the walker checks
   Bars<NS>* bars = reinterpret_cast<Bars<NS>*>(smem + L::bar_off);
   Seg* segs = reinterpret_cast<Seg*>(smem + L::seg_off);
   float2* ml_s = reinterpret_cast<float2*>(smem + L::ml_off);
@@ -467,6 +462,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         // groups that overlap, which the interface rules out, could pass the host's bound on U: no work
         U = 0;
         if (blockIdx.x == 0 && lane == 0) report_error(p.status, KVPOP_ERR_INVALID_ARG, SITE_PREFIX_PRODUCER, 5);
+      }
+      if (sbase & 1023) {
+        // the tiles would miss their swizzle.  No work either: an early return would leave the
+        // merge whatever the workspace held for this CTA's item
+        U = 0;
+        if (lane == 0) report_error(p.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 50);
       }
       const int C = min((int)gridDim.x, U);
       const Share sh(U, max(C, 1));

@@ -385,3 +385,20 @@ def test_training_step_through_norm_and_sparse_attention():
         rx, rw, size, bound = ref64.norm_rope_bwd(x, g, ww, 1e-6, f)
         assert ((dx.double() - rx).abs() <= 2.0 ** -8 * rx.abs() + 2.0 ** -17 * size).all()
         assert ((dw.double() - rw).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("byte", [0x01, 0x7f, 0xff])
+def test_a_call_without_work_uses_nothing_of_the_workspace(byte):
+    """A refused call gives its CTAs no work by the same path as the kernel's check of its shared
+    memory, which no call can make fail.  Each CTA still says that it shares no item: the merge
+    takes no rows from what the workspace held before."""
+    groups, P, H, G, D = [6, 6], 900, 2, 4, 128
+    q, k, v, j = make(groups, P, H, G, D, seed=15, join=True)
+    k3, v3 = torch.cat([k, k[:1]]), torch.cat([v, v[:1]])
+    ws = torch.full((kvpop.prefix_attn_workspace_size(12, 3, P, H * G, H, D),), byte, dtype=torch.uint8, device="cuda")
+    O, lse = torch.full_like(q, 3.0), torch.full((12, H * G), 3.0, device="cuda")
+    kvpop.prefix_attn(q, k3, v3, i32([0, 11, 1, 12]), i32([P] * 3), j, workspace=ws, out=(O, lse))
+    assert kvpop.device_status(reset=True)[0] == 1
+    assert (O == 3.0).all() and (lse == 3.0).all()
+    got = kvpop.prefix_attn(q, k3, v3, i32([0, 5, 5, 12]), i32([P, 7, 100]), j, workspace=ws)
+    check(*got, q, k3, v3, [0, 5, 5, 12], [P, 7, 100], j)
