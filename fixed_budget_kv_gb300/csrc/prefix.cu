@@ -63,6 +63,7 @@ constexpr int kRegsSoftmax = 216;
 constexpr int kRegsNeeded = (128 * kRegsIo + 256 * kRegsSoftmax + kThreads - 1) / kThreads;
 
 // An item that several CTAs share: rows, and its CTAs c0 .. c1.  nrow = 0: none.
+// CTA 0 is nobody's second: its c1 is -1 when the call is refused, otherwise 0.
 struct __align__(16) Split {
   int seq0, h, nrow, c1;
 };
@@ -458,15 +459,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         U = window(w0, U);
         members = min(members, p.n + 1) + __reduce_add_sync(0xffffffffu, min(g.hi - g.lo, p.n));
       }
+      Split split = {0, 0, 0, 0};
       if (members > p.n) {
         // groups that overlap, which the interface rules out, could pass the host's bound on U: no work
         U = 0;
+        split.c1 = -1;
         if (blockIdx.x == 0 && lane == 0) report_error(p.status, KVPOP_ERR_INVALID_ARG, SITE_PREFIX_PRODUCER, 5);
       }
       if (sbase & 1023) {
         // the tiles would miss their swizzle.  No work either: an early return would leave the
         // merge whatever the workspace held for this CTA's item
         U = 0;
+        split.c1 = -1;
         if (lane == 0) report_error(p.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 50);
       }
       const int C = min((int)gridDim.x, U);
@@ -484,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           if (u < at) break;
         }
       }
-      Split split = {0, 0, 0, 0};
       for (int n = 0;; ++n) {
         Seg s = {0, 0, 0, 0, 0, 0, 0, 0};  // NT = 0 ends the work
         while (u < end && s.NT == 0) {
@@ -796,6 +799,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge(const __grid_const
   grid_dep_launch();
   grid_dep_wait();
   if ((int)blockIdx.y == chunks) {
+    if (p.split[0].c1 < 0) return;  // refused: these rows stay as they were too
     const int c4 = threadIdx.x % (D / 4);
     for (int j = blockIdx.x; j < p.m; j += gridDim.x) {
       const Group g = group_of(p, j);

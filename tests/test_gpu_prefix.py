@@ -402,3 +402,20 @@ def test_a_call_without_work_uses_nothing_of_the_workspace(byte):
     assert (O == 3.0).all() and (lse == 3.0).all()
     got = kvpop.prefix_attn(q, k3, v3, i32([0, 5, 5, 12]), i32([P, 7, 100]), j, workspace=ws)
     check(*got, q, k3, v3, [0, 5, 5, 12], [P, 7, 100], j)
+
+
+def test_overlapping_groups_leave_rows_without_keys_alone():
+    """The refusal of overlapping groups covers the groups of length 0 among them, with and
+    without a join, in place too; the next call is as good as ever."""
+    q, k, v, j = make([5, 5, 4], 150, 1, 2, 64, seed=16, join=True)
+    cu, lens = i32([0, 9, 2, 14]), i32([150, 0, 0])
+    for join in (None, j):
+        O, lse = torch.full_like(q, 3.0), torch.full((14, 2), 3.0, device="cuda")
+        kvpop.prefix_attn(q, k, v, cu, lens, join, out=(O, lse))
+        assert kvpop.device_status(reset=True)[0] == 1
+        assert (O == 3.0).all() and (lse == 3.0).all()
+    O, lse = j[0].clone(), j[1].clone()
+    kvpop.prefix_attn(q, k, v, cu, lens, (O, lse), out=(O, lse))
+    assert kvpop.device_status(reset=True)[0] == 1
+    assert torch.equal(O, j[0]) and torch.equal(lse, j[1])
+    check(*kvpop.prefix_attn(q, k, v, i32([0, 9, 9, 14]), lens, j), q, k, v, [0, 9, 9, 14], [150, 0, 0], j)
