@@ -682,11 +682,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       const int c_lo = two ? 0 : w * (D / 2), c_n = two ? D : D / 2;
       const bool both = !two && s.NT > 1, mine = two || steps > 0;
       float w_j = 0.0f;
+      bool joins = false;
       if (s.whole()) {
         const float T = fmaxf(m2, j2);
         const float w_p = m2 != neg_inf() ? ex2_approx(m2 - T) : 0.0f;
         w_j = j2 != neg_inf() ? ex2_approx(j2 - T) : 0.0f;
         l = l * w_p + w_j;
+        joins = w_j != 0.0f;  // before 1 / l, which may be NaN: o2 need not be there
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         w_own *= w_p * inv;
         w_oth *= w_p * inv;
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             for (int c = 0; c < 32; ++c) v[c] += __uint_as_float(r[c]) * w_oth;
           }
           if (row_on && s.whole()) {
-            if (w_j != 0.0f) {
+            if (joins) {
               const uint4* j = reinterpret_cast<const uint4*>(p.o2 + orow * D + c0);
 #pragma unroll
               for (int u = 0; u < 4; ++u) {

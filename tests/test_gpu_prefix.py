@@ -419,3 +419,27 @@ def test_overlapping_groups_leave_rows_without_keys_alone():
     assert kvpop.device_status(reset=True)[0] == 1
     assert torch.equal(O, j[0]) and torch.equal(lse, j[1])
     check(*kvpop.prefix_attn(q, k, v, i32([0, 9, 9, 14]), lens, j), q, k, v, [0, 9, 9, 14], [150, 0, 0], j)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D,G,groups,P", [(64, 1, [3], 100), (128, 4, [6], 1), (128, 4, [40], 120), (64, 2, [2] * 90, 300),
+                                          (128, 128, [3] * 60, 400)], ids=str)
+def test_nan_rows_without_a_join(D, G, groups, P, bad):
+    """A row that becomes NaN reads nothing where there is nothing to join, whether a CTA has its
+    item alone or shares it: a NaN or an infinity in a query, then in a key.  A single softmax of
+    the same scores says which rows those are."""
+    H, n, m = 2, sum(groups), len(groups)
+    q, k, v, _ = make(groups, P, H, G, D, seed=21 + P)
+    cu = [0] + np.cumsum(groups).tolist()
+    clean = kvpop.prefix_attn(q, k, v, i32(cu))
+    q2, k2 = q.clone(), k.clone()
+    q2[n // 2, G, 5] = bad
+    k2[m // 2, P - 1, 0, 3] = bad
+    rows = torch.zeros(2, n, H * G, dtype=torch.bool, device="cuda")
+    rows[0, n // 2, G] = True
+    rows[1, cu[m // 2]:cu[m // 2 + 1], :G] = True
+    for qq, kk, row in ((q2, k, rows[0]), (q, k2, rows[1])):
+        O, lse = kvpop.prefix_attn(qq, kk, v, i32(cu))
+        assert torch.equal(O[~row], clean[0][~row]) and torch.equal(lse[~row], clean[1][~row])
+        if bad != bad:
+            assert torch.isnan(O[row]).all() and torch.isnan(lse[row]).all()
