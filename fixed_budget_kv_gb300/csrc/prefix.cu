@@ -13,10 +13,10 @@
 // Work split: an item is one (group, 256-row block, KV head), in that order, and has
 // kSetup units of setup and then a unit for each 128-key tile.  CTA c takes the c-th
 // part of all units, one CTA an SM, so that every SM has the same work however ragged
-// the groups and lengths.  A CTA's key tiles fall into segments of one item each.  A segment
-// that covers all key tiles is finished by its CTA; of the others a CTA has at
-// most two (it begins inside one and ends inside another), whose running
-// maximum, sum and unnormalised O go to two slots of the workspace, and
+// the groups and lengths.  A CTA's key tiles fall into segments of one item each, of at most
+// kRunTiles, whose running maximum, sum and unnormalised O are added up in a slot of the
+// workspace.  An item whose key tiles are all a CTA's is finished by it; of the others a CTA
+// has at most two (it begins inside one and ends inside another), in a slot each, and
 // prefix_merge joins the slots of an item in the order of the CTAs.  No atomics:
 // the same call gives the same bits.
 //
@@ -57,6 +57,13 @@ constexpr int kMergeThreads = 256;  // 64 rows a head over 16k keys: 33.6 us, wi
 // ragged groups took 61 us with 0, 46 with 1, 41 with 2, 33 with 4, 34 with 6.
 constexpr int kSetup = 4;
 constexpr int kSegs = 4;  // segments between the walker and the last reader
+// Key tiles of a segment at most.  The tensor core truncates what it adds to an accumulator, so a
+// long sum loses part of itself: O of 2^17 / 2^20 / 2^24 keys in one run came out 4e-4 / 6e-3 /
+// 1e-1 too small.  Runs of 2^15 keys (1e-4) are added up outside of it, in fp32 with rounding,
+// for 2-3% of a long item's time (2^20 keys, 256 rows a CTA, D = 64 / 128: 13.1 / 14.6 ms against
+// 12.8 / 14.2 in one run; runs of 2^14 13.2 / 14.8, of 2^16 13.05 / 14.5).  It also keeps the
+// waits that last a segment (query tiles, the walker) far below their limit.
+constexpr int kRunTiles = 256;
 // Register split: warps 0-3 drop to kRegsIo, the softmax warpgroups rise to kRegsSoftmax.
 constexpr int kRegsIo = 64;
 constexpr int kRegsSoftmax = 216;
@@ -127,10 +134,12 @@ struct __align__(16) Seg {
   int kt0, NT, len, flags;
   // two row tiles, one a stream; otherwise one, its key tiles alternating
   __device__ __forceinline__ bool two() const { return flags & 1; }
-  // all key tiles of the block
+  // the last of the block's key tiles, and this CTA had all the others
   __device__ __forceinline__ bool whole() const { return flags & 2; }
   // otherwise: 0 when an earlier CTA began the block, 1 when this one did
-  __device__ __forceinline__ int slot() const { return flags >> 2; }
+  __device__ __forceinline__ int slot() const { return flags >> 2 & 1; }
+  // this CTA had the key tiles before these: their result is in the slot
+  __device__ __forceinline__ bool cont() const { return flags & 8; }
 };
 
 // The MMA wrappers for a whole warp: one elected lane issues.
@@ -488,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           if (u < at) break;
         }
       }
+      bool own = false;  // this CTA began the item that u is in
       for (int n = 0;; ++n) {
         Seg s = {0, 0, 0, 0, 0, 0, 0, 0};  // NT = 0 ends the work
         while (u < end && s.NT == 0) {
@@ -502,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     hi = __shfl_sync(0xffffffffu, g.hi, l), nt = __shfl_sync(0xffffffffu, g.nt, l);
           s.len = __shfl_sync(0xffffffffu, g.len, l);
           const int per = nt + kSetup, item = (u - b) / per, off = (u - b) - item * per;
-          const int stop = min(per, off + (end - u));  // this CTA's units of the item: [off, stop)
+          // this CTA's units of the item from here on, up to a run of key tiles: [off, stop)
+          const int stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
           s.kt0 = max(off - kSetup, 0);
           s.NT = max(stop - kSetup, 0) - s.kt0;
           const int rb = item / p.H;
@@ -510,7 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
           s.h = item - rb * p.H;
           s.seq0 = lo + rb * p.seqs;
           s.nrow = min(p.seqs, hi - s.seq0) * p.G;
-          s.flags = (s.nrow > 128 ? 1 : 0) | (s.NT == nt ? 2 : 0) | (s.kt0 == 0 ? 4 : 0);
+          const bool cont = s.kt0 > 0 && n > 0;
+          own = s.kt0 == 0 || (cont && own);
+          s.flags = (s.nrow > 128 ? 1 : 0) | (own && stop == per ? 2 : 0) | (own ? 4 : 0) | (cont ? 8 : 0);
           if (n == 0 && s.kt0 > 0) {
             // the work begins inside an item; the second of its CTAs leaves word of it
             const int first = b + item * per + kSetup;
@@ -542,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const uint64_t s2 = pack2(sl2, sl2);
     uint32_t cnt = 0, par = 0, nml = 0;
     int sb = 0;
+    float m_run = neg_inf(), l_run = 0.0f;  // of the key tiles in the slot
     bool ok = true;
     for (int n = 0; ok; ++n) {
       if (!warp_wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1, abort_flag)) {
@@ -681,7 +695,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
       // a single-tile segment's columns are shared out between the two streams
       const int c_lo = two ? 0 : w * (D / 2), c_n = two ? D : D / 2;
       const bool both = !two && s.NT > 1, mine = two || steps > 0;
-      float w_j = 0.0f;
+      float w_run = 0.0f, w_j = 0.0f;
+      if (s.cont()) {
+        const float M = fmaxf(m_run, m2);
+        const float f = m2 != neg_inf() ? ex2_approx(m2 - M) : 0.0f;
+        w_run = m_run != neg_inf() ? ex2_approx(m_run - M) : 0.0f;
+        w_own *= f;
+        w_oth *= f;
+        l = l * f + l_run * w_run;
+        m2 = M;
+      }
+      m_run = m2;
+      l_run = l;
+      const bool adds = w_run != 0.0f;
       bool joins = false;
       if (s.whole()) {
         const float T = fmaxf(m2, j2);
@@ -692,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         w_own *= w_p * inv;
         w_oth *= w_p * inv;
+        w_run *= w_p * inv;
         w_j *= inv;
         m2 = T;
       }
@@ -711,6 +738,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             tmem_wait_ld_dep(r);
 #pragma unroll
             for (int c = 0; c < 32; ++c) v[c] += __uint_as_float(r[c]) * w_oth;
+          }
+          if (row_on && adds) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const float4 y = po[(size_t)(c0 / 4 + u) * 128];
+              v[4 * u] += w_run * y.x;
+              v[4 * u + 1] += w_run * y.y;
+              v[4 * u + 2] += w_run * y.z;
+              v[4 * u + 3] += w_run * y.w;
+            }
           }
           if (row_on && s.whole()) {
             if (joins) {

@@ -384,7 +384,9 @@ kvpop_status kvpop_cache_position(const kvpop_cache* cache, int32_t* q_next);
  *          no other overlap
  * scale <= 0 selects 1/sqrt(D).  D 64 or 128, G dividing 128, H, Hq and m up to
  * 65535, n up to 2^24, P up to 2^30, tensors 16-byte aligned.  bf16 operands (the softmax
- * weights rounded to bf16 before their product with V), fp32 accumulation.
+ * weights rounded to bf16 before their product with V), fp32 accumulation: in the tensor
+ * core over up to 2^15 keys, beyond that with rounding, so that the error of O does not
+ * grow with the length.
  * workspace: kvpop_prefix_attn_workspace_size() bytes, 256-byte aligned; contents
  * undefined between calls, so calls that overlap in time need one each.
  * Errors: INVALID_ARG, UNSUPPORTED (D, G, sizes, alignment), CUDA.

@@ -443,3 +443,103 @@ def test_nan_rows_without_a_join(D, G, groups, P, bad):
         assert torch.equal(O[~row], clean[0][~row]) and torch.equal(lse[~row], clean[1][~row])
         if bad != bad:
             assert torch.isnan(O[row]).all() and torch.isnan(lse[row]).all()
+
+
+def long_segments(P):
+    """As many row blocks as SMs over a prefix of P keys, then a group of short ones: every CTA
+    has about P keys of an item or two, and the last CTA many items after them.  All keys but the
+    last of the long prefix score 0 and have values of 1, so the result is known: LSE within 2^-20
+    of the terms' size as elsewhere and 2^-16 for the sum over the runs of keys, O within half a
+    bf16 step and 2^-9 (see test_long_sums) of 1."""
+    blocks, short, G, D = torch.cuda.get_device_properties(0).multi_processor_count, 40, 128, 64
+    n, at = 2 * (blocks + short), 2 * blocks
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    q = torch.randn(n, G, D, generator=gen, device="cuda").bfloat16()
+    kl, vl = (torch.randn(2, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.empty(2, P, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[0], v[0] = 0, 1
+    k[0, -1, 0], v[0, -1, 0], k[1, 0, 0], v[1, 0, 0] = kl[0], vl[0], kl[1], vl[1]
+    O, lse = kvpop.prefix_attn(q, k, v, i32([0, at, n]), i32([P, 1]))
+    assert kvpop.device_status(reset=False)[0] == 0
+    s = torch.einsum("igd,jd->jig", q.double(), kl.double()) / math.sqrt(D)
+    z = torch.logaddexp(s[0, :at], torch.tensor(math.log(P - 1), dtype=torch.float64, device="cuda"))
+    last = torch.exp(s[0, :at] - z)[..., None]
+    o = 1 - last + last * vl[0].double()
+    mass = 1 - last + last * vl[0].double().abs()
+    assert ((lse[:at].double() - z).abs() <= 2.0 ** -16 + 2.0 ** -20 * z.abs()).all()
+    assert ((O[:at].double() - o).abs() <= 2.0 ** -8 * o.abs() + (2.0 ** -9 + 2.0 ** -8 * last) * mass).all()
+    assert ((lse[at:].double() - s[1, at:]).abs() <= 2.0 ** -16 + 2.0 ** -20 * s[1, at:].abs()).all()
+    assert torch.equal(O[at:], vl[1].expand(n - at, G, D))
+
+
+def test_a_prefix_that_takes_longer_than_the_wait_limit():
+    """A wait gives up after 2 s, and two of the waits last a segment: at 1.6 us a key tile of 256
+    rows at D = 64 this prefix takes a CTA 2.5 s, in many segments (103 GB of keys and values)."""
+    torch.cuda.empty_cache()
+    long_segments(200_000_001)
+    torch.cuda.empty_cache()
+
+
+def test_short_groups_after_a_long_one():
+    long_segments(100_001)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_sums(D):
+    """Millions of equal weights in one CTA: the softmax weights are exactly 1, so O is the mean
+    of the values, within half a bf16 step (2^-8) and what a sum of 2^15 products may lose where
+    every one is cut off to the accumulator's 24 bits: 2^15 x 2^-23 of the sum so far, 2^-9 of
+    the whole one.  (A single run of all keys came out 2.4% too small.)"""
+    P, G, blocks = (1 << 22) + 37, 128, torch.cuda.get_device_properties(0).multi_processor_count + 1
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    q = torch.randn(2 * blocks, G, D, generator=gen, device="cuda").bfloat16()
+    k, v = (torch.empty(1, P, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k.zero_()
+    mean = torch.zeros(D, dtype=torch.float64, device="cuda")
+    for i in range(0, P, 1 << 18):
+        part = v[0, i:i + (1 << 18), 0]
+        part.copy_((0.5 + torch.rand(part.shape, generator=gen, device="cuda")) * (1 + torch.arange(D, device="cuda") / D))
+        mean += part.double().sum(0) / P
+    O, lse = kvpop.prefix_attn(q, k, v)
+    assert ((O.double() - mean).abs() <= (2.0 ** -8 + 2.0 ** -9) * mean).all(), float(((O.double() - mean) / mean).abs().max())
+    assert ((lse.double() - math.log(P)).abs() <= 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("G,H,n,join", [(128, 1, 306, True), (128, 1, 306, False), (4, 160, 9, True), (32, 160, 3, False)],
+                         ids=str)
+def test_items_of_several_runs(G, H, n, join):
+    """More items than SMs and a prefix of several runs of key tiles, with one row tile and with
+    two: scores that fall, rise and fall again along the keys, so that the first, a middle or the
+    last run of an item carries most of the weight; joined in place; the same bits again."""
+    P, D = 70001, 64
+    gen = torch.Generator(device="cuda").manual_seed(19 + G)
+    q = torch.randn(n, H * G, D, generator=gen, device="cuda").bfloat16()
+    k, v = (torch.randn(1, P, H, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    for i, (a, b) in enumerate(((100, 1100), (40000, 41000), (69000, 70001))):
+        k[0, a:b] += 0.6 * q[2 * i % n, ::G][None, :, :]
+    j = ((torch.randn(n, H * G, D, generator=gen, device="cuda") * 0.1).bfloat16(),
+         torch.randn(n, H * G, generator=gen, device="cuda") + 10) if join else None
+    ref = kvpop.prefix_attn(q, k, v, join=j)
+    for lo in (0, n - 3):
+        rows = slice(lo, lo + 3)
+        jj = (j[0][rows], j[1][rows]) if join else None
+        check(ref[0][rows], ref[1][rows], q[rows], k, v, [0, 3], [P], jj)
+    out = (j[0].clone(), j[1].clone()) if join else (torch.empty_like(ref[0]), torch.empty_like(ref[1]))
+    kvpop.prefix_attn(q, k, v, join=out if join else None, out=out)
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+
+
+def test_nan_in_one_run_of_keys():
+    """A NaN among the keys of one run makes the rows of its head NaN, as in a single softmax."""
+    H, n, P, D = 160, 3, 70000, 64
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    q = torch.randn(n, H, D, generator=gen, device="cuda").bfloat16()
+    k, v = (torch.randn(1, P, H, D, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    clean = kvpop.prefix_attn(q, k, v)
+    for h, t in ((3, 5), (77, 40000), (159, P - 1)):
+        k[0, t, h, 1] = float("nan")
+    O, lse = kvpop.prefix_attn(q, k, v)
+    bad = torch.zeros(H, dtype=torch.bool, device="cuda")
+    bad[[3, 77, 159]] = True
+    assert torch.isnan(O[:, bad]).all() and torch.isnan(lse[:, bad]).all()
+    assert torch.equal(O[:, ~bad], clean[0][:, ~bad]) and torch.equal(lse[:, ~bad], clean[1][:, ~bad])
