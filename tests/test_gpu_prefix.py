@@ -543,3 +543,51 @@ def test_nan_in_one_run_of_keys():
     bad[[3, 77, 159]] = True
     assert torch.isnan(O[:, bad]).all() and torch.isnan(lse[:, bad]).all()
     assert torch.equal(O[:, ~bad], clean[0][:, ~bad]) and torch.equal(lse[:, ~bad], clean[1][:, ~bad])
+
+
+@pytest.mark.parametrize("D,H,G,m,top", [(128, 8, 4, 3, 300), (64, 3, 1, 40, 9), (128, 1, 2, 256, 3), (64, 1, 4, 700, 2),
+                                         (128, 5, 1, 257, 1), (64, 1, 128, 5, 7)], ids=str)
+def test_rows_without_keys(D, H, G, m, top):
+    """Groups of length 0 of all sizes, by themselves and between groups with keys, over several
+    windows of groups, joined in place and not; rows outside the groups stay as they were."""
+    rng = np.random.default_rng(m)
+    for keys in (0.0, 0.3):
+        groups = rng.integers(0, top + 1, m)
+        groups[m // 2] = top
+        lens = np.where(rng.random(m) < keys, 33, 0)
+        n = int(groups.sum()) + 5
+        cu = (2 + np.concatenate([[0], np.cumsum(groups)])).tolist()
+        q, k, v, j = make([n] + [0] * (m - 1), 40, H, G, D, seed=m, join=True)
+        j[1][::7] = -math.inf
+        j[0][::14] = float("nan")
+        for join in (j, None):
+            O, lse = torch.full_like(q, 3.0), torch.full((n, H * G), 3.0, device="cuda")
+            kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), join, out=(O, lse))
+            check(O, lse, q, k, v, cu, lens.tolist(), join, rows=slice(2, n - 3))
+            for t in (O, lse):
+                assert (t[:2] == 3.0).all() and (t[n - 3:] == 3.0).all()
+            if join:
+                O2, l2 = j[0].clone(), j[1].clone()
+                kvpop.prefix_attn(q, k, v, i32(cu), i32(lens), (O2, l2), out=(O2, l2))
+                assert torch.equal(O2[2:n - 3], O[2:n - 3]) and torch.equal(l2[2:n - 3], lse[2:n - 3])
+
+
+def test_many_rows_without_keys_take_no_longer_than_with_keys():
+    """512 sequences without a prefix beside some with one, joined: at most four times the time
+    of the same rows with 128 keys (as long as it; one CTA for all of a group took 39 times)."""
+    q, k, v, j = make([512, 8], 200, 8, 4, 128, seed=23, join=True)
+    cu = i32([0, 512, 520])
+
+    def best(lens):
+        out = (torch.empty_like(q), torch.empty(520, 32, device="cuda"))
+        times = []
+        for _ in range(10):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(5):
+                kvpop.prefix_attn(q, k, v, cu, lens, j, out=out)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+    assert best(i32([0, 200])) <= 4 * best(i32([128, 200]))
