@@ -21,8 +21,11 @@
 //
 // Angles: f / 2 pi becomes a 64-bit fixed-point fraction of a turn, so the
 // product with an integer position wraps at whole turns without any loss; the
-// top 32 bits, as a signed number, go to sincospif.  The fraction is off by at
-// most 1 + f units of 2^-64, which leaves 2^-30 rad at position 2^31 (f <= 1).
+// top 32 bits, as a signed number, go to sincospif.  The fraction is off by less
+// than 2 units of 2^-64 for any finite f, 2^-32 of a turn at position 2^31, and
+// as much again goes with the low half: 2^-28 rad.  What counts is the conversion
+// of the top half to fp32, at most 2^-25 of a half turn or 2^-23 rad, and
+// sincospif's own rounding: 2^-22 rad in all.
 #include "common.cuh"
 
 namespace kvpop {
@@ -124,18 +127,28 @@ __device__ __forceinline__ void stage_weights(float4* dst, const float* w, int n
   }
 }
 
-// Turns per position as a fraction of 2^64, whole turns dropped: the 24-bit
-// significand times 2^64 / 2 pi, moved to the exponent's place.
+// Turns per position as a fraction of 2^64, whole turns dropped: the 24-bit significand times
+// 1 / 2 pi, moved to the exponent's place (the reduction of Payne and Hanek, 1983).  A large
+// exponent moves leading bits of 1 / 2 pi out as whole turns: 256 bits leave 128 for the largest.
 __device__ __forceinline__ unsigned long long turns64(float f) {
+  const unsigned long long c0 = 0x28be60db9391054aull, c1 = 0x7f09d5f47d4d3770ull, c2 = 0x36d8a5664f10e410ull,
+                           c3 = 0x7f9458eaf7aef158ull;  // 2^256 / (2 pi)
   const uint32_t u = __float_as_uint(f);
   const int exp = (int)(u >> 23 & 255), sh = 150 - exp;  // |f| = sig 2^-sh
   const unsigned long long sig = exp ? (u & 0x7fffffu) | 0x800000u : 0ull;
-  const unsigned long long c = 0x28be60db9391054aull;  // 2^64 / (2 pi)
-  const unsigned long long lo = sig * c, hi = __umul64hi(sig, c);
-  unsigned long long r;
-  if (sh <= 0) r = sh > -64 ? lo << -sh : 0ull;
-  else if (sh < 64) r = lo >> sh | hi << (64 - sh);
-  else r = sh < 128 ? hi >> (sh - 64) : 0ull;
+  unsigned long long hi = c0, lo = c1, r;
+  if (sh < 0) {
+    const bool w = sh <= -64;
+    const int up = -sh & 63;
+    const unsigned long long a = w ? c1 : c0, b = w ? c2 : c1, d = w ? c3 : c2;
+    hi = up ? a << up | b >> (64 - up) : a;
+    lo = up ? b << up | d >> (64 - up) : b;
+  }
+  const unsigned long long carry = __umul64hi(sig, lo), p0 = sig * hi + carry;
+  const unsigned long long p1 = __umul64hi(sig, hi) + (p0 < carry);
+  if (sh <= 0) r = p0;
+  else if (sh < 64) r = p0 >> sh | p1 << (64 - sh);
+  else r = sh < 128 ? p1 >> (sh - 64) : 0ull;
   return u >> 31 ? 0ull - r : r;
 }
 

@@ -248,3 +248,51 @@ def test_gradients_in_place(packed):
                                  out=(q, k, torch.empty_like(wq), torch.empty_like(wk)))
     for a, r in zip(got, ref):
         assert torch.equal(a, r)
+
+
+def exact_angles(pos, inv_freq):
+    """cos, sin [b, S, 1, R/2] of position times frequency, the product and its whole turns in
+    integers: the frequency is a 24-bit integer times a power of two, 1 / 2 pi has 480 bits."""
+    N = 480
+
+    def arctan_inv(x):  # of 1/x, times 2^600
+        s = t = (1 << 600) // x
+        k, sign = 1, -1
+        while t:
+            t //= x * x
+            k += 2
+            s += sign * (t // k)
+            sign = -sign
+        return s
+    inv_turn = (1 << (N + 600)) // (8 * (4 * arctan_inv(5) - arctan_inv(239)))  # Machin's formula for pi / 4
+    turns = []
+    for t in pos.flatten().tolist():
+        for f in inv_freq.tolist():
+            num, den = f.as_integer_ratio()
+            x = t * num * inv_turn // den & ((1 << N) - 1)
+            turns.append(x / (1 << N) if x >> (N - 1) == 0 else -((1 << N) - x) / (1 << N))
+    a = 2 * torch.pi * torch.tensor(turns, dtype=torch.float64, device="cuda").view(*pos.shape, 1, -1)
+    return a.cos(), a.sin()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("inter", [False, True])
+def test_any_finite_frequency(D, inter):
+    """Frequencies over the whole range of fp32, at positions to the ends of int32."""
+    f = torch.tensor([1.0, -0.7, 6.25, 1000.5, 2.0 ** 20, 3.1e9, 2.0 ** 40 + 2.0 ** 20, 2.0 ** 63, 1e20, 1.7e28, 3.3e38,
+                      -3.4028234663852886e38, 1e-20, 1e-44, 0.0, 2.0 ** 24 + 2], dtype=torch.float32, device="cuda")
+    pos = torch.tensor([[0, 1, -1, 2, 2147483647, -2147483648, 123456789, 40000, 1 << 30]], dtype=torch.int32, device="cuda")
+    q, k, wq, wk, gq, gk = make(1, 9, 6, 3, D, seed=30)
+    cos, sin = exact_angles(pos, f)
+    qo, ko = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f, pos, inter)
+    dq, dk, dwq, dwk = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f, pos, inter)
+    for x, w, z, g, dx, dw in ((q, wq, qo, gq, dq, dwq), (k, wk, ko, gk, dk, dwk)):
+        y = ref64.norm_rope(x, w, EPS, None)[1]
+        want = ref64._turn(y, cos, sin, inter)
+        assert ((z.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -17 * y.abs().amax(-1, keepdim=True)).all()
+        back = ref64._turn(g.double(), cos, -sin, inter)
+        rx, rw, size, bound = ref64.norm_rope_bwd(x, back, w, EPS, None)
+        turned = (g.double().abs().amax(-1, keepdim=True) * x.double().abs() /
+                  ((x.double() ** 2).mean(-1, keepdim=True) + EPS).sqrt()).sum((0, 1, 2))
+        assert ((dx.double() - rx).abs() <= 2.0 ** -8 * rx.abs() + 2.0 ** -17 * size).all()
+        assert ((dw.double() - rw).abs() <= bound + 2.0 ** -20 * turned).all()
