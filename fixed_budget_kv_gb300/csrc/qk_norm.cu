@@ -115,15 +115,24 @@ __device__ __forceinline__ void lds8(const float4* s, int j, uint64_t (&x)[4]) {
   x[3] = pack2(v.z, v.w);
 }
 
-// Weights in that order: rows 0, 1 for piece a of each lane, 2, 3 for piece b.
+// 0, or NaN for a column that turns by a frequency that is not finite (whose angle is a NaN).
+template <bool INTER>
+__device__ __forceinline__ float no_angle(const float* inv_freq, int nrot, int col) {
+  if (col >= 16 * nrot) return 0.0f;
+  return fabsf(inv_freq[INTER ? col / 2 : col < 8 * nrot ? col : col - 8 * nrot]) * 0.0f;
+}
+
+// Weights in that order: rows 0, 1 for piece a of each lane, 2, 3 for piece b.  A column
+// without an angle gets a NaN, which reaches both members of its pair.
 template <int D, bool INTER>
-__device__ __forceinline__ void stage_weights(float4* dst, const float* w, int nrot, int thread, int threads) {
+__device__ __forceinline__ void stage_weights(float4* dst, const float* w, const float* inv_freq, int nrot, int thread,
+                                              int threads) {
   constexpr int LPR = D / 16;
-  for (int i = thread; i < 4 * LPR; i += threads) {
+  for (int i = thread; i < 16 * LPR; i += threads) {
     int a, b;
-    pieces<INTER>(i % LPR, nrot, a, b);
-    const int col = 8 * (i < 2 * LPR ? a : b) + 4 * (i / LPR & 1);
-    dst[i] = w ? make_float4(w[col], w[col + 1], w[col + 2], w[col + 3]) : make_float4(1.f, 1.f, 1.f, 1.f);
+    pieces<INTER>(i / 4 % LPR, nrot, a, b);
+    const int col = 8 * (i < 8 * LPR ? a : b) + 4 * (i / 4 / LPR & 1) + (i & 3);
+    reinterpret_cast<float*>(dst)[i] = (w ? w[col] : 1.0f) + no_angle<INTER>(inv_freq, nrot, col);
   }
 }
 
@@ -274,8 +283,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) qk_norm_fwd(const QkP
   r0[0] = r0[1] = r1[0] = r1[1] = make_uint4(0, 0, 0, 0);
   load(r0[0], r0[1]);
   load(r1[0], r1[1]);
-  stage_weights<D, INTER>(w_s, p.wq, p.nrot, threadIdx.x, kWarps * 32);
-  stage_weights<D, INTER>(w_s + 4 * LPR, p.wk, p.nrot, threadIdx.x, kWarps * 32);
+  stage_weights<D, INTER>(w_s, p.wq, p.inv_freq, p.nrot, threadIdx.x, kWarps * 32);
+  stage_weights<D, INTER>(w_s + 4 * LPR, p.wk, p.inv_freq, p.nrot, threadIdx.x, kWarps * 32);
   Angles<LPR> ang;
   if (p.nrot) ang.init(ang_s[warp_id()], p.inv_freq, j, rg, p.nrot);
   __syncthreads();
@@ -356,7 +365,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
   cur.step = ctas * kBwdWarps;
   cur.enter(slices, passes);
   uint64_t da[4] = {}, db[4] = {};
-  stage_weights<D, INTER>(w_s, w, p.nrot, threadIdx.x, kBwdWarps * 32);
+  stage_weights<D, INTER>(w_s, w, p.inv_freq, p.nrot, threadIdx.x, kBwdWarps * 32);
   Angles<LPR> ang;
   if (p.nrot) ang.init(ang_s[warp], p.inv_freq, j, rg, p.nrot);
   __syncthreads();
@@ -445,7 +454,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, kBwdCtasPerSm) qk_norm_bwd(con
   for (int i = threadIdx.x; i < D; i += kBwdWarps * 32) {
     float v = 0.f;
     for (int u = 0; u < kBwdWarps; ++u) v += red[u][i];
-    p.part[(size_t)blockIdx.x * D + i] = v;
+    p.part[(size_t)blockIdx.x * D + i] = v + no_angle<INTER>(p.inv_freq, p.nrot, i);
   }
 }
 

@@ -268,8 +268,8 @@ kvpop_status kvpop_boundary_loss(const float* r_hat, const int32_t* t_bnd, const
  *            q_stride elements apart (Hq * D, or the packed projection's width);
  *            likewise k [b, S, H, D] with k_stride
  *   wq, wk   [D] fp32, nullable (all 1)
- *   inv_freq [R/2] fp32, finite; angles are taken from its exact values at any int32
- *            position
+ *   inv_freq [R/2] fp32; angles are taken from its exact values at any int32 position.
+ *            One that is not finite makes its pair NaN, at position 0 too
  *   pos      [b, S] int32, nullable: the position of token s is s
  *   q_out    [b, S, Hq, D], k_out [b, S, H, D] bf16, contiguous.  q_out may be q
  *            (and k_out k) when the strides are equal too; no other overlap.

@@ -296,3 +296,29 @@ def test_any_finite_frequency(D, inter):
                   ((x.double() ** 2).mean(-1, keepdim=True) + EPS).sqrt()).sum((0, 1, 2))
         assert ((dx.double() - rx).abs() <= 2.0 ** -8 * rx.abs() + 2.0 ** -17 * size).all()
         assert ((dw.double() - rw).abs() <= bound + 2.0 ** -20 * turned).all()
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("D,inter", [(64, False), (64, True), (128, False), (128, True)])
+def test_frequencies_that_are_not_finite(D, inter, weights):
+    """Their pairs come out NaN and the others as ever; backward every dx of a token is NaN, as
+    the mean over the row is, and the weight gradients of the pairs alone."""
+    q, k, wq, wk, gq, gk = make(2, 30, 5, 2, D, seed=31)
+    if not weights:
+        wq = wk = None
+    f = freqs(48)
+    clean = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f, None, inter)
+    cdw = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, f, None, inter)[2:]
+    g = f.clone()
+    pair = torch.tensor([0, 7, 8, 23], device="cuda")
+    g[pair] = torch.tensor([float("nan"), float("inf"), -float("inf"), float("nan")], device="cuda")
+    off = torch.cat([2 * pair, 2 * pair + 1] if inter else [pair, pair + 24])
+    keep = torch.ones(D, dtype=torch.bool, device="cuda")
+    keep[off] = False
+    got = kvpop.qk_norm_rope(q, k, wq, wk, EPS, g, None, inter)
+    out = kvpop.qk_norm_rope_bwd(q, k, gq, gk, wq, wk, EPS, g, None, inter)
+    for z, c in zip(got, clean):
+        assert torch.isnan(z[..., off]).all() and torch.equal(z[..., keep], c[..., keep])
+    assert all(torch.isnan(dx).all() for dx in out[:2])
+    for dw, c in zip(out[2:], cdw):
+        assert torch.isnan(dw[off]).all() and torch.equal(dw[keep], c[keep])
