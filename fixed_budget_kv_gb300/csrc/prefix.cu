@@ -1015,6 +1015,11 @@ extern "C" kvpop_status kvpop_prefix_attn_workspace_size(int n, int m, int P, in
     set_last_error("kvpop_prefix_attn_workspace_size: D=%d (64 or 128), G=%d (dividing 128) unsupported", D, Hq / H);
     return KVPOP_ERR_UNSUPPORTED;
   }
+  // these first: they keep max_units within 64 bits
+  if (H > 65535 || Hq > 65535 || m > 65535 || n > (1 << 24) || (long long)n * Hq > 0x7fffffffll) {
+    set_last_error("kvpop_prefix_attn: at most 65535 heads and prefixes, 2^24 sequences and 2^31 - 1 rows");
+    return KVPOP_ERR_UNSUPPORTED;
+  }
   if (P > (1 << 30) || max_units(n, m, P, H, Hq / H) > 0x7fffffffll) {
     set_last_error("kvpop_prefix_attn_workspace_size: more than 2^30 keys or 2^31 - 1 tiles of rows and keys");
     return KVPOP_ERR_UNSUPPORTED;
@@ -1052,10 +1057,6 @@ extern "C" kvpop_status kvpop_prefix_attn(const void* q, const void* pk, const v
                        reinterpret_cast<uintptr_t>(O2);
   if ((am & 15) || (reinterpret_cast<uintptr_t>(workspace) & 255)) {
     set_last_error("kvpop_prefix_attn: q, pk, pv, O, O2 must be 16-byte, workspace 256-byte aligned");
-    return KVPOP_ERR_UNSUPPORTED;
-  }
-  if (H > 65535 || Hq > 65535 || m > 65535 || n > (1 << 24) || (long long)n * Hq > 0x7fffffffll) {
-    set_last_error("kvpop_prefix_attn: at most 65535 heads and prefixes, 2^24 sequences and 2^31 - 1 rows");
     return KVPOP_ERR_UNSUPPORTED;
   }
   const int G = Hq / H;

@@ -145,3 +145,14 @@ def test_prefix_form_against_one_softmax():
             assert torch.allclose(O[i, hq], p @ v[0, :, hq // 2], atol=1e-12)
             assert math.isclose(float(lse[i, hq]), float(torch.logsumexp(s, 0)), abs_tol=1e-12)
     assert (mass >= O.abs() - 1e-12).all()
+
+
+@pytest.mark.parametrize("n,m,L,H,G", [((1 << 31) - 1, 1, 1 << 30, 1 << 23, 128), (1914826685, 1950157578, 469102189, 19575053, 64),
+                                       (4, (1 << 31) - 1, 1 << 30, (1 << 31) - 1, 1), ((1 << 24) + 1, 1, 1, 1, 1),
+                                       (1, 65536, 1, 1, 1), (1, 1, 1, 65536, 1), (1, 1, 1, 1024, 64), (1 << 24, 1, 1, 2, 64)],
+                         ids=str)
+def test_prefix_workspace_of_refused_sizes(lib, n, m, L, H, G):
+    """What the attention refuses has no workspace either, however large the sizes' products."""
+    nb = ctypes.c_size_t(7)
+    assert lib.kvpop_prefix_attn_workspace_size(n, m, L, H * G, H, 64, ctypes.byref(nb)) == 2
+    assert nb.value == 7 and lib.kvpop_last_error()
