@@ -322,3 +322,25 @@ def test_frequencies_that_are_not_finite(D, inter, weights):
     assert all(torch.isnan(dx).all() for dx in out[:2])
     for dw, c in zip(out[2:], cdw):
         assert torch.isnan(dw[off]).all() and torch.equal(dw[keep], c[keep])
+
+
+def test_calls_go_to_the_current_stream():
+    """Without a stream a call goes to torch's current one, read through calls of torch's binding
+    that are not public: they have to say what the public one says, and work queued before a call
+    on that stream has to come before it."""
+    q, k, wq, wk, _, _ = make(1, 400, 8, 2, 128, seed=32)
+    f = freqs(128)
+    want = kvpop.qk_norm_rope(q, k, wq, wk, EPS, f)
+    side = torch.cuda.Stream()
+    assert kvpop._stream() == torch.cuda.current_stream().cuda_stream
+    src, late = q.clone(), torch.zeros_like(q)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        assert kvpop._stream() == side.cuda_stream == torch.cuda.current_stream().cuda_stream
+        torch.cuda._sleep(20_000_000)
+        late.copy_(src)
+        got = kvpop.qk_norm_rope(late, k, wq, wk, EPS, f)
+    assert kvpop._stream() == torch.cuda.current_stream().cuda_stream != side.cuda_stream
+    assert kvpop._stream(side) == side.cuda_stream
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
