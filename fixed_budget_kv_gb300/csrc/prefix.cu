@@ -32,12 +32,14 @@
 // and every other key tile, and joins the two in the epilogue.  S = Q K^T lands in
 // TMEM (fp32), becomes bf16 P in place, and O += P V reads P from TMEM.  Running
 // maxima are moved lazily, when they grow by more than 2^8 (the weights' precision does
-// not depend on their size).  P is rounded to bf16 for its product; its row sum is not.
+// not depend on their size).  P is rounded to bf16 for its product, as the tensor core wants the
+// type of V: each weight by up to 2^-8 of itself, independently, which leaves O off by about
+// 1.3e-3 of its size beside the 1.7e-3 of its own rounding.  The row sum is not rounded.
 //
 // Measured (8 KV heads, G = 4, D = 128, one GB300, calls in a chain): 16 rows a head
-// over 131 072 keys 93.8 us, 84% of the copy rate (the kernel alone about 94%; the start
-// and the merge cost about 10 us); 64 over 16 384 keys 29.3 us; 2 x 256 over 8192 keys
-// 75.8 us, 894 TFLOP/s, bound by the hand-overs S -> softmax -> P V of the two streams.
+// over 131 072 keys 94 us, 84% of the copy rate (the kernel alone 91-93%, 85-87 us under ncu;
+// the merge the rest); 64 over 16 384 keys 29.4 us; 2 x 256 over 8192 keys
+// 75 us, 900 TFLOP/s, bound by the hand-overs S -> softmax -> P V of the two streams.
 #include <string.h>
 
 #include <atomic>
@@ -52,9 +54,10 @@ constexpr int kKeys = 128;
 constexpr int kBlockRows = 256;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kMergeThreads = 256;  // 64 rows a head over 16k keys: 33.6 us, with 512 36.8
-// Time between the last tile of a segment and the first of the next, in key tiles: eight
-// ragged groups took 61 us with 0, 46 with 1, 41 with 2, 33 with 4, 34 with 6.
+// When chosen, 64 rows a head over 16k keys took 33.6 us with 256 and 36.8 with 512 (29.4 now).
+constexpr int kMergeThreads = 256;
+// Time between the last tile of a segment and the first of the next, in key tiles: when chosen, eight
+// ragged groups took 61 us with 0, 46 with 1, 41 with 2, 33 with 4, 34 with 6 (29.4 now, with 4).
 constexpr int kSetup = 4;
 constexpr int kSegs = 4;  // segments between the walker and the last reader
 // Key tiles of a segment at most.  The tensor core truncates what it adds to an accumulator, so a

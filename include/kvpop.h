@@ -276,7 +276,8 @@ kvpop_status kvpop_boundary_loss(const float* r_hat, const int32_t* t_bnd, const
  * A decode step's single tokens are b = n sequences of S = 1 with their positions.
  * D 64 or 128, any Hq and H up to 65535, R a multiple of 16 up to D, b * S < 2^31,
  * strides multiples of 8, q, k and outputs 16-byte aligned, eps >= 0.  fp32
- * arithmetic, one rounding to bf16 at the end.
+ * arithmetic, one rounding to bf16 at the end; the sum of a head's squares and
+ * mean(x^2) + eps have to be normal fp32 numbers (1.2e-38 to 3.4e38).
  * Errors: INVALID_ARG, UNSUPPORTED (D, R, sizes, alignment), CUDA.
  *
  * kvpop_qk_norm_rope_bwd -- its gradient, for the upstream gradients dq
