@@ -999,8 +999,8 @@ kvpop_status launch(PrefixParams& prm, int ctas, cudaStream_t cs) {
   // SM 8192 such sequences take 293 us, with four 94
   const long long passes = (prm.n * (long long)prm.Hq + kMergeThreads / (D / 4) - 1) / (kMergeThreads / (D / 4));
   const int empties = prm.lens ? (int)min(passes, 4ll * num_sms()) : 0;
-  return cuda_check(launch_pdl(prefix_merge<D>, dim3(across, chunks + (empties + across - 1) / across), dim3(kMergeThreads), 0,
-                               cs, prm, ctas, parts, chunks),
+  const dim3 grid(across, chunks + (empties + across - 1) / across);
+  return cuda_check(launch_pdl(prefix_merge<D>, grid, dim3(kMergeThreads), 0, cs, prm, ctas, parts, chunks),
                     "kvpop_prefix_attn: merge launch");
 }
 
