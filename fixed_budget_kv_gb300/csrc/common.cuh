@@ -38,6 +38,8 @@ enum Site : int {
   SITE_PREFIX_MMA = 51,
   SITE_PREFIX_SOFTMAX = 52,
   SITE_PREFIX_EPILOGUE = 53,
+  SITE_PAGED_TABLE = 60,
+  SITE_PAGED_ROWS = 61,
   SITE_INTERNAL_CHECK = 40,
 };
 

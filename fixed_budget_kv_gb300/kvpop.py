@@ -91,6 +91,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvpop_prefix_attn_workspace_size": ([c_int, c_int, c_int, c_int, c_int, c_int, P], c_int),
         "kvpop_prefix_attn": ([P, P, P, c_int, c_int, c_int, c_int, c_int, c_int, c_float, P, P, P, P, P, P, P, c_size,
                                P], c_int),
+        "kvpop_paged_append": ([P, c_i64, P, c_i64, c_int, c_int, c_int, c_int, P, P, P, c_int, P, c_i64, P, c_i64, c_int,
+                                c_int, P, P], c_int),
+        "kvpop_paged_attn_workspace_size": ([c_int] * 7 + [P], c_int),
+        "kvpop_paged_attn": ([P, c_int, c_int, c_int, c_int, c_int, c_float, P, P, P, c_int, P, c_i64, P, c_i64, c_int, c_int,
+                              P, P, P, c_size, P], c_int),
+        "kvpop_paged_mass_workspace_size": ([c_int] * 7 + [P], c_int),
+        "kvpop_paged_mass": ([P, P, c_int, c_int, c_int, c_int, c_int, c_float, c_float, P, P, P, c_int, P, c_i64, c_int,
+                              c_int, P, P, c_size, P], c_int),
+        "kvpop_paged_evict": ([P, c_i64, P, c_i64, P, c_int, c_int, c_int, Budget, P, P, c_int, c_int, c_int, P, P, P],
+                              c_int),
         "kvpop_cache_create": ([c_int, c_int, c_int, c_int, Budget, P], c_int),
         "kvpop_cache_destroy": ([P], c_int),
         "kvpop_cache_prefill": ([P, P, P, P, c_int, P, P], c_int),
@@ -519,6 +529,177 @@ def prefix_attn(q, pk, pv, cu=None, lens=None, join=None, scale: float = 0.0, wo
                                     _p(lse2), _p(O), _p(lse), _p(workspace), workspace.numel(), _stream(stream)),
            "kvpop_prefix_attn")
     return O, lse
+
+
+# ----------------------------------------------------------------------------
+# paged cache
+# ----------------------------------------------------------------------------
+
+def _page_stride(x, dev, name):
+    """Elements between the pages of a bf16 [pages, H, page, D] cache whose pages are contiguous."""
+    if x.dim() != 4:
+        raise ValueError(f"{name} must be [pages, H, page, D]")
+    if x.is_contiguous() and x.dtype is torch.bfloat16 and x.get_device() == dev:
+        return x.stride(0)
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, not on cuda:{dev}")
+    if not x[:1].is_contiguous():
+        raise ValueError(f"{name}: a page must be contiguous")
+    pages, H, page, D = x.shape
+    return x.stride(0) if pages > 1 else H * page * D
+
+
+def _held(table, lens, cu, T, dev):
+    """Sequences and table width of a call with T rows."""
+    if table.dim() != 2:
+        raise ValueError("table must be [n, max_pages]")
+    n, most = table.shape
+    _fit(table, torch.int32, dev, (n, most), "table")
+    _fit(lens, torch.int32, dev, (n,), "lens")
+    if cu is not None:
+        _fit(cu, torch.int32, dev, (n + 1,), "cu")
+    elif T != n:
+        raise ValueError(f"cu is needed with {T} rows of {n} sequences")
+    return n, most
+
+
+def paged_append(k_new, v_new, kp, vp, table, lens, cu=None, scores=None, stream=None):
+    """New tokens' k_new, v_new [T,H,D] (views of a packed projection, too) into the pages
+    kp, vp [pages,H,page,D]: rows cu[i]..cu[i+1]-1 (int32 [n+1]; None: one each) become the
+    last of the lens[i] slots that table [n,max_pages] gives sequence i.  The weights of
+    the new slots in scores [pages,H,page] become 0."""
+    if k_new.dim() != 3 or kp.dim() != 4:
+        raise ValueError("k_new must be [T, H, D] and kp [pages, H, page, D]")
+    T, H, D = k_new.shape
+    dev = _device(k_new, "k_new")
+    pages, _, page, _ = shape = kp.shape
+    sk, sv = (_token_stride(x[:, None], (T, 1, H, D), dev, name) for x, name in ((k_new, "k_new"), (v_new, "v_new")))
+    if shape != (pages, H, page, D) or vp.shape != shape:
+        raise ValueError(f"kp and vp must be [pages, {H}, page, {D}], got {list(shape)} and {list(vp.shape)}")
+    pk, pv = _page_stride(kp, dev, "kp"), _page_stride(vp, dev, "vp")
+    n, most = _held(table, lens, cu, T, dev)
+    if scores is not None:
+        _fit(scores, torch.float32, dev, (pages, H, page), "scores")
+    st = load().kvpop_paged_append(_p(k_new), sk, _p(v_new), sv, T, n, H, D, _p(cu), _p(lens), _p(table), most, _p(kp), pk,
+                                   _p(vp), pv, pages, page, _p(scores), _stream(stream))
+    if st:
+        _check(st, "kvpop_paged_append")
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_workspace(what, dev, T, n, Hq, H, D, most, page) -> int:
+    """Bytes on device dev: a function of the sizes and of the device's number of SMs."""
+    nb = c_size()
+    name = f"kvpop_paged_{what}_workspace_size"
+    _check(getattr(load(), name)(T, n, Hq, H, D, most, page, ctypes.byref(nb)), name)
+    return nb.value
+
+
+def paged_attn_workspace_size(T, n, Hq, H, D, max_pages, page) -> int:
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _paged_workspace("attn", dev, T, n, Hq, H, D, max_pages, page)
+
+
+def paged_mass_workspace_size(T, n, Hq, H, D, max_pages, page) -> int:
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    return _paged_workspace("mass", dev, T, n, Hq, H, D, max_pages, page)
+
+
+def paged_attn(q, kp, vp, table, lens, cu=None, scale: float = 0.0, workspace=None, out=None, stream=None):
+    """Causal attention of new tokens q [T,Hq,D] over the slots that their sequences hold,
+    their own among them (appended before): table, lens, cu as for paged_append.  Returns
+    (O [T,Hq,D] bf16, lse [T,Hq] fp32); rows of no sequence are not written."""
+    if q.dim() != 3 or kp.dim() != 4:
+        raise ValueError("q must be [T, Hq, D] and kp [pages, H, page, D]")
+    T, Hq, D = rows = q.shape
+    pages, H, page, _ = shape = kp.shape
+    dev = _device(q, "q")
+    _fit(q, torch.bfloat16, dev, rows, "q")
+    if shape[3] != D or vp.shape != shape:
+        raise ValueError(f"kp and vp must be [pages, H, page, {D}], got {list(shape)} and {list(vp.shape)}")
+    pk, pv = _page_stride(kp, dev, "kp"), _page_stride(vp, dev, "vp")
+    n, most = _held(table, lens, cu, T, dev)
+    with _on(stream):
+        if out is None:
+            O, lse = _empty_as(q), torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        else:
+            O, lse = out
+            _fit(O, torch.bfloat16, dev, rows, "O")
+            _fit(lse, torch.float32, dev, (T, Hq), "lse")
+        if workspace is None:
+            workspace = torch.empty(_paged_workspace("attn", dev, T, n, Hq, H, D, most, page), dtype=torch.uint8,
+                                    device=q.device)
+        else:
+            _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
+    st = load().kvpop_paged_attn(_p(q), T, n, Hq, H, D, scale, _p(cu), _p(lens), _p(table), most, _p(kp), pk, _p(vp), pv,
+                                 pages, page, _p(O), _p(lse), _p(workspace), workspace.numel(), _stream(stream))
+    if st:
+        _check(st, "kvpop_paged_attn")
+    return O, lse
+
+
+def paged_mass(q, lse, kp, scores, table, lens, cu=None, scale: float = 0.0, decay: float = 1.0, workspace=None,
+               stream=None):
+    """scores [pages,H,page] fp32 = decay * scores + the attention weight that each held key
+    receives from the rows of q [T,Hq,D], whose log-sum-exp lse [T,Hq] is paged_attn's.  The
+    rows may be the last ones of each chunk only (an observation window).  Returns scores."""
+    if q.dim() != 3 or kp.dim() != 4:
+        raise ValueError("q must be [T, Hq, D] and kp [pages, H, page, D]")
+    T, Hq, D = q.shape
+    pages, H, page, d = kp.shape
+    dev = _device(q, "q")
+    _fit(q, torch.bfloat16, dev, q.shape, "q")
+    _fit(lse, torch.float32, dev, (T, Hq), "lse")
+    if d != D:
+        raise ValueError(f"kp must be [pages, H, page, {D}], got {list(kp.shape)}")
+    pk = _page_stride(kp, dev, "kp")
+    _fit(scores, torch.float32, dev, (pages, H, page), "scores")
+    n, most = _held(table, lens, cu, T, dev)
+    if workspace is None:
+        with _on(stream):
+            workspace = torch.empty(_paged_workspace("mass", dev, T, n, Hq, H, D, most, page), dtype=torch.uint8,
+                                    device=q.device)
+    else:
+        _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
+    st = load().kvpop_paged_mass(_p(q), _p(lse), T, n, Hq, H, D, scale, decay, _p(cu), _p(lens), _p(table), most, _p(kp), pk,
+                                 pages, page, _p(scores), _p(workspace), workspace.numel(), _stream(stream))
+    if st:
+        _check(st, "kvpop_paged_mass")
+    return scores
+
+
+def paged_evict(kp, vp, scores, table, lens, s: int, w: int, k: int, out=None, stream=None):
+    """Each head of the sequences with more than B = s + w + k slots keeps its first s, its
+    last w and the k of the others with the highest scores, moved to slots 0..B-1 in their
+    order.  Returns (kept [n,H,B] int32: the old slot of each new one, -1 behind the new
+    length; new_lens [n] int32)."""
+    if kp.dim() != 4:
+        raise ValueError("kp must be [pages, H, page, D]")
+    pages, H, page, D = shape = kp.shape
+    dev = _device(kp, "kp")
+    if vp.shape != shape:
+        raise ValueError(f"vp must be {list(shape)}, got {list(vp.shape)}")
+    pk, pv = _page_stride(kp, dev, "kp"), _page_stride(vp, dev, "vp")
+    _fit(scores, torch.float32, dev, (pages, H, page), "scores")
+    n, most = _held(table, lens, None, table.shape[0], dev)
+    B = s + w + k
+    if out is None:
+        with _on(stream):
+            kept = torch.empty((n, H, max(B, 0)), dtype=torch.int32, device=kp.device)
+            new = torch.empty(n, dtype=torch.int32, device=kp.device)
+    else:
+        kept, new = out
+        _fit(kept, torch.int32, dev, (n, H, B), "kept")
+        _fit(new, torch.int32, dev, (n,), "new_lens")
+    st = load().kvpop_paged_evict(_p(kp), pk, _p(vp), pv, _p(scores), n, H, D, Budget(s, w, k), _p(lens), _p(table), most,
+                                  pages, page, _p(kept), _p(new), _stream(stream))
+    if st:
+        _check(st, "kvpop_paged_evict")
+    return kept, new
 
 
 # ----------------------------------------------------------------------------

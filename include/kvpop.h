@@ -398,6 +398,90 @@ kvpop_status kvpop_prefix_attn(const void* q, const void* pk, const void* pv, in
                                const float* lse2, void* O, float* lse, void* workspace, size_t workspace_bytes,
                                kvpop_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Paged cache -- keys and values in pages that sequences hold through a table, for
+ * batches in which prompts arrive in chunks beside decode rows, and eviction by the
+ * attention weight that each key has received instead of by a static priority.  Not in
+ * the pages of the method; the mask, the prompt's attention and the norm come before it
+ * as they come before the fixed-budget cache, and O and lse of kvpop_paged_attn join
+ * those of kvpop_prefix_attn.
+ *
+ *   kp, vp   [pages, H, page, D] bf16; the pages kp_stride / vp_stride elements apart
+ *            (H * page * D, or more where a pool holds other data between them)
+ *   scores   [pages, H, page] fp32, contiguous: the weight that each slot has received
+ *   table    [n, max_pages] int32 device: slot t of sequence i lies at place t mod page of
+ *            page table[i][t / page], for every head.  Entries behind the last slot are
+ *            never used, whatever they hold.  Sequences may share pages that a call only
+ *            reads; a page that it writes belongs to one sequence, once
+ *   lens     [n] int32 device: the slots that each sequence holds, the call's new tokens
+ *            included (clamped to [0, max_pages * page])
+ *   cu       [n + 1] int32 device, non-decreasing in [0, T]: rows cu[i] .. cu[i+1]-1 are the
+ *            c new tokens of sequence i, in order; NULL with T = n: one token each.  Row r < c
+ *            is slot lens[i] - c + r and sees the slots up to its own; rows that would lie
+ *            before slot 0 have no slot and see nothing.
+ * page is a power of two from 16 to 65536 (a cache that is contiguous for each sequence is
+ * one page each), D 64 or 128, H and n up to 65535, T up to 2^24, max_pages * page up to
+ * 2^30, strides multiples of 8, kp and vp 16-byte aligned.  A table entry in use that is
+ * outside [0, pages) records KVPOP_ERR_INVALID_ARG in the device status words; its slots
+ * are not written and read as zeros.  K and V of the slots in use must be finite; what other
+ * places of the pages hold does not matter.
+ *
+ * kvpop_paged_append: the new tokens' keys and values into their slots.
+ *   k_new, v_new [T, H, D] bf16, tokens k_new_stride / v_new_stride elements apart (multiples
+ *            of 8; a part of a packed projection may stay where it is), 16-byte aligned
+ *   scores   nullable: the new slots' weights become 0
+ *
+ * kvpop_paged_attn: for query head h G + g of a row, s_t = scale q . k_{t,h} over the slots
+ *   that it sees: lse = log sum exp s_t, O = sum exp(s_t - lse) v_t.
+ *   q        [T, Hq, D] bf16; O [T, Hq, D] bf16, lse [T, Hq] fp32 natural log.  A row that
+ *            sees nothing gets O = 0 and lse = -inf; rows outside cu[0] .. cu[n]-1 are left as
+ *            they were.
+ *
+ * kvpop_paged_mass: for every slot t < lens[i] and head h
+ *     scores = decay * scores + sum over the rows that see t, g < G of exp(s_t - lse_row)
+ *   with kvpop_paged_attn's lse (a row whose lse is -inf adds nothing).  Fewer rows than the
+ *   attention had may be given: the chunk's last ones (an observation window at a prompt's
+ *   end) with their cu.  decay in [0, 1]; 0 does not read the old scores.  The sums are taken
+ *   in a fixed order: the same bits every run.
+ *
+ * kvpop_paged_evict: sequences with more than B = s + w + k slots are cut to B.  Each head
+ *   keeps slots [0, s), [lens - w, lens) and the k best of those between in the order (score
+ *   descending, slot ascending; NaN counts as -inf, -0 as +0), and moves K, V and scores of
+ *   the kept slots to slots 0 .. B-1 in their order.  What lay behind stays as it was; the
+ *   pages from ceil(B / page) on are the caller's again.
+ *   kept     [n, H, B] int32: the old slot of each new one; -1 behind the new length
+ *   new_lens [n] int32: min(lens, B); may be lens
+ *   n * H <= 65535, scores 16-byte aligned; the slots of a table entry outside [0, pages) count
+ *   as -inf and are not moved.
+ *
+ * kvpop_paged_attn and kvpop_paged_mass: scale <= 0 selects 1/sqrt(D); G dividing 128, Hq up
+ * to 65535, T * Hq < 2^31; q and O 16-byte aligned; bf16 operands (the attention rounds its
+ * softmax weights to bf16 before their product with V), fp32 accumulation.  workspace: the
+ * call's _workspace_size() bytes, 256-byte aligned; contents undefined between calls, so calls
+ * that overlap in time need one each.  Sequences that overlap to more than T rows in all
+ * record KVPOP_ERR_INVALID_ARG in the status words, and nothing is computed.
+ * Errors of all: INVALID_ARG, UNSUPPORTED (sizes, alignment), CUDA.
+ * ---------------------------------------------------------------------- */
+kvpop_status kvpop_paged_append(const void* k_new, int64_t k_new_stride, const void* v_new, int64_t v_new_stride, int T,
+                                int n, int H, int D, const int32_t* cu, const int32_t* lens, const int32_t* table,
+                                int max_pages, void* kp, int64_t kp_stride, void* vp, int64_t vp_stride, int pages,
+                                int page, float* scores, kvpop_stream stream);
+kvpop_status kvpop_paged_attn_workspace_size(int T, int n, int Hq, int H, int D, int max_pages, int page,
+                                             size_t* bytes);
+kvpop_status kvpop_paged_attn(const void* q, int T, int n, int Hq, int H, int D, float scale, const int32_t* cu,
+                              const int32_t* lens, const int32_t* table, int max_pages, const void* kp,
+                              int64_t kp_stride, const void* vp, int64_t vp_stride, int pages, int page, void* O,
+                              float* lse, void* workspace, size_t workspace_bytes, kvpop_stream stream);
+kvpop_status kvpop_paged_mass_workspace_size(int T, int n, int Hq, int H, int D, int max_pages, int page,
+                                             size_t* bytes);
+kvpop_status kvpop_paged_mass(const void* q, const float* lse, int T, int n, int Hq, int H, int D, float scale,
+                              float decay, const int32_t* cu, const int32_t* lens, const int32_t* table, int max_pages,
+                              const void* kp, int64_t kp_stride, int pages, int page, float* scores, void* workspace,
+                              size_t workspace_bytes, kvpop_stream stream);
+kvpop_status kvpop_paged_evict(void* kp, int64_t kp_stride, void* vp, int64_t vp_stride, float* scores, int n, int H,
+                               int D, kvpop_budget budget, const int32_t* lens, const int32_t* table, int max_pages,
+                               int pages, int page, int32_t* kept, int32_t* new_lens, kvpop_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
