@@ -40,6 +40,10 @@ enum Site : int {
   SITE_PREFIX_EPILOGUE = 53,
   SITE_PAGED_TABLE = 60,
   SITE_PAGED_ROWS = 61,
+  SITE_PAGED_PRODUCER = 62,
+  SITE_PAGED_MMA = 63,
+  SITE_PAGED_SOFTMAX = 64,
+  SITE_PAGED_EPILOGUE = 65,
   SITE_INTERNAL_CHECK = 40,
 };
 

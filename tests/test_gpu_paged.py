@@ -328,6 +328,16 @@ def test_lengths_and_rows_out_of_range_are_clamped():
     assert new.tolist() == [96, 0] and (kept[1] == -1).all()
 
 
+def test_overlapping_sequences_are_reported():
+    """Sequences that have more than T rows in all: the status says so and nothing is written."""
+    c = Held([150, 150, 150], 1, 16, 64, seed=13)
+    q, cu = c.randn(10, 2, 64), i32([0, 8, 2, 10])
+    O, lse = torch.full_like(q, 3.0), torch.full((10, 2), 3.0, device="cuda")
+    kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, cu, out=(O, lse))
+    assert kvpop.device_status(reset=True)[0] == 1
+    assert (O == 3.0).all() and (lse == 3.0).all()
+
+
 @pytest.mark.parametrize("bad", [-1, 1 << 30, 9])
 def test_pages_that_do_not_exist_are_reported(bad):
     """Their slots read as zeros, and nothing is written to them."""
