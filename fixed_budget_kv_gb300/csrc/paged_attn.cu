@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       const int box = lane / DH, dh = lane - box * DH;
       const bool mine = box < boxes;
       const uint32_t dst = dh * kBlockBytes + (box << log_box) * 128;
-      Seg s;
+      Seg s = {};
       Ring<NS> r;
       int loads = 0;
       bool ok = true;

@@ -1,50 +1,646 @@
-// kvpop_paged_mass: the attention weight that each key of a paged cache receives from a chunk's rows.
+// kvpop_paged_mass: the attention weight that each key of a paged cache receives from a chunk's
+// rows: scores_t = decay scores_t + sum over rows r >= t - (len - c), heads g < G of
+// exp(scale q_{r,hG+g} . k_t - lse_{r,hG+g}).
 //
-// One thread takes one slot of one head and walks the rows that see it.
+// The transposed product S' = K Q^T has a key in each TMEM lane, so that a thread sums its own
+// key's row and nothing is exchanged; every term is a probability, so a plain fp32 sum needs no
+// running maximum.  A CTA holds up to four 128-slot tiles of K (a block of 512 slots of one head)
+// while query tiles of 128 / G tokens by G heads stream past: each tile of either is fetched
+// once for four or more products.  Chunks are bound by the tensor core beside one exponential a
+// (row, slot); decode rows and observation windows by reading K.
+//
+// Work split: an item is one (sequence, block of slots, KV head), in that order, and has kSetup
+// units of setup and one for each query tile that sees the block.  CTA c takes the c-th part of
+// all units, one CTA an SM.  An item whose query tiles are all a CTA's is finished by it; of the
+// others a CTA has at most two, in a slot of the workspace each, and mass_merge adds the slots of
+// an item up in the order of the CTAs.  No atomics: the same call gives the same bits.
+//
+// Warp roles of mass_kernel (640 threads):
+//   warp 0       TMA producer of K: a ring of tiles in the order of their use
+//   warp 1       TMEM allocation; issues tcgen05.mma
+//   warp 2       query tiles and their -lse, in log2 units
+//   warp 3       the CTA's share of the units, handed to the others segment by segment
+//   warps 4-19   four warpgroups that sum, one a tile, one thread a key
+// A tile's 128 TMEM columns are handed back as soon as they are in registers, and the tensor core
+// works on the other tiles meanwhile.  A thread sums 128 columns by themselves before it adds them
+// to its total: long chunks would lose digits in one running sum.
 #include <string.h>
 
+#include <atomic>
+
 #include "paged.cuh"
+#include "segments.cuh"
 
 namespace kvpop {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kTiles = 4;  // tiles of K in a block
+constexpr int kThreads = (4 + 4 * kTiles) * 32;
+constexpr int kKeys = 128, kBlockKeys = kTiles * kKeys;
+constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
+// Loading a block of K and changing over to it, in query tiles.
+constexpr int kSetup = 2;
+constexpr int kSegs = 4;
+// Query tiles of a segment at most: keeps the waits that last one far below their limit.
+constexpr int kRunTiles = 256;
+constexpr int kLseStages = 4;
+// Register split: warps 0-3 drop to kRegsIo, the summing warpgroups rise to kRegsSum.
+constexpr int kRegsIo = 64;
+constexpr int kRegsSum = 104;
+constexpr int kRegsNeeded = (128 * kRegsIo + (kThreads - 128) * kRegsSum + kThreads - 1) / kThreads;
+
+// An item that several CTAs share, and the last of them.  h = -1: none.
+struct __align__(16) Split {
+  int i, h, block, c1;
+};
 
 struct MassParams {
+  CUtensorMap tq, tk;
   Paged c;
-  const __nv_bfloat16 *q, *k;
   const float* lse;
-  int64_t k_stride;  // elements between pages
   float* scores;
-  int Hq, G;
-  float scale, decay;
+  Split* split;  // [CTA] the item that the CTA is the second to work on
+  float* part;   // [CTA, 2 slots, 512 keys]
+  int Hq, G, log_g, log_p;  // query tiles of 2^log_p = 128 / G tokens
+  int q_bytes;              // of a query tile's box and 64 columns
+  float scale_log2, decay;
+};
+
+// A sequence: rows [lo, lo + c), slots, blocks of slots, query tiles and units.  A sequence without
+// rows has one query tile all the same, without columns: its scores fade.
+struct Seq {
+  int lo, c, len, nb, nq, units;
+};
+// The first query tile that sees slot t.
+__device__ __forceinline__ int first_tile(int a, int log_p, int t) { return max(0, t - a) >> log_p; }
+// Units of blocks 0 .. m - 1 for one head.
+__device__ __forceinline__ int units_before(const MassParams& p, const Seq& s, int m) {
+  const int a = s.len - s.c;
+  // blocks that begin at or behind slot a, from b0 on, are not seen by the first tokens: by
+  // f0, f0 + 512 / tokens, ... query tiles
+  const int b0 = a > 0 ? (a + kBlockKeys - 1) / kBlockKeys : 0;
+  const int n = max(0, m - b0);
+  const long long f0 = first_tile(a, p.log_p, b0 * kBlockKeys);
+  return (int)((long long)m * (s.nq + kSetup) - (n * f0 + ((long long)n * (n - 1) / 2 << (9 - p.log_p))));
+}
+__device__ __forceinline__ Seq sequence(const MassParams& p, int i) {
+  Seq s;
+  s.lo = p.c.lo(i);
+  s.c = p.c.hi(i, s.lo) - s.lo;
+  s.len = p.c.len(i);
+  s.nb = (s.len + kBlockKeys - 1) / kBlockKeys;
+  s.nq = max(1, (s.c + (1 << p.log_p) - 1) >> p.log_p);
+  s.units = s.nb ? units_before(p, s, s.nb) * p.c.H : 0;
+  return s;
+}
+
+// One segment: query tiles [q0, q0 + NQ) over a block of slots of sequence i, head h.
+struct __align__(16) Seg {
+  int i, h, slot0, len;
+  int q0, NQ, lo, c;
+  int tiles, flags, pad[2];  // tiles of K that a query tile of the segment sees
+  // the first of the block's query tiles here; the last of them here
+  __device__ __forceinline__ bool begins() const { return flags & 1; }
+  __device__ __forceinline__ bool ends() const { return flags & 2; }
+  // this CTA has all of the block's query tiles
+  __device__ __forceinline__ bool whole() const { return flags & 4; }
+  // otherwise: 0 when an earlier CTA began the block, 1 when this one did
+  __device__ __forceinline__ int slot() const { return flags >> 3 & 1; }
+  // the first query tile that sees tile rt, and the columns of query tile q
+  __device__ __forceinline__ int first(int rt, int log_p) const { return first_tile(len - c, log_p, slot0 + rt * kKeys); }
+  __device__ __forceinline__ int columns(int q, int log_p, int log_g) const {
+    return max(0, min(1 << log_p, c - (q << log_p))) << log_g;
+  }
+};
+
+template <int NK, int NQS>
+struct Bars {
+  uint64_t k_full[NK], k_empty[NK];
+  uint64_t q_full[NQS], q_empty[NQS];
+  uint64_t s_full[kTiles], s_empty[kTiles];
+  uint64_t l_full[kLseStages], l_empty[kLseStages];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t drain;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) mass_simple(const __grid_constant__ MassParams p) {
+struct Layout {
+  static constexpr int DH = D / 64;
+  static constexpr int NK = D == 128 ? 5 : 10;  // tiles of K
+  static constexpr int NQ = D == 128 ? 2 : 4;   // query tiles
+  static constexpr int kTile = DH * kBlockBytes;
+  static constexpr int k_off = 0;
+  static constexpr int q_off = k_off + NK * kTile;
+  static constexpr int lse_off = q_off + NQ * kTile;  // [stage][128]
+  static constexpr int bar_off = lse_off + kLseStages * 512;
+  static constexpr int seg_off = bar_off + ((int)sizeof(Bars<NK, NQ>) + 15) / 16 * 16;
+  static constexpr int misc_off = seg_off + kSegs * (int)sizeof(Seg);  // TMEM address, abort flag, a flag a stage
+  static constexpr int total = misc_off + 8 + 4 * kLseStages;
+  static_assert(total <= 232448, "shared memory of one CTA");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant__ MassParams p) {
+  using L = Layout<D>;
+  constexpr int DH = L::DH, NK = L::NK, NQS = L::NQ;
+  extern __shared__ __align__(1024) uint8_t smem[];  // no slack left to align by hand: the walker checks
+  Bars<NK, NQS>* bars = reinterpret_cast<Bars<NK, NQS>*>(smem + L::bar_off);
+  Seg* segs = reinterpret_cast<Seg*>(smem + L::seg_off);
+  float* lse_s = reinterpret_cast<float*>(smem + L::lse_off);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::misc_off);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc_off + 4);
+  int* none_s = reinterpret_cast<int*>(smem + L::misc_off + 8);  // [stage] whether a row of it has lse = -inf
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = warp_id(), lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 1);
+    }
+    for (int i = 0; i < NQS; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_empty[i], 1);
+    }
+    for (int i = 0; i < kTiles; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->s_empty[i], 4);
+    }
+    for (int i = 0; i < kLseStages; ++i) {
+      mbar_init(&bars->l_full[i], 1);
+      mbar_init(&bars->l_empty[i], 4 * kTiles);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(&bars->seg_full[i], 1);
+      mbar_init(&bars->seg_empty[i], 3 + 4 * kTiles);  // K, query tiles, MMA, summing warps
+    }
+    mbar_init(&bars->drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  // the previous kernel of the stream may still be running (programmatic launch):
+  // wait for it before any global access; this CTA already holds its tensor memory
   grid_dep_wait();
   grid_dep_launch();
-  const Paged& c = p.c;
-  const int i = blockIdx.y / c.H, h = blockIdx.y - i * c.H;
-  const int lo = c.lo(i), hi = c.hi(i, lo), len = c.len(i);
-  for (int t = blockIdx.x * kThreads + threadIdx.x; t < len; t += gridDim.x * kThreads) {
-    const int pg = c.page_of(i, t);
-    if (pg < 0) {
-      report_page(c.status, i);
-      continue;
-    }
-    const __nv_bfloat16* k = p.k + pg * p.k_stride + (((size_t)h << c.log_page) + (t & ((1 << c.log_page) - 1))) * D;
-    float sum = 0.0f;
-    for (int row = max(lo, hi - (len - t)); row < hi; ++row)
-      for (int g = 0; g < p.G; ++g) {
-        const size_t at = (size_t)row * p.Hq + h * p.G + g;
-        float s = 0.0f;
-        for (int d = 0; d < D; ++d) s += __bfloat162float(p.q[at * D + d]) * __bfloat162float(k[d]);
-        sum += p.lse[at] == __int_as_float(0xff800000) ? 0.0f : expf(s * p.scale - p.lse[at]);
+
+  auto fail = [&](int site, int detail) {
+    report_error(p.c.status, KVPOP_ERR_TIMEOUT, site, detail);
+    *abort_flag = 1;
+  };
+  // for a whole warp: false where the wait was given up
+  auto wait_bar = [&](uint64_t* bar, uint32_t ph, int site, int detail) -> bool {
+    if (warp_wait(bar, ph, abort_flag)) return true;
+    if (lane == 0) fail(site, detail);
+    return false;
+  };
+  // segment n, once the walker has written it; false at the end of the work
+  auto get_seg = [&](int n, Seg& s, int site) -> bool {
+    if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, site, 9)) return false;
+    s = segs[n % kSegs];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
+    return s.NQ > 0;
+  };
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegsIo>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ K producer
+      // Lane (box, half) issues its part of a tile: boxes of a page, or of 128 slots of one, of
+      // 64 columns.  The table entries of a segment are read before the loads of the one before.
+      if (lane == 0) tma_prefetch_desc(&p.tk);
+      const int log_box = min(p.c.log_page, 7), boxes = kKeys >> log_box;
+      const int box = lane / DH, dh = lane - box * DH;
+      const bool mine = box < boxes;
+      const uint32_t dst = dh * kBlockBytes + (box << log_box) * 128;
+      Ring<NK> r;
+      int loads = 0;
+      auto pages_of = [&](const Seg& s, int (&pg)[kTiles]) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          const int slot = s.slot0 + t * kKeys + (box << log_box);
+          pg[t] = p.c.pages;  // one past the last: zeros
+          if (mine && t < s.tiles && slot < s.len) {
+            const int x = p.c.page_of(s.i, slot);
+            if (x >= 0) pg[t] = x;
+            else if (dh == 0) report_page(p.c.status, s.i);
+          }
+        }
+      };
+      Seg s, next;
+      int pg[kTiles], pg_next[kTiles];
+      bool ok = true, more = get_seg(0, s, SITE_PAGED_PRODUCER);
+      if (more) pages_of(s, pg);
+      for (int n = 1; ok && more; ++n) {
+        more = get_seg(n, next, SITE_PAGED_PRODUCER);
+        if (more) pages_of(next, pg_next);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if (!ok || t >= s.tiles) break;
+          ok = wait_bar(&bars->k_empty[r.st], r.ph ^ 1, SITE_PAGED_PRODUCER, 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[r.st], L::kTile);
+          __syncwarp();
+          if (mine)
+            tma_load_4d(smem + L::k_off + r.st * L::kTile + dst, &p.tk, &bars->k_full[r.st], dh * 64,
+                        (s.slot0 + t * kKeys + (box << log_box)) & ((1 << p.c.log_page) - 1), s.h, pg[t]);
+          r.skip(1);
+          ++loads;
+        }
+        s = next;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) pg[t] = pg_next[t];
       }
-    float* out = p.scores + c.slot_row(pg, h, t);
-    *out = p.decay == 0.0f ? sum : p.decay * *out + sum;
+      if (*abort_flag && lane == 0) {
+        // given up: nobody has waited for the last loads, which must land before the CTA ends
+        for (int i = 0; i < min(loads, NK); ++i) {
+          const int seq = loads - 1 - i;
+          mbar_wait(&bars->k_full[seq % NK], (seq / NK) & 1, nullptr);
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp runs it, in step, and one elected lane issues (see paged_attn.cu).  Tile rt of
+      // a block has TMEM columns 128 rt ..; the products cover as many columns as the query tile has.
+      const uint32_t k_lo = desc_lo(sbase + L::k_off, 16), q_lo = desc_lo(sbase + L::q_off, 16);
+      Ring<NK> base;
+      Ring<NQS> q;
+      uint32_t ns = 0;  // bit rt: parity of tile rt's next product
+      Seg s;
+      bool ok = true;
+      for (int n = 0; ok && get_seg(n, s, SITE_PAGED_MMA); ++n) {
+        int first[kTiles];
+#pragma unroll
+        for (int rt = 0; rt < kTiles; ++rt) first[rt] = s.first(rt, p.log_p);
+        uint32_t have = 0;  // bit rt: tile rt has landed
+        for (int c = s.q0; ok && c < s.q0 + s.NQ; ++c) {
+          ok = wait_bar(&bars->q_full[q.st], q.ph, SITE_PAGED_MMA, 1);
+          if (!ok) break;
+          const uint32_t cols = max(32, (s.columns(c, p.log_p, p.log_g) + 31) & ~31);
+          const uint32_t idesc = idesc_bf16(128, 0, 0) | (cols >> 3) << 17;
+          Ring<NK> k = base;
+#pragma unroll
+          for (int rt = 0; rt < kTiles; ++rt) {
+            if (rt >= s.tiles) break;
+            if (c >= first[rt]) {
+              if (!(have >> rt & 1)) {
+                ok = wait_bar(&bars->k_full[k.st], k.ph, SITE_PAGED_MMA, 2);
+                have |= 1u << rt;
+              }
+              ok = ok && wait_bar(&bars->s_empty[rt], (ns >> rt & 1) ^ 1, SITE_PAGED_MMA, 3);
+              if (!ok) break;
+              ns ^= 1u << rt;
+              tc_fence_after();
+              const uint32_t a0 = k_lo + k.st * (L::kTile / 16), b0 = q_lo + q.st * (L::kTile / 16);
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((ks >> 2) * kBlockBytes + (ks & 3) * 32) / 16;
+                mma_ss_elect(tbase + 128 * rt, a0 + off, b0 + off, idesc, ks > 0 ? 1u : 0u);
+              }
+              mma_commit_elect(&bars->s_full[rt]);
+              if (c == s.q0 + s.NQ - 1) mma_commit_elect(&bars->k_empty[k.st]);
+            }
+            k.skip(1);
+          }
+          mma_commit_elect(&bars->q_empty[q.st]);
+          q.skip(1);
+        }
+        base.skip(s.tiles);
+      }
+      // drain every issued MMA before teardown
+      mma_commit_elect(&bars->drain);
+      warp_wait(&bars->drain, 0, nullptr);
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ query tiles and their lse
+      if (lane == 0) tma_prefetch_desc(&p.tq);
+      Ring<NQS> q;
+      Ring<kLseStages> r;
+      int loads = 0;
+      Seg s;
+      bool ok = true;
+      for (int n = 0; ok && get_seg(n, s, SITE_PAGED_PRODUCER); ++n) {
+        // rows 4 lane .. 4 lane + 3 of query tile c: -lse in log2 units; -inf adds nothing
+        float x[4];
+        auto read = [&](int c) {
+          const int cols = s.columns(c, p.log_p, p.log_g);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int col = 4 * lane + u;
+            x[u] = col < cols ? p.lse[(size_t)(s.lo + (c << p.log_p) + (col >> p.log_g)) * p.Hq + s.h * p.G + (col & (p.G - 1))]
+                              : __int_as_float(0x7f800000);
+          }
+        };
+        read(s.q0);
+        for (int c = s.q0; c < s.q0 + s.NQ; ++c) {
+          if (!(ok = wait_bar(&bars->q_empty[q.st], q.ph ^ 1, SITE_PAGED_PRODUCER, 2))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full[q.st], DH * p.q_bytes);
+            for (int dh = 0; dh < DH; ++dh)
+              tma_load_4d(smem + L::q_off + q.st * L::kTile + dh * kBlockBytes, &p.tq, &bars->q_full[q.st], dh * 64, s.h * p.G,
+                          s.lo + (c << p.log_p), 0);
+          }
+          __syncwarp();
+          q.skip(1);
+          ++loads;
+          float y[4];
+          bool none = false;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            none |= x[u] == neg_inf();
+            y[u] = x[u] == neg_inf() ? neg_inf() : -x[u] * 1.4426950408889634f;
+          }
+          if (c + 1 < s.q0 + s.NQ) read(c + 1);
+          none = __any_sync(0xffffffffu, none);
+          if (!(ok = wait_bar(&bars->l_empty[r.st], r.ph ^ 1, SITE_PAGED_PRODUCER, 3))) break;
+          reinterpret_cast<float4*>(lse_s)[r.st * 32 + lane] = make_float4(y[0], y[1], y[2], y[3]);
+          if (lane == 0) none_s[r.st] = none;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->l_full[r.st]);
+          r.skip(1);
+        }
+      }
+      if (*abort_flag && lane == 0) {  // as for K
+        for (int i = 0; i < min(loads, NQS); ++i) {
+          const int seq = loads - 1 - i;
+          mbar_wait(&bars->q_full[seq % NQS], (seq / NQS) & 1, nullptr);
+        }
+      }
+    } else {
+      // ------------------------------------------------------------ the CTA's share
+      // lane l holds sequence j0 + l of a window of 32, and its first unit
+      int U = 0, members = 0, j0 = 0, base = 0;
+      Seq g;
+      auto window = [&](int w0, int at) {  // sequences w0 .., the first of them at unit `at`; returns the unit after
+        g = w0 + lane < p.c.n ? sequence(p, w0 + lane) : Seq{0, 0, 0, 0, 0, 0};
+        const int incl = scan_incl(g.units);
+        j0 = w0;
+        base = at + incl - g.units;
+        return at + __shfl_sync(0xffffffffu, incl, 31);
+      };
+#pragma unroll 1
+      for (int w0 = 0; w0 < p.c.n; w0 += 32) {
+        U = window(w0, U);
+        members = min(members, p.c.T + 1) + __reduce_add_sync(0xffffffffu, min(g.c, p.c.T));
+      }
+      Split split = {0, -1, 0, 0};
+      if (members > p.c.T) {
+        // sequences that overlap, which the interface rules out, could pass the host's bound on U: no work
+        U = 0;
+        if (blockIdx.x == 0 && lane == 0) report_error(p.c.status, KVPOP_ERR_INVALID_ARG, SITE_PAGED_ROWS, 6);
+      }
+      if (sbase & 1023) {
+        // the tiles would miss their swizzle.  No work either: an early return would leave the
+        // merge whatever the workspace held for this CTA's item
+        U = 0;
+        if (lane == 0) report_error(p.c.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 61);
+      }
+      const int C = min((int)gridDim.x, U);
+      const Share sh(U, max(C, 1));
+      int u = 0, end = 0;
+      if ((int)blockIdx.x < C) {
+        u = sh.first(blockIdx.x);
+        end = sh.first(blockIdx.x + 1);
+      }
+      if (p.c.n > 32 && u < end) {  // back to the window in which the share begins
+        int at = 0;
+#pragma unroll 1
+        for (int w0 = 0;; w0 += 32) {
+          at = window(w0, at);
+          if (u < at) break;
+        }
+      }
+      bool own = false;  // this CTA began the item that u is in
+      for (int n = 0;; ++n) {
+        Seg s = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, {0, 0}};  // NQ = 0 ends the work
+        while (u < end && s.NQ == 0) {
+          // the sequence that holds unit u: the last of the window that begins at or before it
+          unsigned at = __ballot_sync(0xffffffffu, g.units > 0 && base <= u && u < base + g.units);
+          if (at == 0) {
+            window(j0 + 32, u);  // u is the window's end
+            continue;
+          }
+          const int l = __ffs(at) - 1;
+          Seq q;
+          const int b = __shfl_sync(0xffffffffu, base, l);
+          q.lo = __shfl_sync(0xffffffffu, g.lo, l);
+          q.c = __shfl_sync(0xffffffffu, g.c, l);
+          q.len = __shfl_sync(0xffffffffu, g.len, l);
+          q.nb = __shfl_sync(0xffffffffu, g.nb, l);
+          q.nq = __shfl_sync(0xffffffffu, g.nq, l);
+          // the block of slots: the last that begins at or before the unit
+          const int v = u - b;
+          int kb = 0, over = q.nb;
+          while (over - kb > 1) {
+            const int mid = (kb + over) >> 1;
+            if ((long long)units_before(p, q, mid) * p.c.H <= v) kb = mid;
+            else over = mid;
+          }
+          const int before = units_before(p, q, kb) * p.c.H;
+          s.i = j0 + l;
+          s.slot0 = kb * kBlockKeys;
+          s.len = q.len;
+          s.lo = q.lo;
+          s.c = q.c;
+          const int q_lo = s.first(0, p.log_p);
+          const int per = q.nq - q_lo + kSetup, item = (v - before) / per, off = (v - before) - item * per;
+          // this CTA's units of the item from here on, up to a run of query tiles: [off, stop)
+          const int stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
+          const int t0 = max(off - kSetup, 0), t1 = max(stop - kSetup, 0);
+          s.h = item;
+          s.q0 = q_lo + t0;
+          s.NQ = t1 - t0;
+          s.tiles = 0;
+          for (int rt = 0; rt < kTiles; ++rt)
+            s.tiles += s.slot0 + rt * kKeys < s.len && s.first(rt, p.log_p) < q_lo + t1;
+          const bool cont = t0 > 0 && n > 0;
+          own = t0 == 0 || (cont && own);
+          s.flags = (cont ? 0 : 1) | (stop == per || u + (stop - off) == end ? 2 : 0) | (own && stop == per ? 4 : 0) |
+                    (own ? 8 : 0);
+          if (n == 0 && t0 > 0) {
+            // the work begins inside an item; the second of its CTAs leaves word of it
+            const int first = b + before + item * per + kSetup;
+            split = {s.i, sh.cta_of(first) + 1 == (int)blockIdx.x ? s.h : -1, kb, sh.cta_of(first + q.nq - q_lo - 1)};
+          }
+          u += stop - off;
+        }
+        if (n == 0 && lane == 0) p.split[blockIdx.x] = split;
+        if (!wait_bar(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, SITE_PAGED_PRODUCER, 4)) break;
+        if (lane == 0) {
+          segs[n % kSegs] = s;
+          mbar_arrive(&bars->seg_full[n % kSegs]);
+        }
+        if (s.NQ == 0) break;
+      }
+    }
+  } else {
+    setmaxnreg_inc<kRegsSum>();
+    // ------------------------------------------------------------ sums
+    const int rt = (warp - 4) >> 2;  // tile of the block
+    const int quarter = warp & 3;
+    const int row = rt * kKeys + quarter * 32 + lane;  // key of the block
+    const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16) + 128 * rt;
+    const uint64_t s2 = pack2(p.scale_log2, p.scale_log2);
+    float total = 0.0f;
+    uint32_t ns = 0;  // parity of this tile's next product
+    Ring<kLseStages> r;
+    Seg s;
+    bool ok = true;
+    for (int n = 0; ok && get_seg(n, s, SITE_PAGED_SOFTMAX); ++n) {
+      if (s.begins()) total = 0.0f;
+      const int t = s.slot0 + row, a = s.len - s.c, first = s.first(rt, p.log_p);
+      const bool on = t < s.len, finish = on && s.ends() && s.whole();
+      // the slot's old score, on its way while the products run
+      float* out = nullptr;
+      float old = 0.0f;
+      if (finish) {
+        const int pg = p.c.page_of(s.i, t);
+        if (pg >= 0) {
+          out = p.scores + p.c.slot_row(pg, s.h, t);
+          if (p.decay != 0.0f) old = *out;
+        }
+      }
+      for (int c = s.q0; c < s.q0 + s.NQ; ++c) {
+        if (!(ok = wait_bar(&bars->l_full[r.st], r.ph, SITE_PAGED_SOFTMAX, 1))) break;
+        if (rt < s.tiles && c >= first) {
+          if (!(ok = wait_bar(&bars->s_full[rt], ns, SITE_PAGED_SOFTMAX, 2))) break;
+          ns ^= 1;
+          tc_fence_after();
+          const float* l2 = lse_s + r.st * 128;
+          const int cols = s.columns(c, p.log_p, p.log_g);
+          // columns below lo are of tokens before the key's own
+          const int lo = max(0, t - a - (c << p.log_p)) << p.log_g;
+          const bool masked =
+              cols < 128 || none_s[r.st] || s.slot0 + rt * kKeys + kKeys - 1 - a - (c << p.log_p) > 0;
+          const int chunks = max(1, (cols + 31) >> 5);
+          uint64_t acc0 = 0, acc1 = 0;  // packed fp32 pairs
+          uint32_t ra[32], rb[32];
+          auto sum = [&](uint32_t (&x)[32], int ch) {
+            if (!masked) {
+#pragma unroll
+              for (int cc = 0; cc < 32; cc += 4) {
+                const float4 lv = *reinterpret_cast<const float4*>(l2 + ch * 32 + cc);
+                const uint64_t x0 = fma2(pack2(__uint_as_float(x[cc]), __uint_as_float(x[cc + 1])), s2, pack2(lv.x, lv.y));
+                const uint64_t x1 = fma2(pack2(__uint_as_float(x[cc + 2]), __uint_as_float(x[cc + 3])), s2, pack2(lv.z, lv.w));
+                float e0, e1, e2, e3;
+                unpack2(x0, e0, e1);
+                unpack2(x1, e2, e3);
+                acc0 = add2(acc0, pack2(ex2_approx(e0), ex2_approx(e1)));
+                acc1 = add2(acc1, pack2(ex2_approx(e2), ex2_approx(e3)));
+              }
+            } else {
+              float m = 0.0f;
+#pragma unroll
+              for (int cc = 0; cc < 32; ++cc) {
+                const int col = ch * 32 + cc;
+                const float lv = l2[col], e = fmaf(__uint_as_float(x[cc]), p.scale_log2, lv);
+                m += col >= lo && col < cols && lv != neg_inf() ? ex2_approx(e) : 0.0f;
+              }
+              acc0 = add2(acc0, pack2(m, 0.0f));
+            }
+          };
+          tmem_ld32(tl, ra);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            if (ch >= chunks) break;
+            uint32_t(&cur)[32] = (ch & 1) ? rb : ra;
+            uint32_t(&nxt)[32] = (ch & 1) ? ra : rb;
+            tmem_wait_ld_dep(cur);
+            if (ch + 1 < chunks) {
+              if (ch < 3) tmem_ld32(tl + (ch + 1) * 32, nxt);
+            } else {  // all of the tile's columns are in registers: hand TMEM back
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->s_empty[rt]);
+            }
+            sum(cur, ch);
+          }
+          float y0, y1;
+          unpack2(add2(acc0, acc1), y0, y1);
+          total += y0 + y1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->l_empty[r.st]);
+        r.skip(1);
+      }
+      if (!ok) break;
+      if (finish) {
+        if (out) *out = p.decay != 0.0f ? fmaf(p.decay, old, total) : total;
+      } else if (on && s.ends()) {
+        p.part[((size_t)blockIdx.x * 2 + s.slot()) * kBlockKeys + row] = total;
+      }
+    }
   }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// The items that several of mass_kernel's CTAs shared: CTA x adds up the slots of the one whose
+// second CTA it names, in the order of the CTAs.
+__global__ void __launch_bounds__(kKeys) mass_merge(const __grid_constant__ MassParams p) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const Split s = p.split[blockIdx.x];
+  if (s.h < 0) return;
+  const int row = blockIdx.y * kKeys + threadIdx.x, t = s.block * kBlockKeys + row;
+  if (t >= p.c.len(s.i)) return;
+  const int pg = p.c.page_of(s.i, t);
+  if (pg < 0) return;
+  float* out = p.scores + p.c.slot_row(pg, s.h, t);
+  const float old = p.decay != 0.0f ? *out : 0.0f;
+  const int c0 = blockIdx.x - 1;
+  float total = 0.0f;
+#pragma unroll 8
+  for (int c = c0; c <= s.c1; ++c)  // the item begins in c0's share
+    total += p.part[((size_t)c * 2 + (c == c0 ? 1 : 0)) * kBlockKeys + row];
+  *out = p.decay != 0.0f ? fmaf(p.decay, old, total) : total;
+}
+
+// A bound on the units of a call, and the CTAs of mass_kernel.
+int max_ctas(int T, int n, int G, int H, long long slots) {
+  const long long units = ((long long)T * G / 128 + (long long)n * (1 + kSetup)) * H * ((slots + kBlockKeys - 1) / kBlockKeys);
+  return (int)min((long long)num_sms(), units);
+}
+size_t part_offset(int ctas) { return ((size_t)ctas * sizeof(Split) + 255) / 256 * 256; }
+
+template <int D>
+kvpop_status launch(MassParams& prm, int ctas, cudaStream_t cs) {
+  using L = Layout<D>;
+  auto kern = mass_kernel<D>;
+  kvpop_status st = KVPOP_OK;
+  static std::atomic<uint64_t> ready{0};  // bit d: the kernel is set up on device d
+  const int dev = current_device();
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total),
+                    "kvpop_paged_mass: smem attribute");
+    if (st != KVPOP_OK) return st;
+    // the register re-split must fit in the launch allocation (granule: 8 per thread)
+    cudaFuncAttributes fa;
+    st = cuda_check(cudaFuncGetAttributes(&fa, kern), "kvpop_paged_mass: attributes");
+    if (st != KVPOP_OK) return st;
+    if (((fa.numRegs + 7) / 8) * 8 < kRegsNeeded) {
+      set_last_error("kvpop_paged_mass: kernel built with %d registers per thread, %d needed", fa.numRegs, kRegsNeeded);
+      return KVPOP_ERR_INTERNAL;
+    }
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  st = cuda_check(launch_pdl(kern, dim3(ctas), dim3(kThreads), L::total, cs, prm), "kvpop_paged_mass: launch");
+  if (st != KVPOP_OK) return st;
+  return cuda_check(launch_pdl(mass_merge, dim3(ctas, kTiles), dim3(kKeys), 0, cs, prm), "kvpop_paged_mass: merge launch");
 }
 
 }  // namespace
@@ -61,7 +657,8 @@ extern "C" kvpop_status kvpop_paged_mass_workspace_size(int T, int n, int Hq, in
   }
   kvpop_status st = paged_check_rows(name, T, n, Hq, H, D, max_pages, page);
   if (st != KVPOP_OK) return st;
-  *bytes = 256;
+  const int ctas = max_ctas(T, n, Hq / H, H, (long long)max_pages * page);
+  *bytes = part_offset(ctas) + (size_t)ctas * 2 * kBlockKeys * 4;
   return KVPOP_OK;
 }
 
@@ -93,22 +690,30 @@ extern "C" kvpop_status kvpop_paged_mass(const void* q, const float* lse, int T,
     set_last_error("%s: q must be 16-byte, lse and scores 4-byte, workspace 256-byte aligned", name);
     return KVPOP_ERR_UNSUPPORTED;
   }
-  prm.q = (const __nv_bfloat16*)q;
-  prm.k = (const __nv_bfloat16*)kp;
+  const int G = Hq / H, box = min(page, kKeys);
+  // a decode step's rows lie alone: their boxes take no other sequence's along
+  const int tokens = cu ? 128 / G : 1;
+  const uint64_t dq[4] = {(uint64_t)D, (uint64_t)Hq, (uint64_t)T, 1};
+  const uint64_t sq[3] = {(uint64_t)D * 2, (uint64_t)Hq * D * 2, (uint64_t)T * Hq * D * 2};
+  const uint32_t bq[4] = {64, (uint32_t)G, (uint32_t)tokens, 1};
+  const uint64_t dk[4] = {(uint64_t)D, (uint64_t)page, (uint64_t)H, (uint64_t)pages};
+  const uint64_t sk[3] = {(uint64_t)D * 2, (uint64_t)page * D * 2, (uint64_t)kp_stride * 2};
+  const uint32_t bk[4] = {64, (uint32_t)box, 1, 1};
+  if (!make_tmap_4d(&prm.tq, q, dq, sq, bq) || !make_tmap_4d(&prm.tk, kp, dk, sk, bk)) return KVPOP_ERR_CUDA;
+  const int ctas = max_ctas(T, n, G, H, (long long)max_pages * page);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   prm.lse = lse;
-  prm.k_stride = kp_stride;
   prm.scores = scores;
+  prm.split = reinterpret_cast<Split*>(ws);
+  prm.part = reinterpret_cast<float*>(ws + part_offset(ctas));
   prm.Hq = Hq;
-  prm.G = Hq / H;
-  prm.scale = scale > 0.0f ? scale : 1.0f / sqrtf((float)D);
+  prm.G = G;
+  prm.log_g = 0;
+  while ((1 << prm.log_g) < G) ++prm.log_g;
+  prm.log_p = 7 - prm.log_g;
+  prm.q_bytes = tokens * G * 128;
+  prm.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
   prm.decay = decay;
-  if ((long long)n * H > 65535) {
-    set_last_error("%s: n * H above 65535", name);
-    return KVPOP_ERR_UNSUPPORTED;
-  }
-  const dim3 grid((unsigned)min(1024ll, ((long long)max_pages * page + kThreads - 1) / kThreads), n * H);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_check(D == 128 ? launch_pdl(mass_simple<128>, grid, dim3(kThreads), 0, cs, prm)
-                             : launch_pdl(mass_simple<64>, grid, dim3(kThreads), 0, cs, prm),
-                    "kvpop_paged_mass: launch");
+  return D == 128 ? launch<128>(prm, ctas, cs) : launch<64>(prm, ctas, cs);
 }

@@ -336,6 +336,10 @@ def test_overlapping_sequences_are_reported():
     kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, cu, out=(O, lse))
     assert kvpop.device_status(reset=True)[0] == 1
     assert (O == 3.0).all() and (lse == 3.0).all()
+    before = c.scores.clone()
+    kvpop.paged_mass(q, lse, c.kp, c.scores, c.table, c.lens, cu)
+    assert kvpop.device_status(reset=True)[0] == 1
+    assert torch.equal(c.scores, before)
 
 
 @pytest.mark.parametrize("bad", [-1, 1 << 30, 9])
