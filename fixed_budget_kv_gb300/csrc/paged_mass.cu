@@ -38,12 +38,14 @@ constexpr int kTiles = 4;  // tiles of K in a block
 constexpr int kThreads = (4 + 4 * kTiles) * 32;
 constexpr int kKeys = 128, kBlockKeys = kTiles * kKeys;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
+constexpr int kBoxes = kKeys / kMinPage;  // of a tile, at most
+static_assert(kTiles * kBoxes == 32, "one table entry a lane");
 // Loading a block of K and changing over to it, in query tiles.
 constexpr int kSetup = 2;
 constexpr int kSegs = 4;
 // Query tiles of a segment at most: keeps the waits that last one far below their limit.
 constexpr int kRunTiles = 256;
-constexpr int kLseStages = 4;
+constexpr int kLseStages = 3;
 // Register split: warps 0-3 drop to kRegsIo, the summing warpgroups rise to kRegsSum.
 constexpr int kRegsIo = 64;
 constexpr int kRegsSum = 104;
@@ -99,6 +101,9 @@ struct __align__(16) Seg {
   int i, h, slot0, len;
   int q0, NQ, lo, c;
   int tiles, flags, pad[2];  // tiles of K that a query tile of the segment sees
+  // [tile][box] pages, as the table has them: a box is a page, or 128 slots of one.  One past the
+  // last page where there is no slot
+  int pages[kTiles * kBoxes];
   // the first of the block's query tiles here; the last of them here
   __device__ __forceinline__ bool begins() const { return flags & 1; }
   __device__ __forceinline__ bool ends() const { return flags & 2; }
@@ -201,21 +206,12 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     if (lane == 0) fail(site, detail);
     return false;
   };
-  // segment n, once the walker has written it; false at the end of the work
-  auto get_seg = [&](int n, Seg& s, int site) -> bool {
-    if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, site, 9)) return false;
-    s = segs[n % kSegs];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
-    return s.NQ > 0;
-  };
 
   if (warp < 4) {
     setmaxnreg_dec<kRegsIo>();
     if (warp == 0) {
       // ------------------------------------------------------------ K producer
-      // Lane (box, half) issues its part of a tile: boxes of a page, or of 128 slots of one, of
-      // 64 columns.  The table entries of a segment are read before the loads of the one before.
+      // Lane (box, half) issues its part of a tile: 64 columns of a box.
       if (lane == 0) tma_prefetch_desc(&p.tk);
       const int log_box = min(p.c.log_page, 7), boxes = kKeys >> log_box;
       const int box = lane / DH, dh = lane - box * DH;
@@ -223,41 +219,24 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       const uint32_t dst = dh * kBlockBytes + (box << log_box) * 128;
       Ring<NK> r;
       int loads = 0;
-      auto pages_of = [&](const Seg& s, int (&pg)[kTiles]) {
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          const int slot = s.slot0 + t * kKeys + (box << log_box);
-          pg[t] = p.c.pages;  // one past the last: zeros
-          if (mine && t < s.tiles && slot < s.len) {
-            const int x = p.c.page_of(s.i, slot);
-            if (x >= 0) pg[t] = x;
-            else if (dh == 0) report_page(p.c.status, s.i);
-          }
-        }
-      };
-      Seg s, next;
-      int pg[kTiles], pg_next[kTiles];
-      bool ok = true, more = get_seg(0, s, SITE_PAGED_PRODUCER);
-      if (more) pages_of(s, pg);
-      for (int n = 1; ok && more; ++n) {
-        more = get_seg(n, next, SITE_PAGED_PRODUCER);
-        if (more) pages_of(next, pg_next);
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          if (!ok || t >= s.tiles) break;
-          ok = wait_bar(&bars->k_empty[r.st], r.ph ^ 1, SITE_PAGED_PRODUCER, 1);
-          if (!ok) break;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, SITE_PAGED_PRODUCER, 9)) break;
+        const Seg& s = segs[n % kSegs];
+        if (s.NQ == 0) break;
+        for (int t = 0; t < s.tiles; ++t) {
+          const int pg = mine ? s.pages[t * kBoxes + box] : 0;
+          if (!(ok = wait_bar(&bars->k_empty[r.st], r.ph ^ 1, SITE_PAGED_PRODUCER, 1))) break;
           if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[r.st], L::kTile);
           __syncwarp();
           if (mine)
             tma_load_4d(smem + L::k_off + r.st * L::kTile + dst, &p.tk, &bars->k_full[r.st], dh * 64,
-                        (s.slot0 + t * kKeys + (box << log_box)) & ((1 << p.c.log_page) - 1), s.h, pg[t]);
+                        (s.slot0 + t * kKeys + (box << log_box)) & ((1 << p.c.log_page) - 1), s.h, pg);
           r.skip(1);
           ++loads;
         }
-        s = next;
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) pg[t] = pg_next[t];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
       }
       if (*abort_flag && lane == 0) {
         // given up: nobody has waited for the last loads, which must land before the CTA ends
@@ -274,29 +253,34 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       Ring<NK> base;
       Ring<NQS> q;
       uint32_t ns = 0;  // bit rt: parity of tile rt's next product
-      Seg s;
       bool ok = true;
-      for (int n = 0; ok && get_seg(n, s, SITE_PAGED_MMA); ++n) {
-        int first[kTiles];
+      // warp reductions of equal values: the results are known to be uniform
+      auto uniform = [](int x) { return __reduce_max_sync(0xffffffffu, x); };
+      for (int n = 0; ok; ++n) {
+        if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, SITE_PAGED_MMA, 9)) break;
+        const Seg& s = segs[n % kSegs];
+        int left = uniform(s.NQ), cols = uniform(s.columns(s.q0, p.log_p, p.log_g));
+        const int tiles = uniform(s.tiles), last = uniform(s.columns(s.q0 + s.NQ - 1, p.log_p, p.log_g));
+        int hidden[kTiles];  // query tiles that do not see tile rt
 #pragma unroll
-        for (int rt = 0; rt < kTiles; ++rt) first[rt] = s.first(rt, p.log_p);
+        for (int rt = 0; rt < kTiles; ++rt) hidden[rt] = uniform(s.first(rt, p.log_p) - s.q0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
+        if (left == 0) break;
         uint32_t have = 0;  // bit rt: tile rt has landed
-        for (int c = s.q0; ok && c < s.q0 + s.NQ; ++c) {
-          ok = wait_bar(&bars->q_full[q.st], q.ph, SITE_PAGED_MMA, 1);
-          if (!ok) break;
-          const uint32_t cols = max(32, (s.columns(c, p.log_p, p.log_g) + 31) & ~31);
-          const uint32_t idesc = idesc_bf16(128, 0, 0) | (cols >> 3) << 17;
+        for (; ok && left > 0; --left) {
+          if (left == 1) cols = last;  // only a chunk's last tile has fewer
+          if (!(ok = wait_bar(&bars->q_full[q.st], q.ph, SITE_PAGED_MMA, 1))) break;
+          const uint32_t idesc = idesc_bf16(128, 0, 0) | (uint32_t)max(4, ((cols + 31) & ~31) >> 3) << 17;
           Ring<NK> k = base;
 #pragma unroll
           for (int rt = 0; rt < kTiles; ++rt) {
-            if (rt >= s.tiles) break;
-            if (c >= first[rt]) {
+            if (rt < tiles && hidden[rt] <= 0) {
               if (!(have >> rt & 1)) {
-                ok = wait_bar(&bars->k_full[k.st], k.ph, SITE_PAGED_MMA, 2);
+                if (!(ok = wait_bar(&bars->k_full[k.st], k.ph, SITE_PAGED_MMA, 2))) break;
                 have |= 1u << rt;
               }
-              ok = ok && wait_bar(&bars->s_empty[rt], (ns >> rt & 1) ^ 1, SITE_PAGED_MMA, 3);
-              if (!ok) break;
+              if (!(ok = wait_bar(&bars->s_empty[rt], (ns >> rt & 1) ^ 1, SITE_PAGED_MMA, 3))) break;
               ns ^= 1u << rt;
               tc_fence_after();
               const uint32_t a0 = k_lo + k.st * (L::kTile / 16), b0 = q_lo + q.st * (L::kTile / 16);
@@ -306,14 +290,15 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 mma_ss_elect(tbase + 128 * rt, a0 + off, b0 + off, idesc, ks > 0 ? 1u : 0u);
               }
               mma_commit_elect(&bars->s_full[rt]);
-              if (c == s.q0 + s.NQ - 1) mma_commit_elect(&bars->k_empty[k.st]);
+              if (left == 1) mma_commit_elect(&bars->k_empty[k.st]);
             }
+            --hidden[rt];
             k.skip(1);
           }
           mma_commit_elect(&bars->q_empty[q.st]);
           q.skip(1);
         }
-        base.skip(s.tiles);
+        base.skip(tiles);
       }
       // drain every issued MMA before teardown
       mma_commit_elect(&bars->drain);
@@ -324,9 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       Ring<NQS> q;
       Ring<kLseStages> r;
       int loads = 0;
-      Seg s;
       bool ok = true;
-      for (int n = 0; ok && get_seg(n, s, SITE_PAGED_PRODUCER); ++n) {
+      for (int n = 0; ok; ++n) {
+        if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, SITE_PAGED_PRODUCER, 9)) break;
+        const Seg& s = segs[n % kSegs];
+        if (s.NQ == 0) break;
         // rows 4 lane .. 4 lane + 3 of query tile c: -lse in log2 units; -inf adds nothing
         float x[4];
         auto read = [&](int c) {
@@ -366,6 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           if (lane == 0) mbar_arrive(&bars->l_full[r.st]);
           r.skip(1);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
       }
       if (*abort_flag && lane == 0) {  // as for K
         for (int i = 0; i < min(loads, NQS); ++i) {
@@ -375,7 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       }
     } else {
       // ------------------------------------------------------------ the CTA's share
-      // lane l holds sequence j0 + l of a window of 32, and its first unit
+      // lane l holds sequence j0 + l of a window of 32, and its first unit.  The walker also reads the
+      // table, segments ahead of the others
+      const int log_box = min(p.c.log_page, 7);
       int U = 0, members = 0, j0 = 0, base = 0;
       Seq g;
       auto window = [&](int w0, int at) {  // sequences w0 .., the first of them at unit `at`; returns the unit after
@@ -419,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       }
       bool own = false;  // this CTA began the item that u is in
       for (int n = 0;; ++n) {
-        Seg s = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, {0, 0}};  // NQ = 0 ends the work
+        Seg s = {};  // NQ = 0 ends the work
         while (u < end && s.NQ == 0) {
           // the sequence that holds unit u: the last of the window that begins at or before it
           unsigned at = __ballot_sync(0xffffffffu, g.units > 0 && base <= u && u < base + g.units);
@@ -472,11 +463,25 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           u += stop - off;
         }
         if (n == 0 && lane == 0) p.split[blockIdx.x] = split;
-        if (!wait_bar(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, SITE_PAGED_PRODUCER, 4)) break;
-        if (lane == 0) {
-          segs[n % kSegs] = s;
-          mbar_arrive(&bars->seg_full[n % kSegs]);
+        int pg = p.c.pages;
+        const int slot = s.slot0 + lane / kBoxes * kKeys + (lane % kBoxes << log_box);
+        if (lane / kBoxes < s.tiles && lane % kBoxes < kKeys >> log_box && slot < s.len) {
+          pg = p.c.page_of(s.i, slot);
+          if (pg < 0) {
+            report_page(p.c.status, s.i);
+            pg = p.c.pages;
+          }
         }
+        if (!wait_bar(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, SITE_PAGED_PRODUCER, 4)) break;
+        segs[n % kSegs].pages[lane] = pg;
+        if (lane == 0) {
+          Seg& to = segs[n % kSegs];
+          to.i = s.i, to.h = s.h, to.slot0 = s.slot0, to.len = s.len;
+          to.q0 = s.q0, to.NQ = s.NQ, to.lo = s.lo, to.c = s.c;
+          to.tiles = s.tiles, to.flags = s.flags;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->seg_full[n % kSegs]);
         if (s.NQ == 0) break;
       }
     }
@@ -491,9 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     float total = 0.0f;
     uint32_t ns = 0;  // parity of this tile's next product
     Ring<kLseStages> r;
-    Seg s;
     bool ok = true;
-    for (int n = 0; ok && get_seg(n, s, SITE_PAGED_SOFTMAX); ++n) {
+    for (int n = 0; ok; ++n) {
+      if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, SITE_PAGED_SOFTMAX, 9)) break;
+      const Seg& s = segs[n % kSegs];
+      if (s.NQ == 0) break;
       if (s.begins()) total = 0.0f;
       const int t = s.slot0 + row, a = s.len - s.c, first = s.first(rt, p.log_p);
       const bool on = t < s.len, finish = on && s.ends() && s.whole();
@@ -501,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       float* out = nullptr;
       float old = 0.0f;
       if (finish) {
-        const int pg = p.c.page_of(s.i, t);
-        if (pg >= 0) {
+        const int pg = segs[n % kSegs].pages[rt * kBoxes + ((row & (kKeys - 1)) >> min(p.c.log_page, 7))];
+        if (pg < p.c.pages) {
           out = p.scores + p.c.slot_row(pg, s.h, t);
           if (p.decay != 0.0f) old = *out;
         }
@@ -519,11 +526,22 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           const int lo = max(0, t - a - (c << p.log_p)) << p.log_g;
           const bool masked =
               cols < 128 || none_s[r.st] || s.slot0 + rt * kKeys + kKeys - 1 - a - (c << p.log_p) > 0;
-          const int chunks = max(1, (cols + 31) >> 5);
           uint64_t acc0 = 0, acc1 = 0;  // packed fp32 pairs
           uint32_t ra[32], rb[32];
-          auto sum = [&](uint32_t (&x)[32], int ch) {
-            if (!masked) {
+          auto hand_back = [&]() {  // all of the tile's columns are in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->s_empty[rt]);
+          };
+          tmem_ld32(tl, ra);
+          if (!masked) {
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t(&x)[32] = (ch & 1) ? rb : ra;
+              uint32_t(&nxt)[32] = (ch & 1) ? ra : rb;
+              tmem_wait_ld_dep(x);
+              if (ch < 3) tmem_ld32(tl + (ch + 1) * 32, nxt);
+              else hand_back();
 #pragma unroll
               for (int cc = 0; cc < 32; cc += 4) {
                 const float4 lv = *reinterpret_cast<const float4*>(l2 + ch * 32 + cc);
@@ -535,32 +553,23 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 acc0 = add2(acc0, pack2(ex2_approx(e0), ex2_approx(e1)));
                 acc1 = add2(acc1, pack2(ex2_approx(e2), ex2_approx(e3)));
               }
-            } else {
-              float m = 0.0f;
+            }
+          } else {
+            const int chunks = max(1, (cols + 31) >> 5);
+            float m = 0.0f;
+#pragma unroll 1
+            for (int ch = 0; ch < chunks; ++ch) {
+              tmem_wait_ld_dep(ra);
+              if (ch + 1 == chunks) hand_back();
 #pragma unroll
               for (int cc = 0; cc < 32; ++cc) {
                 const int col = ch * 32 + cc;
-                const float lv = l2[col], e = fmaf(__uint_as_float(x[cc]), p.scale_log2, lv);
+                const float lv = l2[col], e = fmaf(__uint_as_float(ra[cc]), p.scale_log2, lv);
                 m += col >= lo && col < cols && lv != neg_inf() ? ex2_approx(e) : 0.0f;
               }
-              acc0 = add2(acc0, pack2(m, 0.0f));
+              if (ch + 1 < chunks) tmem_ld32(tl + (ch + 1) * 32, ra);
             }
-          };
-          tmem_ld32(tl, ra);
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            if (ch >= chunks) break;
-            uint32_t(&cur)[32] = (ch & 1) ? rb : ra;
-            uint32_t(&nxt)[32] = (ch & 1) ? ra : rb;
-            tmem_wait_ld_dep(cur);
-            if (ch + 1 < chunks) {
-              if (ch < 3) tmem_ld32(tl + (ch + 1) * 32, nxt);
-            } else {  // all of the tile's columns are in registers: hand TMEM back
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars->s_empty[rt]);
-            }
-            sum(cur, ch);
+            acc0 = pack2(m, 0.0f);
           }
           float y0, y1;
           unpack2(add2(acc0, acc1), y0, y1);
@@ -576,6 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       } else if (on && s.ends()) {
         p.part[((size_t)blockIdx.x * 2 + s.slot()) * kBlockKeys + row] = total;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
     }
   }
 
