@@ -1,8 +1,9 @@
 // The checks that the kvpop_paged_* calls share, and kvpop_paged_append: new tokens' keys
 // and values into the pages.
 //
-// Row r of a sequence with c new tokens goes to slot len - c + r.  A warp takes one row of one
-// KV head: 16-byte pieces of k and v, and the slot's score.  Bound by memory: 8 D bytes a row.
+// Row r of a sequence with c new tokens goes to slot len - c + r.  A warp takes a token's k and v
+// of up to kHeads (D = 128) or twice as many heads: all 16-byte pieces are on their way before the
+// slot is looked up.  Bound by memory: 8 D bytes a token and head.
 #include <string.h>
 
 #include "paged.cuh"
@@ -100,6 +101,7 @@ kvpop_status paged_check_cache(const char* name, const char* which, const void* 
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 8;  // rows of k or v that a lane has in flight
 
 struct AppendParams {
   Paged c;
@@ -127,11 +129,23 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   grid_dep_wait();
   grid_dep_launch();
   const Paged& c = p.c;
-  const int ch = c.D / 8;  // pieces of a row
-  const long long rows = (long long)c.T * c.H;
-  for (long long w = (long long)blockIdx.x * (kThreads / 32) + warp_id(); w < rows;
+  const int ch = c.D / 8, lane = lane_id();  // pieces of a row
+  // D = 128: half of the lanes take a row of k, half one of v; D = 64: two rows of each
+  const int x = lane % ch, sub = lane / ch % (16 / ch);
+  const bool is_v = lane >= 16;
+  const uint4* from = is_v ? p.v_new : p.k_new;
+  uint4* to = is_v ? p.v : p.k;
+  const int64_t from_stride = is_v ? p.v_new_stride : p.k_new_stride, to_stride = is_v ? p.v_stride : p.k_stride;
+  const int rows = 16 / ch, heads = kHeads * rows, groups = (c.H + heads - 1) / heads;
+  const long long items = (long long)c.T * groups;
+  for (long long w = (long long)blockIdx.x * (kThreads / 32) + warp_id(); w < items;
        w += (long long)gridDim.x * (kThreads / 32)) {
-    const int row = (int)(w / c.H), h = (int)(w - (long long)row * c.H);
+    const int row = (int)(w / groups), h0 = (int)(w - (long long)row * groups) * heads + sub;
+    // the new rows do not depend on where they go
+    uint4 y[kHeads];
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u)
+      if (h0 + u * rows < c.H) y[u] = from[row * from_stride + (size_t)(h0 + u * rows) * ch + x];
     const int i = sequence_of(c, row);
     if (i < 0) continue;
     const int lo = c.lo(i), hi = c.hi(i, lo);
@@ -139,14 +153,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     if (t < 0 || t >= len) continue;  // more new tokens than slots: the first of them have none
     const int pg = c.page_of(i, t);
     if (pg < 0) {
-      if (lane_id() == 0) report_page(c.status, i);
+      if (lane == 0) report_page(c.status, i);
       continue;
     }
-    const size_t at = (((size_t)h << c.log_page) + (t & ((1 << c.log_page) - 1))) * ch;
-    const int x = lane_id() % ch;
-    if (lane_id() < ch) p.k[pg * p.k_stride + at + x] = p.k_new[row * p.k_new_stride + (size_t)h * ch + x];
-    if (lane_id() >= 32 - ch) p.v[pg * p.v_stride + at + x] = p.v_new[row * p.v_new_stride + (size_t)h * ch + x];
-    if (p.scores && lane_id() == 0) p.scores[c.slot_row(pg, h, t)] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+      const int h = h0 + u * rows;
+      if (h < c.H) {
+        to[pg * to_stride + (((size_t)h << c.log_page) + (t & ((1 << c.log_page) - 1))) * ch + x] = y[u];
+        if (p.scores && !is_v && x == 0) p.scores[c.slot_row(pg, h, t)] = 0.0f;
+      }
+    }
   }
 }
 
@@ -188,8 +205,9 @@ extern "C" kvpop_status kvpop_paged_append(const void* k_new, int64_t k_new_stri
   prm.k_stride = kp_stride / 8;
   prm.v_stride = vp_stride / 8;
   prm.scores = scores;
-  const long long rows = (long long)T * H;
-  const int blocks = (int)min((rows + kThreads / 32 - 1) / (kThreads / 32), 8ll * num_sms());
+  const int heads = kHeads * (128 / D);
+  const long long items = (long long)T * ((H + heads - 1) / heads);
+  const int blocks = (int)min((items + kThreads / 32 - 1) / (kThreads / 32), 8ll * num_sms());
   return cuda_check(launch_pdl(append_kernel, dim3(blocks), dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), prm),
                     "kvpop_paged_append: launch");
 }
