@@ -6,8 +6,9 @@
 //
 // evict_select, one cluster a (sequence, head), its CTAs a part of the slots each: the k-th best
 // score by a radix select (11 + 11 + 10 bits of an order-preserving key, the CTAs' histograms
-// added up through distributed shared memory), then the kept slots in their order: a thread has
-// consecutive slots, so one scan gives every thread its place.  Bound by its chain of barriers.
+// added up through distributed shared memory; the keys that share the first digit are set aside
+// for the others), then the kept slots in their order: a thread has consecutive slots, so one scan
+// gives every thread its place.  Bound by its chain of barriers.
 // evict_move: kept slot j goes from kept[j] >= j to j.  One CTA moves one column slice of K or V
 // (or the scores) of a head in rising order, a batch at a time: loads, barrier, stores.  The next
 // batch's sources lie at or above its own slots, so behind everything stored before: nothing is
@@ -21,6 +22,7 @@ namespace kvpop {
 namespace {
 
 constexpr int kBins = 2048;
+constexpr int kTied = 2048;  // keys with the first digit of the k-th best that are set aside, at most
 constexpr int kCacheKeys = 49152;  // keys of a CTA's part held in shared memory, at most
 constexpr int kMaxCluster = 8;
 constexpr int kMoveThreads = 256;
@@ -71,15 +73,18 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_s) {
 }
 
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) evict_select(const __grid_constant__ EvictParams p) {
-  static_assert(THREADS / 32 <= 32 && kBins % THREADS == 0, "one warp holds the warps' sums");
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(const __grid_constant__ EvictParams p) {
+  static_assert(THREADS / 32 <= 32 && 1024 % THREADS == 0, "one warp holds the warps' sums; whole bins a thread");
   extern __shared__ __align__(16) uint32_t keys_s[];  // the part's keys, if they fit
-  __shared__ uint32_t hist[kBins], total[kBins];
+  __shared__ uint32_t hists[2][kBins], total[kBins];  // a pass counts in one while the next one's is cleared
+  __shared__ uint32_t tied[kTied];                    // keys that share the first digit of the k-th best
   __shared__ uint32_t warp_s[THREADS / 32];
   __shared__ uint32_t found[2];   // the bin of the k-th best, and how many of it stay
   __shared__ uint32_t counts[2];  // keys of this part above the k-th best, and equal to it
+  __shared__ uint32_t ntied;
   const int tid = threadIdx.x;
-  for (int b = tid; b < kBins; b += THREADS) hist[b] = 0;
+  for (int b = tid; b < kBins; b += THREADS) hists[0][b] = 0;
+  if (tid == 0) ntied = 0;
   grid_dep_wait();
   grid_dep_launch();
   const Paged& c = p.c;
@@ -98,71 +103,41 @@ __global__ void __launch_bounds__(THREADS) evict_select(const __grid_constant__ 
   const int end = len - p.w, first = p.s & ~3, groups = (end - first + 3) / 4;
   const int g0 = (int)((long long)groups * rank / CS), g1 = (int)((long long)groups * (rank + 1) / CS);
   const bool held = (g1 - g0) * 4 <= p.held;
-  // the page of group g < g1; 0 and a report where the table names none
-  auto page_at = [&](int g, bool& bad) -> int {
-    const int pg = g < g1 ? c.table[(size_t)i * c.max_pages + ((first + 4 * g) >> c.log_page)] : 0;
-    bad = pg < 0 || pg >= c.pages;
-    return bad ? 0 : pg;
-  };
-  auto keys_at = [&](int g, int pg, bool bad) -> uint4 {
+  const int32_t* table = c.table + (size_t)i * c.max_pages;
+  // group g's keys; a table entry that names no page: the worst
+  auto keys_at = [&](int g, int pg) -> uint4 {
     float4 x = make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
-    if (g < g1 && !bad) x = *reinterpret_cast<const float4*>(p.scores + c.slot_row(pg, h, first + 4 * g));
+    if ((unsigned)pg < (unsigned)c.pages) x = *reinterpret_cast<const float4*>(p.scores + c.slot_row(pg, h, first + 4 * g));
     return make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
   };
   auto keys_of = [&](int g) -> uint4 {
-    if (held) return reinterpret_cast<const uint4*>(keys_s)[g - g0];
-    bool bad;
-    const int pg = page_at(g, bad);
-    return keys_at(g, pg, bad);
+    return held ? reinterpret_cast<const uint4*>(keys_s)[g - g0] : keys_at(g, table[(first + 4 * g) >> c.log_page]);
   };
-  auto free_slot = [&](int t) { return t >= p.s && t < end; };
-  uint32_t prefix = 0, mask = 0, need = p.top;
-  // one warp's groups into the histogram
-  auto count = [&](int g, const uint4& x, int shift, int bins) {
-    const uint32_t key[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const bool on = g < g1 && free_slot(first + 4 * g + u) && (key[u] & mask) == prefix;
-      const uint32_t bin = (key[u] >> shift) & (bins - 1);
-      // many equal scores (nothing received yet): one addition for the whole warp
-      const unsigned act = __ballot_sync(0xffffffffu, on);
-      if (act == 0) continue;
-      const int lead = __ffs(act) - 1;
-      const uint32_t ref = __shfl_sync(0xffffffffu, bin, lead);
-      if (__all_sync(0xffffffffu, !on || bin == ref)) {
-        if (lane_id() == lead) atomicAdd(&hist[bin], (uint32_t)__popc(act));
-      } else if (on) {
-        atomicAdd(&hist[bin], 1u);
-      }
-    }
+  // bit u: slot u of group g may go
+  auto free_slots = [&](int g) -> uint32_t {
+    const int t = first + 4 * g;
+    uint32_t m = 15;
+    if (t < p.s) m &= 15u << (p.s - t);
+    if (t + 4 > end) m &= 15u >> (t + 4 - end);
+    return m;
   };
-  __syncthreads();
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-    if (pass == 0) {
-      // four groups a thread on their way at a time
-      for (int base = g0; base < g1; base += 4 * THREADS) {
-        int pg[4];
-        bool bad[4];
-        uint4 x[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) pg[v] = page_at(base + v * THREADS + tid, bad[v]);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x[v] = keys_at(base + v * THREADS + tid, pg[v], bad[v]);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int g = base + v * THREADS + tid;
-          if (bad[v]) report_page(c.status, i);
-          if (held && g < g1) reinterpret_cast<uint4*>(keys_s)[g - g0] = x[v];
-          count(g, x[v], shift, bins);
-        }
-      }
-    } else {
-      for (int base = g0; base < g1; base += THREADS) {
-        const int g = base + tid;
-        count(g, g < g1 ? keys_of(g) : make_uint4(0, 0, 0, 0), shift, bins);
-      }
+  // one warp's keys into a histogram, m: which of them
+  auto count = [&](uint32_t* hist, uint32_t m, const uint4& x, int shift, int bins) {
+    const uint32_t bin[4] = {x.x >> shift & bins - 1, x.y >> shift & bins - 1, x.z >> shift & bins - 1, x.w >> shift & bins - 1};
+    // many equal scores (nothing received yet): one addition for the whole warp
+    const uint32_t ref = __shfl_sync(0xffffffffu, bin[1], 16);
+    const bool same = m == 15 && bin[0] == ref && bin[1] == ref && bin[2] == ref && bin[3] == ref;
+    if (__all_sync(0xffffffffu, same)) {
+      if (lane_id() == 0) atomicAdd(&hist[ref], 128u);
+      return;
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (m >> u & 1) atomicAdd(&hist[bin[u]], 1u);
+  };
+  uint32_t prefix = 0, need = p.top;
+  // the bin of the k-th best from the counts of a pass, over the cluster
+  auto find = [&](const uint32_t* hist, int shift, int bins) {
     if (CS > 1) {
       // CTA r adds up its share of the bins over the cluster and hands the sums to all
       cluster_sync();
@@ -201,26 +176,88 @@ __global__ void __launch_bounds__(THREADS) evict_select(const __grid_constant__ 
     }
     __syncthreads();
     prefix |= found[0] << shift;
-    mask |= (uint32_t)(bins - 1) << shift;
     need = found[1];
-    if (pass < 2) {
-      // in a cluster every CTA has read it: the sums are out
-      for (int b = tid; b < kBins; b += THREADS) hist[b] = 0;
-      __syncthreads();
+  };
+  __syncthreads();
+  // first digit.  Four groups a thread on their way at a time
+  for (int base = g0; base < g1; base += 4 * THREADS) {
+    int pg[4];
+    uint4 x[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int g = base + v * THREADS + tid;
+      pg[v] = g < g1 ? table[(first + 4 * g) >> c.log_page] : -1;
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = keys_at(base + v * THREADS + tid, pg[v]);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int g = base + v * THREADS + tid;
+      if (base + v * THREADS + (tid & ~31) >= g1) break;  // nothing for this warp
+      if (g < g1) {
+        if ((unsigned)pg[v] >= (unsigned)c.pages) report_page(c.status, i);
+        if (held) reinterpret_cast<uint4*>(keys_s)[g - g0] = x[v];
+      }
+      count(hists[0], g < g1 ? free_slots(g) : 0, x[v], 21, 2048);
     }
   }
-  // prefix is the k-th best key, and `need` of its slots stay, the lowest ones
+  for (int b = tid; b < kBins; b += THREADS) hists[1][b] = 0;
+  find(hists[0], 21, 2048);
+  // the keys that share it, by themselves if they are not too many
+  auto ties = [&](int g, const uint4& x, int shift) -> uint32_t {
+    const uint32_t d = prefix >> shift;
+    return ((x.x >> shift == d) | (x.y >> shift == d) << 1 | (x.z >> shift == d) << 2 | (x.w >> shift == d) << 3) & free_slots(g);
+  };
+  for (int base = g0; base < g1; base += THREADS) {
+    const int g = base + tid;
+    if (g >= g1) break;
+    const uint4 x = keys_of(g);
+    const uint32_t m = ties(g, x, 21);
+    if (m) {
+      uint32_t at = atomicAdd(&ntied, (uint32_t)__popc(m));
+      const uint32_t key[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (m >> u & 1) {
+          if (at < kTied) tied[at] = key[u];
+          ++at;
+        }
+    }
+  }
+  for (int b = tid; b < kBins; b += THREADS) hists[0][b] = 0;
+  __syncthreads();
+  const bool few = ntied <= kTied;
+#pragma unroll 1
+  for (int pass = 1; pass < 3; ++pass) {
+    const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0, bins = pass == 1 ? 2048 : 1024;
+    uint32_t* hist = hists[pass & 1];
+    if (few) {
+      for (int k = tid; k < (int)ntied; k += THREADS)
+        if (tied[k] >> above == prefix >> above) atomicAdd(&hist[tied[k] >> shift & bins - 1], 1u);
+    } else {
+      for (int base = g0; base < g1; base += THREADS) {
+        const int g = base + tid;
+        const uint4 x = g < g1 ? keys_of(g) : make_uint4(0, 0, 0, 0);
+        count(hist, g < g1 ? ties(g, x, above) : 0, x, shift, bins);
+      }
+    }
+    find(hist, shift, bins);
+  }
+  // prefix is the k-th best key, and `need` of its slots stay, the lowest ones.  A thread has `per`
+  // consecutive groups; bits: slots of the first eight above the k-th best, and equal to it
   const int per = (g1 - g0 + THREADS - 1) / THREADS, ga = min(g1, g0 + tid * per), gb = min(g1, ga + per);
-  uint32_t above = 0, equal = 0;
+  uint32_t above = 0, equal = 0, bits_a = 0, bits_e = 0;
   for (int g = ga; g < gb; ++g) {
     const uint4 x = keys_of(g);
-    const uint32_t key[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (free_slot(first + 4 * g + u)) {
-        above += key[u] > prefix;
-        equal += key[u] == prefix;
-      }
+    const uint32_t m = free_slots(g);
+    const uint32_t a = ((x.x > prefix) | (x.y > prefix) << 1 | (x.z > prefix) << 2 | (x.w > prefix) << 3) & m;
+    const uint32_t e = ((x.x == prefix) | (x.y == prefix) << 1 | (x.z == prefix) << 2 | (x.w == prefix) << 3) & m;
+    above += __popc(a);
+    equal += __popc(e);
+    if (g - ga < 8) {
+      bits_a |= a << 4 * (g - ga);
+      bits_e |= e << 4 * (g - ga);
+    }
   }
   const uint32_t mine_above = above, mine_equal = equal;
   above = block_scan<THREADS>(above, warp_s);
@@ -243,18 +280,23 @@ __global__ void __launch_bounds__(THREADS) evict_select(const __grid_constant__ 
       equal += e[r];
     }
   }
-  if (mine_above + mine_equal > 0) {
+  auto keep = [&](bool is_above, int t) {
+    if (is_above || equal < need) kept[p.s + above + min(equal, need)] = t;
+    above += is_above;
+    equal += !is_above;
+  };
+  if (per <= 8) {
+    for (uint32_t m = bits_a | bits_e; m; m &= m - 1) {
+      const int u = __ffs(m) - 1;
+      keep(bits_a >> u & 1, first + 4 * ga + u);
+    }
+  } else if (mine_above + mine_equal > 0) {
     for (int g = ga; g < gb; ++g) {
       const uint4 x = keys_of(g);
-      const uint32_t key[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t key[4] = {x.x, x.y, x.z, x.w}, m = free_slots(g);
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (free_slot(first + 4 * g + u)) {
-          const bool stays = key[u] > prefix || (key[u] == prefix && equal < need);
-          if (stays) kept[p.s + above + min(equal, need)] = first + 4 * g + u;
-          above += key[u] > prefix;
-          equal += key[u] == prefix;
-        }
+        if ((m >> u & 1) && key[u] >= prefix) keep(key[u] > prefix, first + 4 * g + u);
     }
   }
   if (CS > 1) cluster_sync();  // nobody leaves while its counts are read
@@ -271,22 +313,32 @@ struct Moves {
 template <int BATCH, typename V, typename At>
 __device__ __forceinline__ void move_rows(const EvictParams& p, Moves& m, const int32_t* kept, int i, int per, V* base, At at) {
   const Paged& c = p.c;
+  const int32_t* table = c.table + (size_t)i * c.max_pages;
   const int rows = kMoveThreads / per, batch = rows * BATCH, r = threadIdx.x / per, x = threadIdx.x - r * per;
   auto resolve = [&](int j0, int buf) {
-    for (int k = threadIdx.x; k < batch; k += kMoveThreads) {
-      const int j = j0 + k, t = j < p.B ? kept[j] : -1;
-      int64_t src = -1, dst = -1;
-      if (t > j) {
-        const int a = c.page_of(i, t), b = c.page_of(i, j);
-        if (a >= 0 && b >= 0) {
-          src = at(a, t);
-          dst = at(b, j);
-        } else {
-          report_page(c.status, i);
-        }
-      }
-      m.src[buf][k] = src;
-      m.dst[buf][k] = dst;
+    // a thread's lookups together: one wait for the slots, one for their pages
+    constexpr int kLook = kMoveRows / kMoveThreads;
+    int t[kLook], from[kLook], to[kLook];
+#pragma unroll
+    for (int u = 0; u < kLook; ++u) {
+      const int k = threadIdx.x + u * kMoveThreads;
+      t[u] = k < batch && j0 + k < p.B ? kept[j0 + k] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kLook; ++u) {
+      const int j = j0 + threadIdx.x + u * kMoveThreads;
+      from[u] = t[u] > j ? table[t[u] >> c.log_page] : 0;
+      to[u] = t[u] > j ? table[j >> c.log_page] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kLook; ++u) {
+      const int k = threadIdx.x + u * kMoveThreads, j = j0 + k;
+      if (k >= batch) break;
+      const bool there = (unsigned)from[u] < (unsigned)c.pages && (unsigned)to[u] < (unsigned)c.pages;
+      if (!there) report_page(c.status, i);
+      const bool moves = t[u] > j && there;
+      m.src[buf][k] = moves ? at(from[u], t[u]) : -1;
+      m.dst[buf][k] = moves ? at(to[u], j) : -1;
     }
   };
   resolve(0, 0);
