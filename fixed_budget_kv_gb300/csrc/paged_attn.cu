@@ -472,54 +472,72 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         }
       }
       bool own = false;  // this CTA began the item that u is in
+      // the sequence, row block and head of the item that holds unit u, the item's units, and the
+      // first of them; looked up once and counted on
+      Seq q = {};
+      int seq = 0, rb = 0, h = 0, per = 0, at = 0;
+      bool known = false;
+      auto enter_block = [&]() {
+        // slots that its last row sees
+        const int sees = rb == q.nb - 1 ? q.len : q.len - q.c + (rb + 1) * p.toks;
+        per = max(1, (sees + kKeys - 1) / kKeys) + kSetup;
+      };
       for (int n = 0;; ++n) {
         Seg s = {0, 0, 0, 0, 0, 0, 0, 0, 0, {0, 0, 0}};  // NT = 0 ends the work
         while (u < end && s.NT == 0) {
-          // the sequence that holds unit u: the last of the window that begins at or before it
-          unsigned at = __ballot_sync(0xffffffffu, g.units > 0 && base <= u && u < base + g.units);
-          if (at == 0) {
-            window(j0 + 32, u);  // u is the window's end
-            continue;
+          if (!known) {
+            // the sequence: the one of the window whose units these are
+            const unsigned hit = __ballot_sync(0xffffffffu, g.units > 0 && base <= u && u < base + g.units);
+            if (hit == 0) {
+              window(j0 + 32, u);  // u is the window's end
+              continue;
+            }
+            const int l = __ffs(hit) - 1, b = __shfl_sync(0xffffffffu, base, l);
+            seq = j0 + l;
+            q.lo = __shfl_sync(0xffffffffu, g.lo, l);
+            q.c = __shfl_sync(0xffffffffu, g.c, l);
+            q.len = __shfl_sync(0xffffffffu, g.len, l);
+            q.nb = __shfl_sync(0xffffffffu, g.nb, l);
+            // the row block: the last that begins at or before the unit
+            int over = q.nb;
+            rb = 0;
+            while (over - rb > 1) {
+              const int mid = (rb + over) >> 1;
+              if ((long long)units_before(p, q, mid) * p.c.H <= u - b) rb = mid;
+              else over = mid;
+            }
+            enter_block();
+            at = b + units_before(p, q, rb) * p.c.H;
+            h = (u - at) / per;
+            at += h * per;
+            known = true;
           }
-          const int l = __ffs(at) - 1;
-          Seq q;
-          const int b = __shfl_sync(0xffffffffu, base, l);
-          q.lo = __shfl_sync(0xffffffffu, g.lo, l);
-          q.c = __shfl_sync(0xffffffffu, g.c, l);
-          q.len = __shfl_sync(0xffffffffu, g.len, l);
-          q.nb = __shfl_sync(0xffffffffu, g.nb, l);
-          // the row block: the last that begins at or before the unit
-          const int v = u - b;
-          int rb = 0, over = q.nb;
-          while (over - rb > 1) {
-            const int mid = (rb + over) >> 1;
-            if ((long long)units_before(p, q, mid) * p.c.H <= v) rb = mid;
-            else over = mid;
-          }
-          const int before = units_before(p, q, rb) * p.c.H;
-          const int a = q.len - q.c;
-          const int sees = rb == q.nb - 1 ? q.len : a + (rb + 1) * p.toks;  // slots that its last row sees
-          const int nt = max(1, (sees + kKeys - 1) / kKeys);
-          const int per = nt + kSetup, item = (v - before) / per, off = (v - before) - item * per;
           // this CTA's units of the item from here on, up to a run of tiles: [off, stop)
-          const int stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
+          const int off = u - at, stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
           s.kt0 = max(off - kSetup, 0);
           s.NT = max(stop - kSetup, 0) - s.kt0;
-          s.i = j0 + l;
-          s.h = item;
+          s.i = seq;
+          s.h = h;
           s.row0 = q.lo + rb * p.toks;
           s.nrow = min(p.toks, q.c - rb * p.toks) * p.G;
           s.len = q.len;
-          s.sees = a + rb * p.toks + 1;
+          s.sees = q.len - q.c + rb * p.toks + 1;
           const bool cont = s.kt0 > 0 && n > 0;
           own = s.kt0 == 0 || (cont && own);
           s.flags = (s.nrow > 128 ? 1 : 0) | (own && stop == per ? 2 : 0) | (own ? 4 : 0) | (cont ? 8 : 0);
           if (n == 0 && s.kt0 > 0) {
             // the work begins inside an item; the second of its CTAs leaves word of it
-            const int first = b + before + item * per + kSetup;
-            split = {s.row0, s.h, sh.cta_of(first) + 1 == (int)blockIdx.x ? s.nrow : 0, sh.cta_of(first + nt - 1)};
+            split = {s.row0, h, sh.cta_of(at + kSetup) + 1 == (int)blockIdx.x ? s.nrow : 0, sh.cta_of(at + per - 1)};
           }
           u += stop - off;
+          if (stop == per) {  // on to the next item
+            at += per;
+            if (++h == p.c.H) {
+              h = 0;
+              if (++rb == q.nb) known = false;
+              else enter_block();
+            }
+          }
         }
         if (n == 0 && lane == 0) p.split[blockIdx.x] = split;
         if (!warp_wait(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag)) {

@@ -409,45 +409,67 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         }
       }
       bool own = false;  // this CTA began the item that u is in
+      // the sequence, block of slots and head of the item that holds unit u, the block's units for
+      // one head, and the first of the item's; looked up once and counted on
+      Seq q = {};
+      int seq = 0, kb = 0, h = 0, per = 0, at = 0, pg = 0, seg_pg = 0;
+      bool known = false;
+      auto enter_block = [&]() {  // lane l reads a table entry of the block, for all of its heads
+        per = q.nq - first_tile(q.len - q.c, p.log_p, kb * kBlockKeys) + kSetup;
+        const int slot = kb * kBlockKeys + lane / kBoxes * kKeys + (lane % kBoxes << log_box);
+        pg = p.c.pages;
+        if (lane % kBoxes < kKeys >> log_box && slot < q.len) {
+          pg = p.c.page_of(seq, slot);
+          if (pg < 0) {
+            report_page(p.c.status, seq);
+            pg = p.c.pages;
+          }
+        }
+      };
       for (int n = 0;; ++n) {
         Seg s = {};  // NQ = 0 ends the work
         while (u < end && s.NQ == 0) {
-          // the sequence that holds unit u: the last of the window that begins at or before it
-          unsigned at = __ballot_sync(0xffffffffu, g.units > 0 && base <= u && u < base + g.units);
-          if (at == 0) {
-            window(j0 + 32, u);  // u is the window's end
-            continue;
+          if (!known) {
+            // the sequence: the one of the window whose units these are
+            const unsigned hit = __ballot_sync(0xffffffffu, g.units > 0 && base <= u && u < base + g.units);
+            if (hit == 0) {
+              window(j0 + 32, u);  // u is the window's end
+              continue;
+            }
+            const int l = __ffs(hit) - 1, b = __shfl_sync(0xffffffffu, base, l);
+            seq = j0 + l;
+            q.lo = __shfl_sync(0xffffffffu, g.lo, l);
+            q.c = __shfl_sync(0xffffffffu, g.c, l);
+            q.len = __shfl_sync(0xffffffffu, g.len, l);
+            q.nb = __shfl_sync(0xffffffffu, g.nb, l);
+            q.nq = __shfl_sync(0xffffffffu, g.nq, l);
+            // the block: the last that begins at or before the unit
+            int over = q.nb;
+            kb = 0;
+            while (over - kb > 1) {
+              const int mid = (kb + over) >> 1;
+              if ((long long)units_before(p, q, mid) * p.c.H <= u - b) kb = mid;
+              else over = mid;
+            }
+            enter_block();
+            at = b + units_before(p, q, kb) * p.c.H;
+            h = (u - at) / per;
+            at += h * per;
+            known = true;
           }
-          const int l = __ffs(at) - 1;
-          Seq q;
-          const int b = __shfl_sync(0xffffffffu, base, l);
-          q.lo = __shfl_sync(0xffffffffu, g.lo, l);
-          q.c = __shfl_sync(0xffffffffu, g.c, l);
-          q.len = __shfl_sync(0xffffffffu, g.len, l);
-          q.nb = __shfl_sync(0xffffffffu, g.nb, l);
-          q.nq = __shfl_sync(0xffffffffu, g.nq, l);
-          // the block of slots: the last that begins at or before the unit
-          const int v = u - b;
-          int kb = 0, over = q.nb;
-          while (over - kb > 1) {
-            const int mid = (kb + over) >> 1;
-            if ((long long)units_before(p, q, mid) * p.c.H <= v) kb = mid;
-            else over = mid;
-          }
-          const int before = units_before(p, q, kb) * p.c.H;
-          s.i = j0 + l;
+          s.i = seq;
+          s.h = h;
           s.slot0 = kb * kBlockKeys;
           s.len = q.len;
           s.lo = q.lo;
           s.c = q.c;
-          const int q_lo = s.first(0, p.log_p);
-          const int per = q.nq - q_lo + kSetup, item = (v - before) / per, off = (v - before) - item * per;
+          const int q_lo = s.first(0, p.log_p), off = u - at;
           // this CTA's units of the item from here on, up to a run of query tiles: [off, stop)
           const int stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
           const int t0 = max(off - kSetup, 0), t1 = max(stop - kSetup, 0);
-          s.h = item;
           s.q0 = q_lo + t0;
           s.NQ = t1 - t0;
+          seg_pg = pg;
           s.tiles = 0;
           for (int rt = 0; rt < kTiles; ++rt)
             s.tiles += s.slot0 + rt * kKeys < s.len && s.first(rt, p.log_p) < q_lo + t1;
@@ -457,23 +479,22 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                     (own ? 8 : 0);
           if (n == 0 && t0 > 0) {
             // the work begins inside an item; the second of its CTAs leaves word of it
-            const int first = b + before + item * per + kSetup;
-            split = {s.i, sh.cta_of(first) + 1 == (int)blockIdx.x ? s.h : -1, kb, sh.cta_of(first + q.nq - q_lo - 1)};
+            const int first = at + kSetup;
+            split = {seq, sh.cta_of(first) + 1 == (int)blockIdx.x ? h : -1, kb, sh.cta_of(at + per - 1)};
           }
           u += stop - off;
-        }
-        if (n == 0 && lane == 0) p.split[blockIdx.x] = split;
-        int pg = p.c.pages;
-        const int slot = s.slot0 + lane / kBoxes * kKeys + (lane % kBoxes << log_box);
-        if (lane / kBoxes < s.tiles && lane % kBoxes < kKeys >> log_box && slot < s.len) {
-          pg = p.c.page_of(s.i, slot);
-          if (pg < 0) {
-            report_page(p.c.status, s.i);
-            pg = p.c.pages;
+          if (stop == per) {  // on to the next item
+            at += per;
+            if (++h == p.c.H) {
+              h = 0;
+              if (++kb == q.nb) known = false;
+              else if (u < end) enter_block();
+            }
           }
         }
+        if (n == 0 && lane == 0) p.split[blockIdx.x] = split;
         if (!wait_bar(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, SITE_PAGED_PRODUCER, 4)) break;
-        segs[n % kSegs].pages[lane] = pg;
+        segs[n % kSegs].pages[lane] = seg_pg;
         if (lane == 0) {
           Seg& to = segs[n % kSegs];
           to.i = s.i, to.h = s.h, to.slot0 = s.slot0, to.len = s.len;
