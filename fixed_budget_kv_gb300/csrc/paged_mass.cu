@@ -46,10 +46,6 @@ constexpr int kSegs = 4;
 // Query tiles of a segment at most: keeps the waits that last one far below their limit.
 constexpr int kRunTiles = 256;
 constexpr int kLseStages = 3;
-// Register split: warps 0-3 drop to kRegsIo, the summing warpgroups rise to kRegsSum.
-constexpr int kRegsIo = 64;
-constexpr int kRegsSum = 104;
-constexpr int kRegsNeeded = (128 * kRegsIo + (kThreads - 128) * kRegsSum + kThreads - 1) / kThreads;
 
 // An item that several CTAs share, and the last of them.  h = -1: none.
 struct __align__(16) Split {
@@ -100,7 +96,7 @@ __device__ __forceinline__ Seq sequence(const MassParams& p, int i) {
 struct __align__(16) Seg {
   int i, h, slot0, len;
   int q0, NQ, lo, c;
-  int tiles, flags, pad[2];  // tiles of K that a query tile of the segment sees
+  int tiles, flags, cmd, pad;  // tiles of K, all of which each of these query tiles sees
   // [tile][box] pages, as the table has them: a box is a page, or 128 slots of one.  One past the
   // last page where there is no slot
   int pages[kTiles * kBoxes];
@@ -111,8 +107,11 @@ struct __align__(16) Seg {
   __device__ __forceinline__ bool whole() const { return flags & 4; }
   // otherwise: 0 when an earlier CTA began the block, 1 when this one did
   __device__ __forceinline__ int slot() const { return flags >> 3 & 1; }
-  // the first query tile that sees tile rt, and the columns of query tile q
-  __device__ __forceinline__ int first(int rt, int log_p) const { return first_tile(len - c, log_p, slot0 + rt * kKeys); }
+  // NQ, tiles and the last query tile's columns in units of 32 in one word, for the issuer
+  __device__ __forceinline__ void pack(int log_p, int log_g) {
+    cmd = NQ | tiles << 10 | max(1, (columns(q0 + NQ - 1, log_p, log_g) + 31) >> 5) << 13;
+  }
+  // the columns of query tile q
   __device__ __forceinline__ int columns(int q, int log_p, int log_g) const {
     return max(0, min(1 << log_p, c - (q << log_p))) << log_g;
   }
@@ -131,8 +130,9 @@ struct Bars {
 template <int D>
 struct Layout {
   static constexpr int DH = D / 64;
-  static constexpr int NK = D == 128 ? 5 : 10;  // tiles of K
-  static constexpr int NQ = D == 128 ? 2 : 4;   // query tiles
+  static constexpr int KB = D == 128 ? 1 : 2;  // blocks of K: tile rt of one has a place of its own
+  static constexpr int NK = KB * kTiles;
+  static constexpr int NQ = D == 128 ? 3 : 5;  // query tiles
   static constexpr int kTile = DH * kBlockBytes;
   static constexpr int k_off = 0;
   static constexpr int q_off = k_off + NK * kTile;
@@ -208,7 +208,6 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   };
 
   if (warp < 4) {
-    setmaxnreg_dec<kRegsIo>();
     if (warp == 0) {
       // ------------------------------------------------------------ K producer
       // Lane (box, half) issues its part of a tile: 64 columns of a box.
@@ -217,92 +216,103 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       const int box = lane / DH, dh = lane - box * DH;
       const bool mine = box < boxes;
       const uint32_t dst = dh * kBlockBytes + (box << log_box) * 128;
-      Ring<NK> r;
-      int loads = 0;
+      uint32_t used = 0, ph = 0;  // places that hold a tile; parity of each place's next use
+      int kb = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
         if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, SITE_PAGED_PRODUCER, 9)) break;
         const Seg& s = segs[n % kSegs];
         if (s.NQ == 0) break;
         for (int t = 0; t < s.tiles; ++t) {
-          const int pg = mine ? s.pages[t * kBoxes + box] : 0;
-          if (!(ok = wait_bar(&bars->k_empty[r.st], r.ph ^ 1, SITE_PAGED_PRODUCER, 1))) break;
-          if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[r.st], L::kTile);
+          const int pg = mine ? s.pages[t * kBoxes + box] : 0, at = kb + t;
+          if (!(ok = wait_bar(&bars->k_empty[at], (ph >> at & 1) ^ 1, SITE_PAGED_PRODUCER, 1))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[at], L::kTile);
           __syncwarp();
           if (mine)
-            tma_load_4d(smem + L::k_off + r.st * L::kTile + dst, &p.tk, &bars->k_full[r.st], dh * 64,
+            tma_load_4d(smem + L::k_off + at * L::kTile + dst, &p.tk, &bars->k_full[at], dh * 64,
                         (s.slot0 + t * kKeys + (box << log_box)) & ((1 << p.c.log_page) - 1), s.h, pg);
-          r.skip(1);
-          ++loads;
+          ph ^= 1u << at;
+          used |= 1u << at;
         }
+        if (L::KB > 1) kb ^= kTiles;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
       }
       if (*abort_flag && lane == 0) {
         // given up: nobody has waited for the last loads, which must land before the CTA ends
-        for (int i = 0; i < min(loads, NK); ++i) {
-          const int seq = loads - 1 - i;
-          mbar_wait(&bars->k_full[seq % NK], (seq / NK) & 1, nullptr);
-        }
+        for (int i = 0; i < NK; ++i)
+          if (used >> i & 1) mbar_wait(&bars->k_full[i], (ph >> i & 1) ^ 1, nullptr);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      // The whole warp runs it, in step, and one elected lane issues (see paged_attn.cu).  Tile rt of
-      // a block has TMEM columns 128 rt ..; the products cover as many columns as the query tile has.
+      // One thread issues (a whole warp in step, as in paged_attn.cu: decode rows 139 us against 119,
+      // a window 61 against 53).  Tile rt of a block has TMEM columns 128 rt .. and places of its own;
+      // the products cover as many columns as the query tile has.
       const uint32_t k_lo = desc_lo(sbase + L::k_off, 16), q_lo = desc_lo(sbase + L::q_off, 16);
-      Ring<NK> base;
-      Ring<NQS> q;
-      uint32_t ns = 0;  // bit rt: parity of tile rt's next product
-      bool ok = true;
-      // warp reductions of equal values: the results are known to be uniform
-      auto uniform = [](int x) { return __reduce_max_sync(0xffffffffu, x); };
-      for (int n = 0; ok; ++n) {
-        if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, SITE_PAGED_MMA, 9)) break;
-        const Seg& s = segs[n % kSegs];
-        int left = uniform(s.NQ), cols = uniform(s.columns(s.q0, p.log_p, p.log_g));
-        const int tiles = uniform(s.tiles), last = uniform(s.columns(s.q0 + s.NQ - 1, p.log_p, p.log_g));
-        int hidden[kTiles];  // query tiles that do not see tile rt
+      if (lane == 0) {
+        // It waits for the tensor core wherever the short queue is full, so whatever it does between
+        // products counts: a segment is one word, read while the first product of the one before runs.
+        Ring<NQS> q;
+        uint32_t ns = 0, ph = 0;  // bit: parity of a tile's next product, and of a place's next tile of K
+        int kb = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity, int detail) -> bool {
+          if (mbar_wait(bar, parity, abort_flag)) return true;
+          fail(SITE_PAGED_MMA, detail);
+          return ok = false;
+        };
+        auto fetch = [&](int n) -> uint32_t {
+          if (!wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1, 9)) return 0;
+          const uint32_t cmd = segs[n % kSegs].cmd;
+          mbar_arrive(&bars->seg_empty[n % kSegs]);
+          return cmd;
+        };
+        uint32_t cmd = fetch(0);
+        int n = 1;
+        while (ok && cmd != 0) {
+          int left = cmd & 1023;
+          const int tiles = cmd >> 10 & 7;
+          const uint32_t last = cmd >> 13 & 7;
+          bool fresh = true;  // the tiles of K may not have landed
+          // one query tile against the tiles of K
+          auto products = [&](uint32_t idesc) {
+            const uint32_t b0 = q_lo + q.st * (L::kTile / 16);
+            if (!wait(&bars->q_full[q.st], q.ph, 1)) return;
 #pragma unroll
-        for (int rt = 0; rt < kTiles; ++rt) hidden[rt] = uniform(s.first(rt, p.log_p) - s.q0);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->seg_empty[n % kSegs]);
-        if (left == 0) break;
-        uint32_t have = 0;  // bit rt: tile rt has landed
-        for (; ok && left > 0; --left) {
-          if (left == 1) cols = last;  // only a chunk's last tile has fewer
-          if (!(ok = wait_bar(&bars->q_full[q.st], q.ph, SITE_PAGED_MMA, 1))) break;
-          const uint32_t idesc = idesc_bf16(128, 0, 0) | (uint32_t)max(4, ((cols + 31) & ~31) >> 3) << 17;
-          Ring<NK> k = base;
+            for (int rt = 0; rt < kTiles; ++rt) {
+              if (rt < tiles) {
+                if (fresh) {
+                  if (!wait(&bars->k_full[kb + rt], ph >> (kb + rt) & 1, 2)) return;
+                  ph ^= 1u << (kb + rt);
+                }
+                if (!wait(&bars->s_empty[rt], (ns >> rt & 1) ^ 1, 3)) return;
+                ns ^= 1u << rt;
+                tc_fence_after();
+                const uint32_t a0 = k_lo + (kb + rt) * (L::kTile / 16);
 #pragma unroll
-          for (int rt = 0; rt < kTiles; ++rt) {
-            if (rt < tiles && hidden[rt] <= 0) {
-              if (!(have >> rt & 1)) {
-                if (!(ok = wait_bar(&bars->k_full[k.st], k.ph, SITE_PAGED_MMA, 2))) break;
-                have |= 1u << rt;
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint32_t off = ((ks >> 2) * kBlockBytes + (ks & 3) * 32) / 16;
+                  mma_ss_lo(tbase + 128 * rt, a0 + off, b0 + off, idesc, ks > 0 ? 1u : 0u);
+                }
+                mma_commit(&bars->s_full[rt]);
+                if (left == 1) mma_commit(&bars->k_empty[kb + rt]);
+                if (rt == 0 && fresh) cmd = fetch(n);
               }
-              if (!(ok = wait_bar(&bars->s_empty[rt], (ns >> rt & 1) ^ 1, SITE_PAGED_MMA, 3))) break;
-              ns ^= 1u << rt;
-              tc_fence_after();
-              const uint32_t a0 = k_lo + k.st * (L::kTile / 16), b0 = q_lo + q.st * (L::kTile / 16);
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = ((ks >> 2) * kBlockBytes + (ks & 3) * 32) / 16;
-                mma_ss_elect(tbase + 128 * rt, a0 + off, b0 + off, idesc, ks > 0 ? 1u : 0u);
-              }
-              mma_commit_elect(&bars->s_full[rt]);
-              if (left == 1) mma_commit_elect(&bars->k_empty[k.st]);
             }
-            --hidden[rt];
-            k.skip(1);
-          }
-          mma_commit_elect(&bars->q_empty[q.st]);
-          q.skip(1);
+            mma_commit(&bars->q_empty[q.st]);
+            q.skip(1);
+            fresh = false;
+          };
+          // only a chunk's last query tile has fewer than 128 columns
+          for (; ok && left > 1; --left) products(idesc_bf16(128, 128, 0));
+          if (ok) products(idesc_bf16(128, 0, 0) | last << 19);
+          if (L::KB > 1) kb ^= kTiles;
+          ++n;
         }
-        base.skip(tiles);
+        mma_commit(&bars->drain);
+        mbar_wait(&bars->drain, 0, nullptr);
       }
-      // drain every issued MMA before teardown
-      mma_commit_elect(&bars->drain);
-      warp_wait(&bars->drain, 0, nullptr);
+      __syncwarp();
     } else if (warp == 2) {
       // ------------------------------------------------------------ query tiles and their lse
       if (lane == 0) tma_prefetch_desc(&p.tq);
@@ -463,16 +473,22 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           s.len = q.len;
           s.lo = q.lo;
           s.c = q.c;
-          const int q_lo = s.first(0, p.log_p), off = u - at;
-          // this CTA's units of the item from here on, up to a run of query tiles: [off, stop)
-          const int stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
-          const int t0 = max(off - kSetup, 0), t1 = max(stop - kSetup, 0);
+          const int a = q.len - q.c, q_lo = first_tile(a, p.log_p, s.slot0), off = u - at;
+          // this CTA's units of the item from here on, as long as the same tiles are seen, up to a run
+          // of query tiles: [off, stop)
+          const int t0 = max(off - kSetup, 0);
+          int stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
+          s.tiles = 0;
+          for (int rt = 0; rt < kTiles && s.slot0 + rt * kKeys < s.len; ++rt) {
+            const int f = first_tile(a, p.log_p, s.slot0 + rt * kKeys) - q_lo;
+            if (f <= t0) ++s.tiles;
+            else stop = min(stop, f + kSetup);
+          }
+          const int t1 = max(stop - kSetup, 0);
           s.q0 = q_lo + t0;
           s.NQ = t1 - t0;
           seg_pg = pg;
-          s.tiles = 0;
-          for (int rt = 0; rt < kTiles; ++rt)
-            s.tiles += s.slot0 + rt * kKeys < s.len && s.first(rt, p.log_p) < q_lo + t1;
+          if (s.NQ) s.pack(p.log_p, p.log_g);
           const bool cont = t0 > 0 && n > 0;
           own = t0 == 0 || (cont && own);
           s.flags = (cont ? 0 : 1) | (stop == per || u + (stop - off) == end ? 2 : 0) | (own && stop == per ? 4 : 0) |
@@ -499,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           Seg& to = segs[n % kSegs];
           to.i = s.i, to.h = s.h, to.slot0 = s.slot0, to.len = s.len;
           to.q0 = s.q0, to.NQ = s.NQ, to.lo = s.lo, to.c = s.c;
-          to.tiles = s.tiles, to.flags = s.flags;
+          to.tiles = s.tiles, to.flags = s.flags, to.cmd = s.cmd;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->seg_full[n % kSegs]);
@@ -507,7 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       }
     }
   } else {
-    setmaxnreg_inc<kRegsSum>();
     // ------------------------------------------------------------ sums
     const int rt = (warp - 4) >> 2;  // tile of the block
     const int quarter = warp & 3;
@@ -523,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       const Seg& s = segs[n % kSegs];
       if (s.NQ == 0) break;
       if (s.begins()) total = 0.0f;
-      const int t = s.slot0 + row, a = s.len - s.c, first = s.first(rt, p.log_p);
+      const int t = s.slot0 + row, a = s.len - s.c;
       const bool on = t < s.len, finish = on && s.ends() && s.whole();
       // the slot's old score, on its way while the products run
       float* out = nullptr;
@@ -535,18 +550,19 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           if (p.decay != 0.0f) old = *out;
         }
       }
-      for (int c = s.q0; c < s.q0 + s.NQ; ++c) {
+      // query tiles from `clear` on have no column of a token before the key's tile ends; `part` is
+      // the one with fewer than 128 columns.  In registers: the barriers make shared memory anew
+      const bool seen = rt < s.tiles;
+      const int q0 = s.q0, q1 = q0 + s.NQ, clear = (max(0, s.slot0 + rt * kKeys + kKeys - 1 - a) + (1 << p.log_p) - 1) >> p.log_p;
+      const int part = s.c & ((1 << p.log_p) - 1) || s.c == 0 ? s.c >> p.log_p : 0x7fffffff;
+      for (int c = q0; c < q1; ++c) {
         if (!(ok = wait_bar(&bars->l_full[r.st], r.ph, SITE_PAGED_SOFTMAX, 1))) break;
-        if (rt < s.tiles && c >= first) {
+        if (seen) {
+          const float* l2 = lse_s + r.st * 128;
+          const bool masked = c < clear || c >= part || none_s[r.st];
           if (!(ok = wait_bar(&bars->s_full[rt], ns, SITE_PAGED_SOFTMAX, 2))) break;
           ns ^= 1;
           tc_fence_after();
-          const float* l2 = lse_s + r.st * 128;
-          const int cols = s.columns(c, p.log_p, p.log_g);
-          // columns below lo are of tokens before the key's own
-          const int lo = max(0, t - a - (c << p.log_p)) << p.log_g;
-          const bool masked =
-              cols < 128 || none_s[r.st] || s.slot0 + rt * kKeys + kKeys - 1 - a - (c << p.log_p) > 0;
           uint64_t acc0 = 0, acc1 = 0;  // packed fp32 pairs
           uint32_t ra[32], rb[32];
           auto hand_back = [&]() {  // all of the tile's columns are in registers
@@ -576,6 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
               }
             }
           } else {
+            // columns below lo are of tokens before the key's own
+            const int cols = s.columns(c, p.log_p, p.log_g), lo = max(0, t - a - (c << p.log_p)) << p.log_g;
             const int chunks = max(1, (cols + 31) >> 5);
             float m = 0.0f;
 #pragma unroll 1
@@ -660,14 +678,6 @@ kvpop_status launch(MassParams& prm, int ctas, cudaStream_t cs) {
     st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total),
                     "kvpop_paged_mass: smem attribute");
     if (st != KVPOP_OK) return st;
-    // the register re-split must fit in the launch allocation (granule: 8 per thread)
-    cudaFuncAttributes fa;
-    st = cuda_check(cudaFuncGetAttributes(&fa, kern), "kvpop_paged_mass: attributes");
-    if (st != KVPOP_OK) return st;
-    if (((fa.numRegs + 7) / 8) * 8 < kRegsNeeded) {
-      set_last_error("kvpop_paged_mass: kernel built with %d registers per thread, %d needed", fa.numRegs, kRegsNeeded);
-      return KVPOP_ERR_INTERNAL;
-    }
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   st = cuda_check(launch_pdl(kern, dim3(ctas), dim3(kThreads), L::total, cs, prm), "kvpop_paged_mass: launch");
