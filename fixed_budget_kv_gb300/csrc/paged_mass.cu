@@ -34,12 +34,22 @@
 namespace kvpop {
 namespace {
 
-constexpr int kTiles = 4;  // tiles of K in a block
-constexpr int kThreads = (4 + 4 * kTiles) * 32;
-constexpr int kKeys = 128, kBlockKeys = kTiles * kKeys;
+constexpr int kThreads = 640;
+constexpr int kKeys = 128;
+// Two forms of the kernel.  Narrow: a block of four tiles of K against query tiles of up to 128
+// columns, one summing warpgroup a tile.  Wide: two tiles against 256 columns, two warpgroups a tile.
+// The issuing thread takes about 85 cycles for a product's instruction and 300 between two tiles, the
+// tensor core 65 for 128 columns and 130 for 256: wide keeps it busy (4096 rows over 32 768 slots
+// WIDE_CHUNK us against 800), narrow has twice the keys on their way from memory (decode rows).
+template <bool WIDE>
+struct Form {
+  static constexpr int kTiles = WIDE ? 2 : 4;
+  static constexpr int kCols = WIDE ? 256 : 128;
+  static constexpr int kBlockKeys = kTiles * kKeys;
+};
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
 constexpr int kBoxes = kKeys / kMinPage;  // of a tile, at most
-static_assert(kTiles * kBoxes == 32, "one table entry a lane");
+static_assert(Form<false>::kTiles * kBoxes == 32, "one table entry a lane");
 // Loading a block of K and changing over to it, in query tiles.
 constexpr int kSetup = 2;
 constexpr int kSegs = 4;
@@ -58,9 +68,10 @@ struct MassParams {
   const float* lse;
   float* scores;
   Split* split;  // [CTA] the item that the CTA is the second to work on
-  float* part;   // [CTA, 2 slots, 512 keys]
-  int Hq, G, log_g, log_p;  // query tiles of 2^log_p = 128 / G tokens
+  float* part;   // [CTA, 2 slots, keys of a block]
+  int Hq, G, log_g, log_p;  // query tiles of 2^log_p tokens
   int q_bytes;              // of a query tile's box and 64 columns
+  int block_keys;
   float scale_log2, decay;
 };
 
@@ -75,18 +86,18 @@ __device__ __forceinline__ int first_tile(int a, int log_p, int t) { return max(
 __device__ __forceinline__ int units_before(const MassParams& p, const Seq& s, int m) {
   const int a = s.len - s.c;
   // blocks that begin at or behind slot a, from b0 on, are not seen by the first tokens: by
-  // f0, f0 + 512 / tokens, ... query tiles
-  const int b0 = a > 0 ? (a + kBlockKeys - 1) / kBlockKeys : 0;
+  // f0, f0 + block_keys / tokens, ... query tiles
+  const int b0 = a > 0 ? (a + p.block_keys - 1) / p.block_keys : 0;
   const int n = max(0, m - b0);
-  const long long f0 = first_tile(a, p.log_p, b0 * kBlockKeys);
-  return (int)((long long)m * (s.nq + kSetup) - (n * f0 + ((long long)n * (n - 1) / 2 << (9 - p.log_p))));
+  const long long f0 = first_tile(a, p.log_p, b0 * p.block_keys);
+  return (int)((long long)m * (s.nq + kSetup) - (n * f0 + (long long)n * (n - 1) / 2 * (p.block_keys >> p.log_p)));
 }
 __device__ __forceinline__ Seq sequence(const MassParams& p, int i) {
   Seq s;
   s.lo = p.c.lo(i);
   s.c = p.c.hi(i, s.lo) - s.lo;
   s.len = p.c.len(i);
-  s.nb = (s.len + kBlockKeys - 1) / kBlockKeys;
+  s.nb = (s.len + p.block_keys - 1) / p.block_keys;
   s.nq = max(1, (s.c + (1 << p.log_p) - 1) >> p.log_p);
   s.units = s.nb ? units_before(p, s, s.nb) * p.c.H : 0;
   return s;
@@ -99,7 +110,7 @@ struct __align__(16) Seg {
   int tiles, flags, cmd, pad;  // tiles of K, all of which each of these query tiles sees
   // [tile][box] pages, as the table has them: a box is a page, or 128 slots of one.  One past the
   // last page where there is no slot
-  int pages[kTiles * kBoxes];
+  int pages[32];
   // the first of the block's query tiles here; the last of them here
   __device__ __forceinline__ bool begins() const { return flags & 1; }
   __device__ __forceinline__ bool ends() const { return flags & 2; }
@@ -121,33 +132,39 @@ template <int NK, int NQS>
 struct Bars {
   uint64_t k_full[NK], k_empty[NK];
   uint64_t q_full[NQS], q_empty[NQS];
-  uint64_t s_full[kTiles], s_empty[kTiles];
+  uint64_t s_full[4], s_empty[4];
+  uint64_t x_full[2];
   uint64_t l_full[kLseStages], l_empty[kLseStages];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t drain;
 };
 
-template <int D>
-struct Layout {
+template <int D, bool WIDE>
+struct Layout : Form<WIDE> {
+  using F = Form<WIDE>;
   static constexpr int DH = D / 64;
   static constexpr int KB = D == 128 ? 1 : 2;  // blocks of K: tile rt of one has a place of its own
-  static constexpr int NK = KB * kTiles;
-  static constexpr int NQ = D == 128 ? 3 : 5;  // query tiles
-  static constexpr int kTile = DH * kBlockBytes;
+  static constexpr int NK = KB * F::kTiles;
+  static constexpr int NQ = WIDE ? (D == 128 ? 2 : 4) : (D == 128 ? 3 : 5);  // query tiles
+  static constexpr int kTile = DH * kBlockBytes;          // of K
+  static constexpr int kHalf = F::kCols * 128;            // 64 columns of a query tile
+  static constexpr int kQuery = DH * kHalf;
   static constexpr int k_off = 0;
   static constexpr int q_off = k_off + NK * kTile;
-  static constexpr int lse_off = q_off + NQ * kTile;  // [stage][128]
-  static constexpr int bar_off = lse_off + kLseStages * 512;
+  static constexpr int lse_off = q_off + NQ * kQuery;     // [stage][kCols]
+  static constexpr int x_off = lse_off + kLseStages * F::kCols * 4;  // [2][tile][key] sums of the second warpgroup
+  static constexpr int bar_off = x_off + (WIDE ? 2 * F::kBlockKeys * 4 : 0);
   static constexpr int seg_off = bar_off + ((int)sizeof(Bars<NK, NQ>) + 15) / 16 * 16;
   static constexpr int misc_off = seg_off + kSegs * (int)sizeof(Seg);  // TMEM address, abort flag, a flag a stage
   static constexpr int total = misc_off + 8 + 4 * kLseStages;
   static_assert(total <= 232448, "shared memory of one CTA");
 };
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant__ MassParams p) {
-  using L = Layout<D>;
-  constexpr int DH = L::DH, NK = L::NK, NQS = L::NQ;
+  using L = Layout<D, WIDE>;
+  constexpr int DH = L::DH, NK = L::NK, NQS = L::NQ, kTiles = L::kTiles, kCols = L::kCols, kBlockKeys = L::kBlockKeys;
+  constexpr int kGroups = 4 / kTiles;  // summing warpgroups a tile
   extern __shared__ __align__(1024) uint8_t smem[];  // no slack left to align by hand: the walker checks
   Bars<NK, NQS>* bars = reinterpret_cast<Bars<NK, NQS>*>(smem + L::bar_off);
   Seg* segs = reinterpret_cast<Seg*>(smem + L::seg_off);
@@ -169,15 +186,16 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     }
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->s_empty[i], 4);
+      mbar_init(&bars->s_empty[i], 4 * kGroups);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&bars->x_full[i], 4);
     for (int i = 0; i < kLseStages; ++i) {
       mbar_init(&bars->l_full[i], 1);
-      mbar_init(&bars->l_empty[i], 4 * kTiles);
+      mbar_init(&bars->l_empty[i], 16);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&bars->seg_full[i], 1);
-      mbar_init(&bars->seg_empty[i], 3 + 4 * kTiles);  // K, query tiles, MMA, summing warps
+      mbar_init(&bars->seg_empty[i], 3 + 16);  // K, query tiles, MMA, summing warps
     }
     mbar_init(&bars->drain, 1);
     *abort_flag = 0;
@@ -246,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
       // One thread issues (a whole warp in step, as in paged_attn.cu: decode rows 139 us against 119,
-      // a window 61 against 53).  Tile rt of a block has TMEM columns 128 rt .. and places of its own;
+      // a window 61 against 53).  Tile rt of a block has TMEM columns kCols rt .. and places of its own;
       // the products cover as many columns as the query tile has.
       const uint32_t k_lo = desc_lo(sbase + L::k_off, 16), q_lo = desc_lo(sbase + L::q_off, 16);
       if (lane == 0) {
@@ -272,11 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         while (ok && cmd != 0) {
           int left = cmd & 1023;
           const int tiles = cmd >> 10 & 7;
-          const uint32_t last = cmd >> 13 & 7;
+          const uint32_t last = cmd >> 13 & 15;
           bool fresh = true;  // the tiles of K may not have landed
           // one query tile against the tiles of K
           auto products = [&](uint32_t idesc) {
-            const uint32_t b0 = q_lo + q.st * (L::kTile / 16);
+            const uint32_t b0 = q_lo + q.st * (L::kQuery / 16);
             if (!wait(&bars->q_full[q.st], q.ph, 1)) return;
 #pragma unroll
             for (int rt = 0; rt < kTiles; ++rt) {
@@ -291,8 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 const uint32_t a0 = k_lo + (kb + rt) * (L::kTile / 16);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
-                  const uint32_t off = ((ks >> 2) * kBlockBytes + (ks & 3) * 32) / 16;
-                  mma_ss_lo(tbase + 128 * rt, a0 + off, b0 + off, idesc, ks > 0 ? 1u : 0u);
+                  const uint32_t in = (ks & 3) * 32;
+                  mma_ss_lo(tbase + kCols * rt, a0 + ((ks >> 2) * kBlockBytes + in) / 16, b0 + ((ks >> 2) * L::kHalf + in) / 16,
+                            idesc, ks > 0 ? 1u : 0u);
                 }
                 mma_commit(&bars->s_full[rt]);
                 if (left == 1) mma_commit(&bars->k_empty[kb + rt]);
@@ -303,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             q.skip(1);
             fresh = false;
           };
-          // only a chunk's last query tile has fewer than 128 columns
-          for (; ok && left > 1; --left) products(idesc_bf16(128, 128, 0));
+          // only a chunk's last query tile has fewer columns
+          for (; ok && left > 1; --left) products(idesc_bf16(128, kCols, 0));
           if (ok) products(idesc_bf16(128, 0, 0) | last << 19);
           if (L::KB > 1) kb ^= kTiles;
           ++n;
@@ -324,13 +343,13 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, SITE_PAGED_PRODUCER, 9)) break;
         const Seg& s = segs[n % kSegs];
         if (s.NQ == 0) break;
-        // rows 4 lane .. 4 lane + 3 of query tile c: -lse in log2 units; -inf adds nothing
-        float x[4];
+        // rows 4 lane .. 4 lane + 3 (and 128 further on) of query tile c: -lse in log2 units; -inf adds nothing
+        float x[kCols / 32];
         auto read = [&](int c) {
           const int cols = s.columns(c, p.log_p, p.log_g);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int col = 4 * lane + u;
+          for (int u = 0; u < kCols / 32; ++u) {
+            const int col = (u >> 2) * 128 + 4 * lane + (u & 3);
             x[u] = col < cols ? p.lse[(size_t)(s.lo + (c << p.log_p) + (col >> p.log_g)) * p.Hq + s.h * p.G + (col & (p.G - 1))]
                               : __int_as_float(0x7f800000);
           }
@@ -341,23 +360,25 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           if (lane == 0) {
             mbar_arrive_expect_tx(&bars->q_full[q.st], DH * p.q_bytes);
             for (int dh = 0; dh < DH; ++dh)
-              tma_load_4d(smem + L::q_off + q.st * L::kTile + dh * kBlockBytes, &p.tq, &bars->q_full[q.st], dh * 64, s.h * p.G,
+              tma_load_4d(smem + L::q_off + q.st * L::kQuery + dh * L::kHalf, &p.tq, &bars->q_full[q.st], dh * 64, s.h * p.G,
                           s.lo + (c << p.log_p), 0);
           }
           __syncwarp();
           q.skip(1);
           ++loads;
-          float y[4];
+          float y[kCols / 32];
           bool none = false;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < kCols / 32; ++u) {
             none |= x[u] == neg_inf();
             y[u] = x[u] == neg_inf() ? neg_inf() : -x[u] * 1.4426950408889634f;
           }
           if (c + 1 < s.q0 + s.NQ) read(c + 1);
           none = __any_sync(0xffffffffu, none);
           if (!(ok = wait_bar(&bars->l_empty[r.st], r.ph ^ 1, SITE_PAGED_PRODUCER, 3))) break;
-          reinterpret_cast<float4*>(lse_s)[r.st * 32 + lane] = make_float4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+          for (int u = 0; u < kCols / 32; u += 4)
+            reinterpret_cast<float4*>(lse_s)[(r.st * kCols + u * 32) / 4 + lane] = make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]);
           if (lane == 0) none_s[r.st] = none;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->l_full[r.st]);
@@ -428,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         per = q.nq - first_tile(q.len - q.c, p.log_p, kb * kBlockKeys) + kSetup;
         const int slot = kb * kBlockKeys + lane / kBoxes * kKeys + (lane % kBoxes << log_box);
         pg = p.c.pages;
-        if (lane % kBoxes < kKeys >> log_box && slot < q.len) {
+        if (lane / kBoxes < kTiles && lane % kBoxes < kKeys >> log_box && slot < q.len) {
           pg = p.c.page_of(seq, slot);
           if (pg < 0) {
             report_page(p.c.status, seq);
@@ -524,13 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     }
   } else {
     // ------------------------------------------------------------ sums
-    const int rt = (warp - 4) >> 2;  // tile of the block
+    const int rt = (warp - 4) / (4 * kGroups), half = (warp - 4) / 4 % kGroups;  // tile of the block, columns of it
     const int quarter = warp & 3;
     const int row = rt * kKeys + quarter * 32 + lane;  // key of the block
-    const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16) + 128 * rt;
+    const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16) + kCols * rt + 128 * half;
     const uint64_t s2 = pack2(p.scale_log2, p.scale_log2);
     float total = 0.0f;
     uint32_t ns = 0;  // parity of this tile's next product
+    uint32_t nx = 0;  // items finished
     Ring<kLseStages> r;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -539,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       if (s.NQ == 0) break;
       if (s.begins()) total = 0.0f;
       const int t = s.slot0 + row, a = s.len - s.c;
-      const bool on = t < s.len, finish = on && s.ends() && s.whole();
+      const bool on = t < s.len, finish = on && half == 0 && s.ends() && s.whole();
       // the slot's old score, on its way while the products run
       float* out = nullptr;
       float old = 0.0f;
@@ -551,14 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         }
       }
       // query tiles from `clear` on have no column of a token before the key's tile ends; `part` is
-      // the one with fewer than 128 columns.  In registers: the barriers make shared memory anew
+      // the one with fewer columns than the others.  In registers: the barriers make shared memory anew
       const bool seen = rt < s.tiles;
       const int q0 = s.q0, q1 = q0 + s.NQ, clear = (max(0, s.slot0 + rt * kKeys + kKeys - 1 - a) + (1 << p.log_p) - 1) >> p.log_p;
       const int part = s.c & ((1 << p.log_p) - 1) || s.c == 0 ? s.c >> p.log_p : 0x7fffffff;
       for (int c = q0; c < q1; ++c) {
         if (!(ok = wait_bar(&bars->l_full[r.st], r.ph, SITE_PAGED_SOFTMAX, 1))) break;
         if (seen) {
-          const float* l2 = lse_s + r.st * 128;
+          const float* l2 = lse_s + r.st * kCols + 128 * half;
           const bool masked = c < clear || c >= part || none_s[r.st];
           if (!(ok = wait_bar(&bars->s_full[rt], ns, SITE_PAGED_SOFTMAX, 2))) break;
           ns ^= 1;
@@ -593,8 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             }
           } else {
             // columns below lo are of tokens before the key's own
-            const int cols = s.columns(c, p.log_p, p.log_g), lo = max(0, t - a - (c << p.log_p)) << p.log_g;
-            const int chunks = max(1, (cols + 31) >> 5);
+            const int cols = s.columns(c, p.log_p, p.log_g) - 128 * half;
+            const int lo = (max(0, t - a - (c << p.log_p)) << p.log_g) - 128 * half;
+            const int chunks = min(4, max(1, (cols + 31) >> 5));
             float m = 0.0f;
 #pragma unroll 1
             for (int ch = 0; ch < chunks; ++ch) {
@@ -619,9 +642,23 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         r.skip(1);
       }
       if (!ok) break;
+      if (WIDE && s.ends()) {
+        // the second warpgroup's sums join the first's.  Two buffers: it is never two items ahead, as
+        // TMEM is handed back by both
+        float* x_s = reinterpret_cast<float*>(smem + L::x_off) + (nx & 1) * kBlockKeys;
+        if (half == 1) {
+          x_s[row] = total;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->x_full[rt]);
+        } else {
+          if (!(ok = wait_bar(&bars->x_full[rt], nx & 1, SITE_PAGED_SOFTMAX, 3))) break;
+          total += x_s[row];
+        }
+        ++nx;
+      }
       if (finish) {
         if (out) *out = p.decay != 0.0f ? fmaf(p.decay, old, total) : total;
-      } else if (on && s.ends()) {
+      } else if (on && half == 0 && s.ends()) {
         p.part[((size_t)blockIdx.x * 2 + s.slot()) * kBlockKeys + row] = total;
       }
       __syncwarp();
@@ -646,7 +683,7 @@ __global__ void __launch_bounds__(kKeys) mass_merge(const __grid_constant__ Mass
   grid_dep_wait();
   const Split s = p.split[blockIdx.x];
   if (s.h < 0) return;
-  const int row = blockIdx.y * kKeys + threadIdx.x, t = s.block * kBlockKeys + row;
+  const int row = blockIdx.y * kKeys + threadIdx.x, t = s.block * p.block_keys + row;
   if (t >= p.c.len(s.i)) return;
   const int pg = p.c.page_of(s.i, t);
   if (pg < 0) return;
@@ -656,21 +693,23 @@ __global__ void __launch_bounds__(kKeys) mass_merge(const __grid_constant__ Mass
   float total = 0.0f;
 #pragma unroll 8
   for (int c = c0; c <= s.c1; ++c)  // the item begins in c0's share
-    total += p.part[((size_t)c * 2 + (c == c0 ? 1 : 0)) * kBlockKeys + row];
+    total += p.part[((size_t)c * 2 + (c == c0 ? 1 : 0)) * p.block_keys + row];
   *out = p.decay != 0.0f ? fmaf(p.decay, old, total) : total;
 }
 
-// A bound on the units of a call, and the CTAs of mass_kernel.
+// A bound on the units of a call, and the CTAs of mass_kernel: as many for both forms, so that
+// the workspace does not depend on which is taken.
 int max_ctas(int T, int n, int G, int H, long long slots) {
-  const long long units = ((long long)T * G / 128 + (long long)n * (1 + kSetup)) * H * ((slots + kBlockKeys - 1) / kBlockKeys);
+  constexpr int kBlock = Form<true>::kBlockKeys;
+  const long long units = ((long long)T * G / 128 + (long long)n * (1 + kSetup)) * H * ((slots + kBlock - 1) / kBlock);
   return (int)min((long long)num_sms(), units);
 }
 size_t part_offset(int ctas) { return ((size_t)ctas * sizeof(Split) + 255) / 256 * 256; }
 
-template <int D>
+template <int D, bool WIDE>
 kvpop_status launch(MassParams& prm, int ctas, cudaStream_t cs) {
-  using L = Layout<D>;
-  auto kern = mass_kernel<D>;
+  using L = Layout<D, WIDE>;
+  auto kern = mass_kernel<D, WIDE>;
   kvpop_status st = KVPOP_OK;
   static std::atomic<uint64_t> ready{0};  // bit d: the kernel is set up on device d
   const int dev = current_device();
@@ -682,7 +721,7 @@ kvpop_status launch(MassParams& prm, int ctas, cudaStream_t cs) {
   }
   st = cuda_check(launch_pdl(kern, dim3(ctas), dim3(kThreads), L::total, cs, prm), "kvpop_paged_mass: launch");
   if (st != KVPOP_OK) return st;
-  return cuda_check(launch_pdl(mass_merge, dim3(ctas, kTiles), dim3(kKeys), 0, cs, prm), "kvpop_paged_mass: merge launch");
+  return cuda_check(launch_pdl(mass_merge, dim3(ctas, L::kTiles), dim3(kKeys), 0, cs, prm), "kvpop_paged_mass: merge launch");
 }
 
 }  // namespace
@@ -700,7 +739,7 @@ extern "C" kvpop_status kvpop_paged_mass_workspace_size(int T, int n, int Hq, in
   kvpop_status st = paged_check_rows(name, T, n, Hq, H, D, max_pages, page);
   if (st != KVPOP_OK) return st;
   const int ctas = max_ctas(T, n, Hq / H, H, (long long)max_pages * page);
-  *bytes = part_offset(ctas) + (size_t)ctas * 2 * kBlockKeys * 4;
+  *bytes = part_offset(ctas) + (size_t)ctas * 2 * Form<false>::kBlockKeys * 4;
   return KVPOP_OK;
 }
 
@@ -733,8 +772,11 @@ extern "C" kvpop_status kvpop_paged_mass(const void* q, const float* lse, int T,
     return KVPOP_ERR_UNSUPPORTED;
   }
   const int G = Hq / H, box = min(page, kKeys);
+  // wide from 256 rows a sequence and head on (their mean: only the device knows each)
+  const bool wide = (long long)T * G >= 256ll * n;
+  const int cols = wide ? Form<true>::kCols : Form<false>::kCols;
   // a decode step's rows lie alone: their boxes take no other sequence's along
-  const int tokens = cu ? 128 / G : 1;
+  const int tokens = cu ? cols / G : 1;
   const uint64_t dq[4] = {(uint64_t)D, (uint64_t)Hq, (uint64_t)T, 1};
   const uint64_t sq[3] = {(uint64_t)D * 2, (uint64_t)Hq * D * 2, (uint64_t)T * Hq * D * 2};
   const uint32_t bq[4] = {64, (uint32_t)G, (uint32_t)tokens, 1};
@@ -752,10 +794,12 @@ extern "C" kvpop_status kvpop_paged_mass(const void* q, const float* lse, int T,
   prm.G = G;
   prm.log_g = 0;
   while ((1 << prm.log_g) < G) ++prm.log_g;
-  prm.log_p = 7 - prm.log_g;
+  prm.log_p = (wide ? 8 : 7) - prm.log_g;
+  prm.block_keys = wide ? Form<true>::kBlockKeys : Form<false>::kBlockKeys;
   prm.q_bytes = tokens * G * 128;
   prm.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
   prm.decay = decay;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return D == 128 ? launch<128>(prm, ctas, cs) : launch<64>(prm, ctas, cs);
+  if (D == 128) return wide ? launch<128, true>(prm, ctas, cs) : launch<128, false>(prm, ctas, cs);
+  return wide ? launch<64, true>(prm, ctas, cs) : launch<64, false>(prm, ctas, cs);
 }
