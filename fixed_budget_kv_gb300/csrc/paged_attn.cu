@@ -211,13 +211,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   grid_dep_wait();
   grid_dep_launch();
 
-  auto fail = [&](int site, int detail) {
-    report_error(p.c.status, KVPOP_ERR_TIMEOUT, site, detail);
-    *abort_flag = 1;
-  };
+  auto fail = [&](int site, int detail) { give_up(p.c.status, site, detail, abort_flag); };
   // segment n, once the walker has written it; false at the end of the work
   auto get_seg = [&](int n, Seg& s) -> bool {
-    if (!mbar_wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1, abort_flag)) {
+    if (!bar_wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1, abort_flag)) {
       fail(SITE_PAGED_PRODUCER, 3);
       return false;
     }
@@ -254,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         return p.c.pages;
       };
       auto load = [&](const CUtensorMap* map, int t, int pg) {
-        if (!warp_wait(&bars->kv_empty[r.st], r.ph ^ 1, abort_flag)) {
+        if (!bar_wait_warp(&bars->kv_empty[r.st], r.ph ^ 1, abort_flag)) {
           if (lane == 0) fail(SITE_PAGED_PRODUCER, 1);
           ok = false;
           return;
@@ -268,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         ++loads;
       };
       for (int n = 0; ok; ++n) {
-        if (!warp_wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1, abort_flag)) {
+        if (!bar_wait_warp(&bars->seg_full[n % kSegs], (n / kSegs) & 1, abort_flag)) {
           if (lane == 0) fail(SITE_PAGED_PRODUCER, 3);
           break;
         }
@@ -296,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         // given up: nobody has waited for the last loads, which must land before the CTA ends
         for (int i = 0; i < min(loads, NS); ++i) {
           const int seq = loads - 1 - i;
-          mbar_wait(&bars->kv_full[seq % NS], (seq / NS) & 1, nullptr);
+          bar_wait(&bars->kv_full[seq % NS], (seq / NS) & 1, nullptr);
         }
       }
     } else if (warp == 1) {
@@ -321,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       uint32_t np = 0;                                // bit w: parity of stream w's next P
       bool ok = true;
       auto wait_bar = [&](uint64_t* bar, uint32_t ph, int detail) -> bool {
-        if (!warp_wait(bar, ph, abort_flag)) {
+        if (!bar_wait_warp(bar, ph, abort_flag)) {
           if (lane == 0) fail(SITE_PAGED_MMA, detail);
           ok = false;
           return false;
@@ -408,14 +405,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       }
       // drain every issued MMA before teardown
       mma_commit_elect(&bars->drain);
-      warp_wait(&bars->drain, 0, nullptr);
+      bar_wait_warp(&bars->drain, 0, nullptr);
     } else if (warp == 2 && lane == 0) {
       // ------------------------------------------------------------ query tiles
       tma_prefetch_desc(&p.tq);
       Seg s;
       int n = 0;
       for (; get_seg(n, s); ++n) {
-        if (!mbar_wait(&bars->q_empty, (n & 1) ^ 1, abort_flag)) {
+        if (!bar_wait(&bars->q_empty, (n & 1) ^ 1, abort_flag)) {
           fail(SITE_PAGED_PRODUCER, 2);
           break;
         }
@@ -426,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             tma_load_4d(smem + L::q_off + i * L::kTile + dh * kBlockBytes, &p.tq, &bars->q_full, dh * 64, s.h * p.G,
                         s.row0 + i * (p.toks / 2), 0);
       }
-      if (*abort_flag && n > 0) mbar_wait(&bars->q_full, (n - 1) & 1, nullptr);  // as for K and V
+      if (*abort_flag && n > 0) bar_wait(&bars->q_full, (n - 1) & 1, nullptr);  // as for K and V
     } else if (warp == 3) {
       // ------------------------------------------------------------ the CTA's share
       // lane l holds sequence j0 + l of a window of 32, and its first unit
@@ -540,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           }
         }
         if (n == 0 && lane == 0) p.split[blockIdx.x] = split;
-        if (!warp_wait(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag)) {
+        if (!bar_wait_warp(&bars->seg_empty[n % kSegs], ((n / kSegs) & 1) ^ 1, abort_flag)) {
           if (lane == 0) fail(SITE_PAGED_PRODUCER, 4);
           break;
         }
@@ -553,6 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
+    // in line: a call leaves too few registers here
+    auto fail_here = [&](int site, int detail) {
+      report_error(p.c.status, KVPOP_ERR_TIMEOUT, site, detail);
+      *abort_flag = 1;
+    };
     // ------------------------------------------------------------ softmax
     const int w = (warp - 4) >> 2;  // stream
     const int quarter = warp & 3;
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     bool ok = true;
     for (int n = 0; ok; ++n) {
       if (!warp_wait(&bars->seg_full[n % kSegs], (n / kSegs) & 1, abort_flag)) {
-        if (lane == 0) fail(SITE_PAGED_SOFTMAX, 3);
+        if (lane == 0) fail_here(SITE_PAGED_SOFTMAX, 3);
         break;
       }
       const Seg& s = segs[n % kSegs];
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       for (int i = 0; i < steps; ++i, ++cnt) {
         const int t = two ? i : 2 * i + a;
         if (!warp_wait(&bars->s_full[w], cnt & 1, abort_flag)) {
-          if (lane == 0) fail(SITE_PAGED_SOFTMAX, 1);
+          if (lane == 0) fail_here(SITE_PAGED_SOFTMAX, 1);
           ok = false;
           break;
         }
@@ -654,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           // V rows behind the length hold anything, and 0 * NaN would be NaN: zero them
           const int seq = sb + pos_v(two, s.NT, t), st = seq % NS;
           if (!warp_wait(&bars->kv_full[st], (seq / NS) & 1, abort_flag)) {
-            if (lane == 0) fail(SITE_PAGED_SOFTMAX, 2);
+            if (lane == 0) fail_here(SITE_PAGED_SOFTMAX, 2);
             ok = false;
             break;
           }
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       // no weight: -inf; a NaN among the scores keeps a finite maximum and travels in l
       float m2 = l == 0.0f ? neg_inf() : (m_ref == neg_inf() ? 0.0f : m_ref * sl2);
       if (!warp_wait(&bars->o_full, n & 1, abort_flag)) {
-        if (lane == 0) fail(SITE_PAGED_EPILOGUE, 1);
+        if (lane == 0) fail_here(SITE_PAGED_EPILOGUE, 1);
         break;
       }
       tc_fence_after();
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->ml_full);
         if (!warp_wait(&bars->ml_full, nml & 1, abort_flag)) {
-          if (lane == 0) fail(SITE_PAGED_EPILOGUE, 2);
+          if (lane == 0) fail_here(SITE_PAGED_EPILOGUE, 2);
           break;
         }
         ++nml;

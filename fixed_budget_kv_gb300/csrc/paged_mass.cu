@@ -215,12 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   grid_dep_launch();
 
   auto fail = [&](int site, int detail) {
-    report_error(p.c.status, KVPOP_ERR_TIMEOUT, site, detail);
-    *abort_flag = 1;
+    give_up(p.c.status, site, detail, abort_flag);
   };
   // for a whole warp: false where the wait was given up
   auto wait_bar = [&](uint64_t* bar, uint32_t ph, int site, int detail) -> bool {
-    if (warp_wait(bar, ph, abort_flag)) return true;
+    if (bar_wait_warp(bar, ph, abort_flag)) return true;
     if (lane == 0) fail(site, detail);
     return false;
   };
@@ -259,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       if (*abort_flag && lane == 0) {
         // given up: nobody has waited for the last loads, which must land before the CTA ends
         for (int i = 0; i < NK; ++i)
-          if (used >> i & 1) mbar_wait(&bars->k_full[i], (ph >> i & 1) ^ 1, nullptr);
+          if (used >> i & 1) bar_wait(&bars->k_full[i], (ph >> i & 1) ^ 1, nullptr);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         int kb = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity, int detail) -> bool {
-          if (mbar_wait(bar, parity, abort_flag)) return true;
+          if (bar_wait(bar, parity, abort_flag)) return true;
           fail(SITE_PAGED_MMA, detail);
           return ok = false;
         };
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           ++n;
         }
         mma_commit(&bars->drain);
-        mbar_wait(&bars->drain, 0, nullptr);
+        bar_wait(&bars->drain, 0, nullptr);
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -390,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       if (*abort_flag && lane == 0) {  // as for K
         for (int i = 0; i < min(loads, NQS); ++i) {
           const int seq = loads - 1 - i;
-          mbar_wait(&bars->q_full[seq % NQS], (seq / NQS) & 1, nullptr);
+          bar_wait(&bars->q_full[seq % NQS], (seq / NQS) & 1, nullptr);
         }
       }
     } else {

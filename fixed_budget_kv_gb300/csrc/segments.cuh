@@ -8,6 +8,23 @@ namespace kvpop {
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
+// mbar_wait and report_error with their long parts out of line: a persistent kernel's roles wait in
+// dozens of places, and with all of them inline its loops leave the instruction cache (the received
+// weight of decode rows: a quarter of the fetches missed).
+static __device__ __noinline__ bool bar_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_wait(bar, parity, abort_flag);
+}
+static __device__ __noinline__ void give_up(int* status, int site, int detail, volatile int* abort_flag) {
+  report_error(status, KVPOP_ERR_TIMEOUT, site, detail);
+  *abort_flag = 1;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || bar_wait_long(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool bar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, abort_flag));
+}
+
 __device__ __forceinline__ int scan_incl(int x) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
