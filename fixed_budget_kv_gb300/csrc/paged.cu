@@ -73,9 +73,10 @@ kvpop_status paged_check_rows(const char* name, int T, int n, int Hq, int H, int
     set_last_error("%s: at most 65535 heads and sequences, 2^24 tokens, 2^31 - 1 rows and 2^30 slots a sequence", name);
     return KVPOP_ERR_UNSUPPORTED;
   }
-  // tiles of rows and keys are numbered in 32 bits; setting a tile of rows up counts as eight more
-  if ((n + (long long)T * (Hq / H) / 128) * H > 0x7fffffffll / ((slots + 127) / 128 + 8)) {
-    set_last_error("%s: more than 2^31 - 1 tiles of rows and keys", name);
+  // the kernels number their units of work in 32 bits: up to three for a tile of rows and keys, and
+  // setting a tile of rows up counts as eight more
+  if ((n + (long long)T * (Hq / H) / 128) * H > 0x7fffffffll / (3 * ((slots + 127) / 128 + 8))) {
+    set_last_error("%s: more than 7 * 10^8 tiles of rows and keys", name);
     return KVPOP_ERR_UNSUPPORTED;
   }
   return KVPOP_OK;

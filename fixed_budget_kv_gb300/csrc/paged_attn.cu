@@ -49,8 +49,12 @@ constexpr int kBlockRows = 256;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 128 bytes
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMergeThreads = 256;
-// Time between the last tile of a segment and the first of the next, in tiles.
-constexpr int kSetup = 4;
+// Units of a tile, and of setup, the time between the last tile of a segment and the first of the
+// next.  A tile takes 1.9 us with two row tiles (bound by products and softmax) and 1.3 with one (by
+// its way from memory): the mixed step of 12 sequences took 228 us with 2 : 1, 213 with 1 : 1, 200
+// with 3 : 2.
+__host__ __device__ constexpr int tile_units(int two) { return 2 + two; }
+__host__ __device__ constexpr int setup_units(int two) { return 4 * tile_units(two); }
 constexpr int kSegs = 4;  // segments between the walker and the last reader
 // Tiles of a segment at most: the tensor core truncates what it adds to an accumulator, so sums of
 // more than 2^15 keys are added up outside of it, in fp32 with rounding (prefix.cu has the figures).
@@ -110,7 +114,11 @@ __device__ __forceinline__ int tiles_before(int a, int log_t, int m) {
   return t + (int)(sum(j + m) - sum(j));
 }
 __device__ __forceinline__ int units_before(const AttnParams& p, const Seq& s, int m) {
-  return tiles_before(s.len - s.c, 8 - p.log_g, m) + m * kSetup;
+  return tile_units(1) * tiles_before(s.len - s.c, 8 - p.log_g, m) + m * setup_units(1);
+}
+// Whether block b has two row tiles; all but the last do.
+__device__ __forceinline__ int two_tiles(const AttnParams& p, const Seq& s, int b) {
+  return (s.c - b * p.toks) << p.log_g > 128;
 }
 __device__ __forceinline__ Seq sequence(const AttnParams& p, int i) {
   Seq s;
@@ -118,7 +126,8 @@ __device__ __forceinline__ Seq sequence(const AttnParams& p, int i) {
   s.c = p.c.hi(i, s.lo) - s.lo;
   s.len = p.c.len(i);
   s.nb = (s.c + p.toks - 1) / p.toks;
-  s.units = s.nb ? (units_before(p, s, s.nb - 1) + max(1, (s.len + kKeys - 1) / kKeys) + kSetup) * p.c.H : 0;
+  const int two = two_tiles(p, s, s.nb - 1);
+  s.units = s.nb ? (units_before(p, s, s.nb - 1) + max(1, (s.len + kKeys - 1) / kKeys) * tile_units(two) + setup_units(two)) * p.c.H : 0;
   return s;
 }
 
@@ -453,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
         U = 0;
         if (lane == 0) report_error(p.c.status, KVPOP_ERR_INTERNAL, SITE_INTERNAL_CHECK, 60);
       }
-      const int C = min((int)gridDim.x, U);
+      const int C = min((int)gridDim.x, (U + 2) / 3);  // three units each: none has a part of a tile only
       const Share sh(U, max(C, 1));
       int u = 0, end = 0;
       if ((int)blockIdx.x < C) {
@@ -472,12 +481,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       // the sequence, row block and head of the item that holds unit u, the item's units, and the
       // first of them; looked up once and counted on
       Seq q = {};
-      int seq = 0, rb = 0, h = 0, per = 0, at = 0;
+      int seq = 0, rb = 0, h = 0, per = 0, at = 0, two = 0, setup = 0;
       bool known = false;
       auto enter_block = [&]() {
         // slots that its last row sees
         const int sees = rb == q.nb - 1 ? q.len : q.len - q.c + (rb + 1) * p.toks;
-        per = max(1, (sees + kKeys - 1) / kKeys) + kSetup;
+        two = two_tiles(p, q, rb);
+        setup = setup_units(two);
+        per = max(1, (sees + kKeys - 1) / kKeys) * tile_units(two) + setup;
       };
       for (int n = 0;; ++n) {
         Seg s = {0, 0, 0, 0, 0, 0, 0, 0, 0, {0, 0, 0}};  // NT = 0 ends the work
@@ -510,9 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             known = true;
           }
           // this CTA's units of the item from here on, up to a run of tiles: [off, stop)
-          const int off = u - at, stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
-          s.kt0 = max(off - kSetup, 0);
-          s.NT = max(stop - kSetup, 0) - s.kt0;
+          const int off = u - at, stop = min(min(per, off + (end - u)), max(off, setup) + kRunTiles * tile_units(two));
+          auto tile = [&](int x) { return two ? max(x - setup, 0) / tile_units(1) : max(x - setup, 0) / tile_units(0); };
+          s.kt0 = tile(off);
+          s.NT = tile(stop) - s.kt0;
           s.i = seq;
           s.h = h;
           s.row0 = q.lo + rb * p.toks;
@@ -524,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           s.flags = (s.nrow > 128 ? 1 : 0) | (own && stop == per ? 2 : 0) | (own ? 4 : 0) | (cont ? 8 : 0);
           if (n == 0 && s.kt0 > 0) {
             // the work begins inside an item; the second of its CTAs leaves word of it
-            split = {s.row0, h, sh.cta_of(at + kSetup) + 1 == (int)blockIdx.x ? s.nrow : 0, sh.cta_of(at + per - 1)};
+            split = {s.row0, h, sh.cta_of(at + setup + tile_units(two) - 1) + 1 == (int)blockIdx.x ? s.nrow : 0, sh.cta_of(at + per - 1)};
           }
           u += stop - off;
           if (stop == per) {  // on to the next item
@@ -878,8 +890,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge(const __grid_con
 
 // A bound on the units of a call, and the CTAs of paged_kernel.
 int max_ctas(int T, int n, int G, int H, long long slots) {
-  const long long units = (n + (long long)T * G / kBlockRows) * H * ((slots + kKeys - 1) / kKeys + kSetup);
-  return (int)min((long long)num_sms(), units);
+  const long long tiles = (n + (long long)T * G / kBlockRows) * H * ((slots + kKeys - 1) / kKeys);
+  return (int)min((long long)num_sms(), 4 * tiles);  // at least three units a CTA
 }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 size_t ml_offset(int ctas) { return round256((size_t)ctas * sizeof(Split)); }
