@@ -553,6 +553,18 @@ def _page_stride(x, dev, name):
     return x.stride(0) if pages > 1 else H * page * D
 
 
+def _row_stride(t, T, H, D, dev, name):
+    """Elements between the tokens of a bf16 [T, H, D] view whose heads are contiguous."""
+    if t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == (T, H, D):
+        if t.is_contiguous():
+            return H * D
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == D or H == 1):
+            return s0 if T > 1 else H * D
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return _token_stride(t[:, None], (T, 1, H, D), dev, name)
+
+
 def _held(table, lens, cu, T, dev):
     """Sequences and table width of a call with T rows."""
     if table.dim() != 2:
@@ -577,7 +589,7 @@ def paged_append(k_new, v_new, kp, vp, table, lens, cu=None, scores=None, stream
     T, H, D = k_new.shape
     dev = _device(k_new, "k_new")
     pages, _, page, _ = shape = kp.shape
-    sk, sv = (_token_stride(x[:, None], (T, 1, H, D), dev, name) for x, name in ((k_new, "k_new"), (v_new, "v_new")))
+    sk, sv = _row_stride(k_new, T, H, D, dev, "k_new"), _row_stride(v_new, T, H, D, dev, "v_new")
     if shape != (pages, H, page, D) or vp.shape != shape:
         raise ValueError(f"kp and vp must be [pages, {H}, page, {D}], got {list(shape)} and {list(vp.shape)}")
     pk, pv = _page_stride(kp, dev, "kp"), _page_stride(vp, dev, "vp")
