@@ -9,10 +9,10 @@
 // added up through distributed shared memory; the keys that share the first digit are set aside
 // for the others), then the kept slots in their order: a thread has consecutive slots, so one scan
 // gives every thread its place.  Bound by its chain of barriers.
-// evict_move: kept slot j goes from kept[j] >= j to j.  One CTA moves one column slice of K or V
-// (or the scores) of a head in rising order, a batch at a time: loads, barrier, stores.  The next
-// batch's sources lie at or above its own slots, so behind everything stored before: nothing is
-// lost and no second copy is needed.  Bound by memory.
+// evict_move: kept slot j goes from kept[j] >= j to j.  A CTA, or a cluster of them where there are few
+// heads, moves K (with the scores) or V of a head in rising order, a batch of rows at a time: loads,
+// barrier, stores.  The next batch's sources lie at or above its own slots, so behind everything stored
+// before: nothing is lost and no second copy is needed.  Bound by memory.
 #include <atomic>
 
 #include "paged.cuh"
@@ -22,12 +22,12 @@ namespace kvpop {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kTied = 2048;  // keys with the first digit of the k-th best that are set aside, at most
-constexpr int kCacheKeys = 49152;  // keys of a CTA's part held in shared memory, at most
+// Keys with the first digit of the k-th best that are set aside, at most: by a CTA, and of a cluster
+constexpr int kSet = 2048, kTied = 8192;
+constexpr int kCacheBytes = 163840;  // for the keys of a CTA's part, at most
 constexpr int kMaxCluster = 8;
-constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;  // pieces that a thread has in flight
-constexpr int kMoveRows = kMoveThreads * kMoveBatch / 2;  // rows of a batch, at most (32-byte slices)
+constexpr int kMoveFew = 1024, kMoveMany = 256;  // threads of a CTA with few heads and with many
 
 struct EvictParams {
   Paged c;
@@ -35,8 +35,8 @@ struct EvictParams {
   uint4 *k, *v;
   int64_t k_stride, v_stride;  // 16-byte pieces between pages
   int32_t *kept, *new_lens;
-  int s, w, top, B, slices;
-  int held;  // keys that the select's shared memory has room for
+  int s, w, top, B;
+  int held;  // groups of four keys that the select's shared memory has room for
 };
 
 // fp32 -> uint32 of the same order; NaN as -inf, -0 as +0
@@ -56,29 +56,30 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Exclusive sum over the block.  Two barriers.
+// Exclusive sums of two values over the block.  Two barriers.
 template <int THREADS>
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_s) {
-  uint32_t y = x;
+__device__ __forceinline__ uint2 block_scan(uint2 x, uint2* warp_s) {
+  uint2 y = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane_id() >= o) y += z;
+    const uint32_t a = __shfl_up_sync(0xffffffffu, y.x, o), b = __shfl_up_sync(0xffffffffu, y.y, o);
+    if (lane_id() >= o) y.x += a, y.y += b;
   }
   __syncthreads();  // the sums of the scan before have been read
   if (lane_id() == 31) warp_s[warp_id()] = y;
   __syncthreads();
-  uint32_t before = lane_id() < warp_id() ? warp_s[lane_id()] : 0;
-  return __reduce_add_sync(0xffffffffu, before) + y - x;
+  const uint2 before = lane_id() < warp_id() ? warp_s[lane_id()] : make_uint2(0, 0);
+  return make_uint2(__reduce_add_sync(0xffffffffu, before.x) + y.x - x.x, __reduce_add_sync(0xffffffffu, before.y) + y.y - x.y);
 }
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(const __grid_constant__ EvictParams p) {
   static_assert(THREADS / 32 <= 32 && 1024 % THREADS == 0, "one warp holds the warps' sums; whole bins a thread");
-  extern __shared__ __align__(16) uint32_t keys_s[];  // the part's keys, if they fit
+  extern __shared__ __align__(16) uint32_t keys_s[];  // the part's keys, if they fit, and the tied ones
   __shared__ uint32_t hists[2][kBins], total[kBins];  // a pass counts in one while the next one's is cleared
-  __shared__ uint32_t tied[kTied];                    // keys that share the first digit of the k-th best
-  __shared__ uint32_t warp_s[THREADS / 32];
+  uint32_t* tied = keys_s + (p.held + p.held / 8) * 4;  // keys that share the first digit of the k-th best
+  __shared__ uint32_t sets[kMaxCluster];              // how many the CTAs of the cluster have
+  __shared__ uint2 warp_s[THREADS / 32];
   __shared__ uint32_t found[2];   // the bin of the k-th best, and how many of it stay
   __shared__ uint32_t counts[2];  // keys of this part above the k-th best, and equal to it
   __shared__ uint32_t ntied;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
   // the slots that may go, [s, end), in groups of four: this CTA has groups [g0, g1)
   const int end = len - p.w, first = p.s & ~3, groups = (end - first + 3) / 4;
   const int g0 = (int)((long long)groups * rank / CS), g1 = (int)((long long)groups * (rank + 1) / CS);
-  const bool held = (g1 - g0) * 4 <= p.held;
+  const bool held = g1 - g0 <= p.held;
   const int32_t* table = c.table + (size_t)i * c.max_pages;
   // group g's keys; a table entry that names no page: the worst
   auto keys_at = [&](int g, int pg) -> uint4 {
@@ -110,8 +111,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
     if ((unsigned)pg < (unsigned)c.pages) x = *reinterpret_cast<const float4*>(p.scores + c.slot_row(pg, h, first + 4 * g));
     return make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
   };
+  // a gap after eight groups: consecutive groups of a thread then lie in different banks from its neighbours'
+  auto place = [](int g) { return g + (g >> 3); };
   auto keys_of = [&](int g) -> uint4 {
-    return held ? reinterpret_cast<const uint4*>(keys_s)[g - g0] : keys_at(g, table[(first + 4 * g) >> c.log_page]);
+    return held ? reinterpret_cast<const uint4*>(keys_s)[place(g - g0)] : keys_at(g, table[(first + 4 * g) >> c.log_page]);
   };
   // bit u: slot u of group g may go
   auto free_slots = [&](int g) -> uint32_t {
@@ -136,9 +139,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
       if (m >> u & 1) atomicAdd(&hist[bin[u]], 1u);
   };
   uint32_t prefix = 0, need = p.top;
-  // the bin of the k-th best from the counts of a pass, over the cluster
-  auto find = [&](const uint32_t* hist, int shift, int bins) {
-    if (CS > 1) {
+  // the bin of the k-th best from the counts of a pass, over the cluster or those of this CTA
+  auto find = [&](const uint32_t* hist, int shift, int bins, bool over_all) {
+    if (over_all) {
       // CTA r adds up its share of the bins over the cluster and hands the sums to all
       cluster_sync();
       const int per = bins / CS;
@@ -156,12 +159,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
     } else {
       __syncthreads();
     }
-    const uint32_t* sums = CS > 1 ? total : hist;
+    const uint32_t* sums = over_all ? total : hist;
     // from the best bin down: thread `tid` has bins [top - per, top) of them
     const int per = bins / THREADS, top = bins - tid * per;
     uint32_t mine = 0;
     for (int b = 1; b <= per; ++b) mine += sums[top - b];
-    const uint32_t before = block_scan<THREADS>(mine, warp_s);
+    const uint32_t before = block_scan<THREADS>(make_uint2(mine, 0), warp_s).x;
     if (before < need && need <= before + mine) {
       uint32_t at = before;
       for (int b = 1; b <= per; ++b) {
@@ -196,13 +199,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
       if (base + v * THREADS + (tid & ~31) >= g1) break;  // nothing for this warp
       if (g < g1) {
         if ((unsigned)pg[v] >= (unsigned)c.pages) report_page(c.status, i);
-        if (held) reinterpret_cast<uint4*>(keys_s)[g - g0] = x[v];
+        if (held) reinterpret_cast<uint4*>(keys_s)[place(g - g0)] = x[v];
       }
       count(hists[0], g < g1 ? free_slots(g) : 0, x[v], 21, 2048);
     }
   }
   for (int b = tid; b < kBins; b += THREADS) hists[1][b] = 0;
-  find(hists[0], 21, 2048);
+  find(hists[0], 21, 2048, CS > 1);
   // the keys that share it, by themselves if they are not too many
   auto ties = [&](int g, const uint4& x, int shift) -> uint32_t {
     const uint32_t d = prefix >> shift;
@@ -210,29 +213,53 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
   };
   for (int base = g0; base < g1; base += THREADS) {
     const int g = base + tid;
-    if (g >= g1) break;
-    const uint4 x = keys_of(g);
-    const uint32_t m = ties(g, x, 21);
-    if (m) {
-      uint32_t at = atomicAdd(&ntied, (uint32_t)__popc(m));
-      const uint32_t key[4] = {x.x, x.y, x.z, x.w};
+    const uint4 x = g < g1 ? keys_of(g) : make_uint4(0, 0, 0, 0);
+    const uint32_t m = g < g1 ? ties(g, x, 21) : 0, key[4] = {x.x, x.y, x.z, x.w};
+    // one addition a warp
+    uint32_t n = 0, mine[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (m >> u & 1) {
-          if (at < kTied) tied[at] = key[u];
-          ++at;
-        }
+    for (int u = 0; u < 4; ++u) {
+      const unsigned b = __ballot_sync(0xffffffffu, m >> u & 1);
+      mine[u] = n + __popc(b & ((1u << lane_id()) - 1));
+      n += __popc(b);
     }
+    if (n == 0) continue;
+    uint32_t at = lane_id() == 0 ? atomicAdd(&ntied, n) : 0;
+    at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if ((m >> u & 1) && at + mine[u] < kSet) tied[at + mine[u]] = key[u];
   }
   for (int b = tid; b < kBins; b += THREADS) hists[0][b] = 0;
+  // In a cluster every CTA takes the others' sets to its own, and the other digits need no more of it
   __syncthreads();
-  const bool few = ntied <= kTied;
+  bool few = ntied <= kSet;
+  uint32_t n = ntied;
+  if (CS > 1) {
+    cluster_sync();
+    if (tid < CS) sets[tid] = ld_cluster_u32(cluster_addr(smem_u32(&ntied), tid));
+    __syncthreads();
+    for (int r = 0; r < CS; ++r) {
+      few = few && sets[r] <= kSet;
+      if (r != rank) n += sets[r];
+    }
+    few = few && n <= (uint32_t)kTied;
+    if (few) {
+      uint32_t at = sets[rank];
+      for (int r = 0; r < CS; ++r) {
+        if (r == rank) continue;
+        for (uint32_t k = tid; k < sets[r]; k += THREADS) tied[at + k] = ld_cluster_u32(cluster_addr(smem_u32(&tied[k]), r));
+        at += sets[r];
+      }
+    }
+    cluster_sync();
+  }
 #pragma unroll 1
   for (int pass = 1; pass < 3; ++pass) {
     const int above = pass == 1 ? 21 : 10, shift = pass == 1 ? 10 : 0, bins = pass == 1 ? 2048 : 1024;
     uint32_t* hist = hists[pass & 1];
     if (few) {
-      for (int k = tid; k < (int)ntied; k += THREADS)
+      for (uint32_t k = tid; k < n; k += THREADS)
         if (tied[k] >> above == prefix >> above) atomicAdd(&hist[tied[k] >> shift & bins - 1], 1u);
     } else {
       for (int base = g0; base < g1; base += THREADS) {
@@ -241,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
         count(hist, g < g1 ? ties(g, x, above) : 0, x, shift, bins);
       }
     }
-    find(hist, shift, bins);
+    find(hist, shift, bins, CS > 1 && !few);
   }
   // prefix is the k-th best key, and `need` of its slots stay, the lowest ones.  A thread has `per`
   // consecutive groups; bits: slots of the first eight above the k-th best, and equal to it
@@ -260,8 +287,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
     }
   }
   const uint32_t mine_above = above, mine_equal = equal;
-  above = block_scan<THREADS>(above, warp_s);
-  equal = block_scan<THREADS>(equal, warp_s);
+  const uint2 sums = block_scan<THREADS>(make_uint2(above, equal), warp_s);
+  above = sums.x;
+  equal = sums.y;
   if (CS > 1) {
     if (tid == THREADS - 1) {
       counts[0] = above + mine_above;
@@ -302,84 +330,73 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
   if (CS > 1) cluster_sync();  // nobody leaves while its counts are read
 }
 
-// Where a batch's rows come from and go to; -1: nothing to move.  Three batches: of the one that is
-// looked up, the one that is loaded, and the one before, which slower warps may still be storing.
-struct Moves {
-  int64_t src[3][kMoveRows], dst[3][kMoveRows];
-};
-
-// Kept rows j -> their slots, BATCH pieces of type V a thread and batch, `per` pieces a row.
-// at(page, place) is the row's first piece.
-template <int BATCH, typename V, typename At>
-__device__ __forceinline__ void move_rows(const EvictParams& p, Moves& m, const int32_t* kept, int i, int per, V* base, At at) {
-  const Paged& c = p.c;
-  const int32_t* table = c.table + (size_t)i * c.max_pages;
-  const int rows = kMoveThreads / per, batch = rows * BATCH, r = threadIdx.x / per, x = threadIdx.x - r * per;
-  auto resolve = [&](int j0, int buf) {
-    // a thread's lookups together: one wait for the slots, one for their pages
-    constexpr int kLook = kMoveRows / kMoveThreads;
-    int t[kLook], from[kLook], to[kLook];
-#pragma unroll
-    for (int u = 0; u < kLook; ++u) {
-      const int k = threadIdx.x + u * kMoveThreads;
-      t[u] = k < batch && j0 + k < p.B ? kept[j0 + k] : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < kLook; ++u) {
-      const int j = j0 + threadIdx.x + u * kMoveThreads;
-      from[u] = t[u] > j ? table[t[u] >> c.log_page] : 0;
-      to[u] = t[u] > j ? table[j >> c.log_page] : 0;
-    }
-#pragma unroll
-    for (int u = 0; u < kLook; ++u) {
-      const int k = threadIdx.x + u * kMoveThreads, j = j0 + k;
-      if (k >= batch) break;
-      const bool there = (unsigned)from[u] < (unsigned)c.pages && (unsigned)to[u] < (unsigned)c.pages;
-      if (!there) report_page(c.status, i);
-      const bool moves = t[u] > j && there;
-      m.src[buf][k] = moves ? at(from[u], t[u]) : -1;
-      m.dst[buf][k] = moves ? at(to[u], j) : -1;
-    }
-  };
-  resolve(0, 0);
-  __syncthreads();
-  for (int j0 = 0, buf = 0, next = 1; j0 < p.B; j0 += batch, buf = next, next = next == 2 ? 0 : next + 1) {
-    V y[BATCH];
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int64_t src = m.src[buf][u * rows + r];
-      if (src >= 0) y[u] = base[src + x];
-    }
-    if (j0 + batch < p.B) resolve(j0 + batch, next);
-    __syncthreads();  // the whole batch has been read
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int64_t dst = m.dst[buf][u * rows + r];
-      if (dst >= 0) base[dst + x] = y[u];
-    }
-  }
-}
-
-__global__ void __launch_bounds__(kMoveThreads, 4) evict_move(const __grid_constant__ EvictParams p) {
-  __shared__ Moves moves;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) evict_move(const __grid_constant__ EvictParams p) {
+  constexpr int kRows = THREADS;  // of a batch, at most (D = 64)
+  // Pages that a batch's rows come from and go to, and their slots; -1: nothing to move.  Three batches:
+  // the one that is looked up, the one that is loaded, and the one before, which slower warps may
+  // still be storing.
+  __shared__ int from_s[3][kRows], to_s[3][kRows], slot_s[3][kRows];
   grid_dep_wait();
   grid_dep_launch();
   const Paged& c = p.c;
-  const int i = blockIdx.y / c.H, h = blockIdx.y - i * c.H, part = blockIdx.x;
+  const int CS = gridDim.x / 2, rank = blockIdx.x % CS;
+  const bool is_v = (int)blockIdx.x >= CS;
+  const int i = blockIdx.y / c.H, h = blockIdx.y - i * c.H;
   const int32_t* kept = p.kept + (size_t)blockIdx.y * p.B;
-  const int ch = c.D / 8, per = ch / p.slices;  // pieces of a row, and of a slice
-  if (part == 2 * p.slices) {
-    // new_lens may be lens: nothing else here reads it
-    if (h == 0 && threadIdx.x == 0) p.new_lens[i] = min(c.len(i), p.B);
-    move_rows<kMoveRows / kMoveThreads>(p, moves, kept, i, 1, p.scores, [&](int pg, int t) { return (int64_t)c.slot_row(pg, h, t); });
-    return;
-  }
-  const bool is_v = part >= p.slices;
+  const int32_t* table = c.table + (size_t)i * c.max_pages;
+  // new_lens may be lens: nothing else here reads it
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) p.new_lens[i] = min(c.len(i), p.B);
+  uint4* base = is_v ? p.v : p.k;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
-  const int x0 = (part - (is_v ? p.slices : 0)) * per;
-  move_rows<kMoveBatch>(p, moves, kept, i, per, is_v ? p.v : p.k, [&](int pg, int t) {
-    return pg * stride + (int64_t)(((size_t)h << c.log_page) + (t & ((1 << c.log_page) - 1))) * ch + x0;
-  });
+  const int ch = c.D / 8, rows = THREADS / ch, mine = rows * kMoveBatch;  // pieces of a row; rows at a time, and of a batch
+  const int r = threadIdx.x / ch, x = threadIdx.x - r * ch, in_page = (1 << c.log_page) - 1;
+  auto piece = [&](int pg, int t) { return base + pg * stride + (int64_t)(((size_t)h << c.log_page) + (t & in_page)) * ch + x; };
+  // one row a thread: the rows of this CTA's part of the batch at j0
+  auto look_up = [&](int j0, int buf) {
+    const int k = threadIdx.x, j = j0 + rank * mine + k;
+    if (k >= mine) return;
+    const int t = j < p.B ? kept[j] : -1;
+    int from = -1, to = -1;
+    if (t > j) {
+      from = table[t >> c.log_page];
+      to = table[j >> c.log_page];
+      if ((unsigned)from >= (unsigned)c.pages || (unsigned)to >= (unsigned)c.pages) {
+        report_page(c.status, i);
+        from = to = -1;
+      }
+    }
+    from_s[buf][k] = from;
+    to_s[buf][k] = to;
+    slot_s[buf][k] = t;
+  };
+  look_up(0, 0);
+  __syncthreads();
+  const int batch = CS * mine;
+  for (int j0 = 0, buf = 0, next = 1; j0 < p.B; j0 += batch, buf = next, next = next == 2 ? 0 : next + 1) {
+    uint4 y[kMoveBatch];
+    float w[kMoveBatch];
+#pragma unroll
+    for (int u = 0; u < kMoveBatch; ++u) {
+      const int k = u * rows + r, pg = from_s[buf][k], t = slot_s[buf][k];
+      if (pg >= 0) {
+        y[u] = *piece(pg, t);
+        if (!is_v && x == 0) w[u] = p.scores[c.slot_row(pg, h, t)];
+      }
+    }
+    if (j0 + batch < p.B) look_up(j0 + batch, next);
+    // the whole batch has been read
+    if (CS > 1) cluster_sync();
+    else __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMoveBatch; ++u) {
+      const int k = u * rows + r, pg = to_s[buf][k], j = j0 + rank * mine + k;
+      if (pg >= 0) {
+        *piece(pg, j) = y[u];
+        if (!is_v && x == 0) p.scores[c.slot_row(pg, h, j)] = w[u];
+      }
+    }
+  }
 }
 
 }  // namespace
@@ -431,13 +448,13 @@ extern "C" kvpop_status kvpop_paged_evict(void* kp, int64_t kp_stride, void* vp,
   const long long heads = (long long)n * H, most = (long long)max_pages * page;
   int CS = 1;
   while (CS < kMaxCluster && heads * CS * 2 <= 2ll * num_sms() && most / (CS * 2) >= 2048) CS *= 2;
-  prm.held = (int)min((long long)kCacheKeys, (most / CS + 16) / 4 * 4);
+  prm.held = (int)min((long long)(kCacheBytes / 16 * 8 / 9), most / CS / 4 + 4);
   auto select = CS > 1 ? evict_select<1024> : evict_select<512>;
   static std::atomic<uint64_t> ready{0};  // bit d: the kernels are set up on device d
   const int dev = current_device();
   if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
     for (auto kern : {evict_select<1024>, evict_select<512>}) {
-      st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheKeys * 4),
+      st = cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCacheBytes + kTied * 4),
                       "kvpop_paged_evict: smem attribute");
       if (st != KVPOP_OK) return st;
     }
@@ -446,7 +463,7 @@ extern "C" kvpop_status kvpop_paged_evict(void* kp, int64_t kp_stride, void* vp,
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CS, (unsigned)heads);
   cfg.blockDim = dim3(CS > 1 ? 1024 : 512);
-  cfg.dynamicSmemBytes = (size_t)prm.held * 4;
+  cfg.dynamicSmemBytes = ((size_t)prm.held + prm.held / 8) * 16 + (CS > 1 ? kTied : kSet) * 4;
   cfg.stream = cs;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -459,9 +476,14 @@ extern "C" kvpop_status kvpop_paged_evict(void* kp, int64_t kp_stride, void* vp,
   cfg.numAttrs = 2;
   st = cuda_check(cudaLaunchKernelEx(&cfg, select, prm), "kvpop_paged_evict: launch");
   if (st != KVPOP_OK) return st;
-  // column slices of a head's K and V: down to 32 bytes, until there are four CTAs an SM
-  prm.slices = 1;
-  while (prm.slices < D / 16 && heads * 2 * prm.slices < 4ll * num_sms()) prm.slices *= 2;
-  return cuda_check(launch_pdl(evict_move, dim3(2 * prm.slices + 1, (unsigned)heads), dim3(kMoveThreads), 0, cs, prm),
+  // CTAs a head's K (and as many its V): one an SM as long as there are few heads, and rows for them
+  const bool few = heads * 2 <= num_sms();
+  int CM = 1;
+  while (CM < kMaxCluster && heads * 4 * CM <= num_sms() && (long long)CM * kMoveFew / (D / 8) * kMoveBatch < B) CM *= 2;
+  cfg.gridDim = dim3(2 * CM, (unsigned)heads);
+  cfg.blockDim = dim3(few ? kMoveFew : kMoveMany);
+  cfg.dynamicSmemBytes = 0;
+  attr[1].val.clusterDim.x = CM;
+  return cuda_check(cudaLaunchKernelEx(&cfg, few ? evict_move<kMoveFew> : evict_move<kMoveMany>, prm),
                     "kvpop_paged_evict: move launch");
 }
