@@ -78,7 +78,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
   extern __shared__ __align__(16) uint32_t keys_s[];  // the part's keys, if they fit, and the tied ones
   __shared__ uint32_t hists[2][kBins], total[kBins];  // a pass counts in one while the next one's is cleared
   uint32_t* tied = keys_s + (p.held + p.held / 8) * 4;  // keys that share the first digit of the k-th best
-  __shared__ uint32_t sets[kMaxCluster];              // how many the CTAs of the cluster have
   __shared__ uint2 warp_s[THREADS / 32];
   __shared__ uint32_t found[2];   // the bin of the k-th best, and how many of it stay
   __shared__ uint32_t counts[2];  // keys of this part above the k-th best, and equal to it
@@ -236,22 +235,25 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
   bool few = ntied <= kSet;
   uint32_t n = ntied;
   if (CS > 1) {
+    // threads / 8 to each of the others
     cluster_sync();
-    if (tid < CS) sets[tid] = ld_cluster_u32(cluster_addr(smem_u32(&ntied), tid));
-    __syncthreads();
-    for (int r = 0; r < CS; ++r) {
-      few = few && sets[r] <= kSet;
-      if (r != rank) n += sets[r];
+    const int r = tid * kMaxCluster / THREADS, k0 = tid % (THREADS / kMaxCluster);
+    uint32_t to = n, of = 0, sum = 0, most = 0;
+#pragma unroll
+    for (int x = 0; x < kMaxCluster; ++x) {
+      const uint32_t y = x < CS ? ld_cluster_u32(cluster_addr(smem_u32(&ntied), x)) : 0;
+      sum += y;
+      most = max(most, y);
+      if (x == r) of = y;
+      if (x < r && x != rank) to += y;
     }
-    few = few && n <= (uint32_t)kTied;
-    if (few) {
-      uint32_t at = sets[rank];
-      for (int r = 0; r < CS; ++r) {
-        if (r == rank) continue;
-        for (uint32_t k = tid; k < sets[r]; k += THREADS) tied[at + k] = ld_cluster_u32(cluster_addr(smem_u32(&tied[k]), r));
-        at += sets[r];
-      }
+    few = most <= kSet && sum <= kTied;
+    if (few && r < CS && r != rank) {
+#pragma unroll 4
+      for (uint32_t k = k0; k < of; k += THREADS / kMaxCluster)
+        tied[to + k] = ld_cluster_u32(cluster_addr(smem_u32(&tied[k]), r));
     }
+    n = sum;
     cluster_sync();
   }
 #pragma unroll 1
@@ -307,6 +309,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
       above += a[r];
       equal += e[r];
     }
+    // Both sums go through the barrier, so that the others' counts have been read when it is reached;
+    // what this CTA still writes is no business of the cluster's
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" : "+r"(above), "+r"(equal)::"memory");
   }
   auto keep = [&](bool is_above, int t) {
     if (is_above || equal < need) kept[p.s + above + min(equal, need)] = t;
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 4 : 1) evict_select(
         if ((m >> u & 1) && key[u] >= prefix) keep(key[u] > prefix, first + 4 * g + u);
     }
   }
-  if (CS > 1) cluster_sync();  // nobody leaves while its counts are read
+  if (CS > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // nobody leaves while its counts are read
 }
 
 template <int THREADS>
