@@ -824,32 +824,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 
 // The items that several of paged_kernel's CTAs shared, each joined from the slots of its CTAs in
 // their order: CTA (x, y) takes rows y of those whose second CTA is in the x-th part of the CTAs.
-// Thread (part, c4, row) takes four columns and every parts-th slot; the parts are joined through
-// shared memory.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads, 4) paged_merge(const __grid_constant__ AttnParams p, int ctas, int parts) {
-  constexpr int kBatch = 4;
+// Thread (part, c4, row) takes four columns of ROWS rows and every parts-th slot, SLOTS of them at a
+// time; the parts are joined through shared memory.  Decode rows have many slots of few rows, blocks
+// of a chunk two or three slots of 256: with one row a thread the mixed step of 12
+// sequences spent 22 us here, with four 15.
+template <int D, int ROWS, int SLOTS>
+__global__ void __launch_bounds__(kMergeThreads, ROWS == 1 ? 4 : 2) paged_merge(const __grid_constant__ AttnParams p, int ctas, int parts) {
   __shared__ float2 ml_s[kMergeThreads];
   __shared__ float4 o_s[kMergeThreads];
+  static_assert(ROWS == 1 || SLOTS <= 2, "registers");
   grid_dep_launch();
   grid_dep_wait();
   const int wide = kMergeThreads / parts, rows = wide / (D / 4);
-  const int part = threadIdx.x / wide, x = threadIdx.x - part * wide, c4 = x / rows, r = blockIdx.y * rows + x - c4 * rows;
+  const int part = threadIdx.x / wide, x = threadIdx.x - part * wide, c4 = x / rows;
+  const int r0 = blockIdx.y * rows * ROWS + x - c4 * rows;  // and every rows-th after it
   const int lo = (int)((long long)ctas * blockIdx.x / gridDim.x), hi = (int)((long long)ctas * (blockIdx.x + 1) / gridDim.x);
   for (int w0 = lo; w0 < hi; w0 += 32) {
     const Split mine = w0 + lane_id() < hi ? p.split[w0 + lane_id()] : Split{0, 0, 0, 0};
-    unsigned todo = __ballot_sync(0xffffffffu, (int)blockIdx.y * rows < mine.nrow);
+    unsigned todo = __ballot_sync(0xffffffffu, (int)blockIdx.y * rows * ROWS < mine.nrow);
     while (todo) {  // the same in every warp
       const int src = __ffs(todo) - 1;
       todo &= todo - 1;
       const int row0 = __shfl_sync(0xffffffffu, mine.row0, src), h = __shfl_sync(0xffffffffu, mine.h, src),
                 nrow = __shfl_sync(0xffffffffu, mine.nrow, src), c1 = __shfl_sync(0xffffffffu, mine.c1, src);
       const int c0 = w0 + src - 1;
-      const bool on = r < nrow;
-      const size_t orow = on ? (size_t)(row0 + (r >> p.log_g)) * p.Hq + h * p.G + (r & (p.G - 1)) : 0;
-      float M = neg_inf(), l = 0.0f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](const float2& ml, const float4& y, float m) {
+      float M[ROWS], l[ROWS];
+      float4 o[ROWS];
+#pragma unroll
+      for (int u = 0; u < ROWS; ++u) {
+        M[u] = neg_inf();
+        l[u] = 0.0f;
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      auto add = [](const float2& ml, const float4& y, float m, float& l, float4& o) {
         const float f = ml.x != neg_inf() ? ex2_approx(ml.x - m) : 0.0f;
         l += f * ml.y;
         if (ml.x != neg_inf()) {
@@ -859,48 +866,60 @@ __global__ void __launch_bounds__(kMergeThreads, 4) paged_merge(const __grid_con
           o.w += f * y.w;
         }
       };
-      for (int c = c0 + part; on && c <= c1; c += kBatch * parts) {
-        float2 ml[kBatch];
-        float4 y[kBatch];
+      for (int c = c0 + part; c <= c1; c += SLOTS * parts) {
+        float2 ml[ROWS][SLOTS];
+        float4 y[ROWS][SLOTS];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int cc = c + k * parts;
-          ml[k] = make_float2(neg_inf(), 0.0f);
-          y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (cc <= c1) {
-            const size_t slot = (size_t)cc * 2 + (cc == c0 ? 1 : 0);  // the item begins in c0's share
-            ml[k] = p.part_ml[slot * kBlockRows + r];
-            y[k] = p.part_o[((slot * 2 + (r >> 7)) * (D / 4) + c4) * 128 + (r & 127)];
+        for (int u = 0; u < ROWS; ++u)
+#pragma unroll
+          for (int k = 0; k < SLOTS; ++k) {
+            const int cc = c + k * parts, r = r0 + u * rows;
+            ml[u][k] = make_float2(neg_inf(), 0.0f);
+            y[u][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (cc <= c1 && r < nrow) {
+              const size_t slot = (size_t)cc * 2 + (cc == c0 ? 1 : 0);  // the item begins in c0's share
+              ml[u][k] = p.part_ml[slot * kBlockRows + r];
+              y[u][k] = p.part_o[((slot * 2 + (r >> 7)) * (D / 4) + c4) * 128 + (r & 127)];
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < ROWS; ++u) {
+          float m = M[u];
+#pragma unroll
+          for (int k = 0; k < SLOTS; ++k) m = fmaxf(m, ml[u][k].x);
+          if (m != neg_inf()) {
+            const float f = M[u] != neg_inf() ? ex2_approx(M[u] - m) : 0.0f;
+            l[u] *= f;
+            o[u].x *= f, o[u].y *= f, o[u].z *= f, o[u].w *= f;
+            M[u] = m;
+#pragma unroll
+            for (int k = 0; k < SLOTS; ++k) add(ml[u][k], y[u][k], m, l[u], o[u]);
           }
         }
-        float m = M;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) m = fmaxf(m, ml[k].x);
-        if (m != neg_inf()) {
-          const float f = M != neg_inf() ? ex2_approx(M - m) : 0.0f;
-          l *= f;
-          o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-          M = m;
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) add(ml[k], y[k], m);
+      }
+      if (parts > 1) {  // ROWS = 1
+        ml_s[threadIdx.x] = make_float2(M[0], l[0]);
+        o_s[threadIdx.x] = o[0];
+        __syncthreads();
+        if (part == 0) {
+          for (int k = 1; k < parts; ++k) M[0] = fmaxf(M[0], ml_s[x + k * wide].x);
+          l[0] = 0.0f;
+          o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; M[0] != neg_inf() && k < parts; ++k) add(ml_s[x + k * wide], o_s[x + k * wide], M[0], l[0], o[0]);
         }
       }
-      ml_s[threadIdx.x] = make_float2(M, l);
-      o_s[threadIdx.x] = o;
-      __syncthreads();
-      if (on && part == 0) {
-        if (parts > 1) {
-          for (int k = 1; k < parts; ++k) M = fmaxf(M, ml_s[x + k * wide].x);
-          l = 0.0f;
-          o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int k = 0; M != neg_inf() && k < parts; ++k) add(ml_s[x + k * wide], o_s[x + k * wide], M);
+#pragma unroll
+      for (int u = 0; u < ROWS; ++u) {
+        const int r = r0 + u * rows;
+        if (part == 0 && r < nrow) {
+          const size_t orow = (size_t)(row0 + (r >> p.log_g)) * p.Hq + h * p.G + (r & (p.G - 1));
+          const float inv = l[u] != 0.0f ? 1.0f / l[u] : 0.0f;
+          *reinterpret_cast<uint2*>(p.O + orow * D + 4 * c4) =
+              make_uint2(pack_bf16x2(o[u].x * inv, o[u].y * inv), pack_bf16x2(o[u].z * inv, o[u].w * inv));
+          if (c4 == 0) p.lse[orow] = l[u] != 0.0f ? (M[u] + __log2f(l[u])) * 0.69314718055994531f : neg_inf();
         }
-        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-        *reinterpret_cast<uint2*>(p.O + orow * D + 4 * c4) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (c4 == 0) p.lse[orow] = l != 0.0f ? (M + __log2f(l)) * 0.69314718055994531f : neg_inf();
       }
-      __syncthreads();
+      if (parts > 1) __syncthreads();
     }
   }
 }
@@ -937,16 +956,18 @@ kvpop_status launch(AttnParams& prm, int ctas, cudaStream_t cs) {
   }
   st = cuda_check(launch_pdl(kern, dim3(ctas), dim3(kThreads), L::total, cs, prm), "kvpop_paged_attn: launch");
   if (st != KVPOP_OK) return st;
-  // A thread of the merge takes about four slots of a row, a CTA at least four rows (two sectors of a
-  // slot's columns).  There are at most `items` items, and at most one a CTA that several CTAs share.
+  // There are at most `items` items, of at most `most` rows, and at most one a CTA that several CTAs share.
+  // With few items for the CTAs a thread takes about four slots of a row, and its CTA at least four rows
+  // (two sectors of a slot's columns); otherwise four rows, of all slots.
   const long long rows_all = (long long)prm.c.T * prm.G;
   const long long items = prm.c.H * (prm.c.n + rows_all / kBlockRows);
+  const int most = prm.c.cu ? (int)min((long long)kBlockRows, rows_all) : prm.G;
   int parts = 1;
   while (kMergeThreads / (D / 4) / parts > 4 && ctas > 4 * parts * items) parts *= 2;
-  const int rows = kMergeThreads / (D / 4) / parts;
-  const int chunks = ((int)min((long long)kBlockRows, rows_all) + rows - 1) / rows;
-  return cuda_check(launch_pdl(paged_merge<D>, dim3((unsigned)min((long long)ctas, items), chunks), dim3(kMergeThreads), 0, cs,
-                               prm, ctas, parts),
+  const bool few = ctas > 4 * items || most <= kMergeThreads / (D / 4);
+  const int rows = kMergeThreads / (D / 4) / parts * (few ? 1 : 4);
+  const dim3 grid((unsigned)min((long long)ctas, items), (most + rows - 1) / rows);
+  return cuda_check(launch_pdl(few ? paged_merge<D, 1, 4> : paged_merge<D, 4, 2>, grid, dim3(kMergeThreads), 0, cs, prm, ctas, parts),
                     "kvpop_paged_attn: merge launch");
 }
 
