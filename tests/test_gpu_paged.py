@@ -628,3 +628,84 @@ def test_serving_loop():
                 used = -(-lens[i] // page)
                 free += [int(t) for t in table[i, used:] if t >= 0]
                 table[i, used:] = -1
+
+
+def test_many_sequences():
+    """More sequences than a warp takes at a time, whole windows of them without rows or without
+    slots, and shares that begin in a later window."""
+    chunks = [[0, 1, 2, 40][i % 4] if not 64 <= i < 140 else 0 for i in range(300)]
+    lens = [(i * 37) % 400 if not 160 <= i < 230 else 0 for i in range(300)]
+    c = Held(lens, 1, 16, 64, seed=12)
+    cu = sums(chunks)
+    q = c.randn(cu[-1], 4, 64)
+    O, lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32(cu))
+    check_attn(O, lse, q, c, cu)
+    before = c.scores.clone()
+    check_mass(kvpop.paged_mass(q, lse, c.kp, c.scores, c.table, c.lens, i32(cu), decay=0.5), before, q, lse, c, cu, 0.5)
+
+
+def test_sums_of_more_than_one_run():
+    """A CTA's tiles of one item beyond the 256 that it sums in one run: decode rows over so many
+    slots, blocks of 256 rows, and received weight of so many query tiles."""
+    c = Held([5_600_000], 1, 1024, 64, seed=21)
+    c.vp += 1  # a sum that does not cancel
+    q = c.randn(1, 1, 64)
+    O, lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens)
+    check_attn(O, lse, q, c, [0, 1])
+    c = Held([33000], 152, 128, 64, seed=22)
+    q = c.randn(64, 152 * 4, 64)
+    O, lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32([0, 64]))
+    check_attn(O, lse, q, c, [0, 64])
+    c = Held([530], 152, 64, 64, seed=23)
+    q = c.randn(530, 152 * 128, 64)
+    lse = torch.full((530, 152 * 128), 6.5, device="cuda") + torch.randn(530, 152 * 128, generator=c.gen, device="cuda") * 0.1
+    before = c.scores.clone()
+    check_mass(kvpop.paged_mass(q, lse, c.kp, c.scores, c.table, c.lens, i32([0, 530])), before, q, lse, c, [0, 530], 1.0)
+
+
+@pytest.mark.parametrize("D,G,S,page", [(128, 4, 900, 64), (64, 2, 515, 16)])
+def test_against_the_contiguous_calls(D, G, S, page):
+    """A whole prompt: the attention over the pages is the library's dense attention (its tolerances,
+    2e-2 and 2e-3), and the weight that its keys receive is the future target with an empty window
+    (the log of the same sum, 2e-2)."""
+    H = 2
+    c = Held([S], H, page, D, seed=D)
+    q, k, v = c.randn(S, H * G, D), c.randn(S, H, D), c.randn(S, H, D)
+    kvpop.paged_append(k, v, c.kp, c.vp, c.table, c.lens, i32([0, S]), scores=c.scores)
+    O, lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32([0, S]))
+    dO, dl = kvpop.attn_fwd(q[None], k[None], v[None])
+    assert float((O.float() - dO[0].float()).abs().max()) <= 2e-2
+    assert float((lse - dl[0].T).abs().max()) <= 2e-3
+    kvpop.paged_mass(q, lse, c.kp, c.scores, c.table, c.lens, i32([0, S]))
+    target = kvpop.future_target(q[None], k[None], dl, 0)
+    for h in range(H):
+        got = ref.slots(c.scores, c.table, 0, h, S).log()
+        assert float((got - target[0, h]).abs().max()) <= 2e-2
+
+
+def test_two_graphs_in_turn():
+    """Two captured steps on the same cache, replayed in turn on two streams' order: each has its
+    own workspace, and each replay equals the eager calls."""
+    lens, cu = [700, 130], [0, 40, 41]
+    c = Held(lens, 2, 32, 128, seed=31)
+    q1, q2 = c.randn(41, 8, 128), c.randn(41, 8, 128)
+
+    def step(q, scores):
+        O, lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32_cu)
+        return O, lse, kvpop.paged_mass(q, lse, c.kp, scores, c.table, c.lens, i32_cu, decay=0.0)
+    i32_cu = i32(cu)
+    want = [step(q, c.scores.clone()) for q in (q1, q2)]
+    graphs, outs = [], []
+    for q in (q1, q2):
+        mine = c.scores.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(q, mine))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+        assert torch.equal(got[2][c.used()], w[2][c.used()])
