@@ -537,8 +537,6 @@ def prefix_attn(q, pk, pv, cu=None, lens=None, join=None, scale: float = 0.0, wo
 
 def _page_stride(x, dev, name):
     """Elements between the pages of a bf16 [pages, H, page, D] cache whose pages are contiguous."""
-    if x.dim() != 4:
-        raise ValueError(f"{name} must be [pages, H, page, D]")
     if x.is_contiguous() and x.dtype is torch.bfloat16 and x.get_device() == dev:
         return x.stride(0)
     if not x.is_cuda:
@@ -565,18 +563,31 @@ def _row_stride(t, T, H, D, dev, name):
     return _token_stride(t[:, None], (T, 1, H, D), dev, name)
 
 
-def _held(table, lens, cu, T, dev):
-    """Sequences and table width of a call with T rows."""
+def _paged_args(kp, vp, table, lens, cu, T, D, dev):
+    """(pages, H, page, elements between the pages of kp and of vp, n, max_pages) of a call with T
+    rows; vp may be None."""
+    shape = kp.shape
+    if len(shape) != 4 or shape[3] != D:
+        raise ValueError(f"kp must be [pages, H, page, {D}], got {list(shape)}")
     if table.dim() != 2:
         raise ValueError("table must be [n, max_pages]")
     n, most = table.shape
-    _fit(table, torch.int32, dev, (n, most), "table")
-    _fit(lens, torch.int32, dev, (n,), "lens")
+    i32 = torch.int32
+    # the cheap questions together: a small call costs the host more than the GPU
+    if not (table.dtype is i32 and lens.dtype is i32 and table.get_device() == dev and lens.get_device() == dev
+            and table.is_contiguous() and lens.is_contiguous() and lens.shape == (n,)):
+        _fit(table, i32, dev, (n, most), "table")
+        _fit(lens, i32, dev, (n,), "lens")
     if cu is not None:
-        _fit(cu, torch.int32, dev, (n + 1,), "cu")
+        _fit(cu, i32, dev, (n + 1,), "cu")
     elif T != n:
         raise ValueError(f"cu is needed with {T} rows of {n} sequences")
-    return n, most
+    pk = _page_stride(kp, dev, "kp")
+    if vp is None:
+        return shape[0], shape[1], shape[2], pk, 0, n, most
+    if vp.shape != shape:
+        raise ValueError(f"vp must be {list(shape)}, got {list(vp.shape)}")
+    return shape[0], shape[1], shape[2], pk, _page_stride(vp, dev, "vp"), n, most
 
 
 def paged_append(k_new, v_new, kp, vp, table, lens, cu=None, scores=None, stream=None):
@@ -584,16 +595,14 @@ def paged_append(k_new, v_new, kp, vp, table, lens, cu=None, scores=None, stream
     kp, vp [pages,H,page,D]: rows cu[i]..cu[i+1]-1 (int32 [n+1]; None: one each) become the
     last of the lens[i] slots that table [n,max_pages] gives sequence i.  The weights of
     the new slots in scores [pages,H,page] become 0."""
-    if k_new.dim() != 3 or kp.dim() != 4:
-        raise ValueError("k_new must be [T, H, D] and kp [pages, H, page, D]")
+    if k_new.dim() != 3:
+        raise ValueError("k_new must be [T, H, D]")
     T, H, D = k_new.shape
     dev = _device(k_new, "k_new")
-    pages, _, page, _ = shape = kp.shape
     sk, sv = _row_stride(k_new, T, H, D, dev, "k_new"), _row_stride(v_new, T, H, D, dev, "v_new")
-    if shape != (pages, H, page, D) or vp.shape != shape:
-        raise ValueError(f"kp and vp must be [pages, {H}, page, {D}], got {list(shape)} and {list(vp.shape)}")
-    pk, pv = _page_stride(kp, dev, "kp"), _page_stride(vp, dev, "vp")
-    n, most = _held(table, lens, cu, T, dev)
+    pages, heads, page, pk, pv, n, most = _paged_args(kp, vp, table, lens, cu, T, D, dev)
+    if heads != H:
+        raise ValueError(f"kp must be [pages, {H}, page, {D}], got {list(kp.shape)}")
     if scores is not None:
         _fit(scores, torch.float32, dev, (pages, H, page), "scores")
     st = load().kvpop_paged_append(_p(k_new), sk, _p(v_new), sv, T, n, H, D, _p(cu), _p(lens), _p(table), most, _p(kp), pk,
@@ -625,16 +634,12 @@ def paged_attn(q, kp, vp, table, lens, cu=None, scale: float = 0.0, workspace=No
     """Causal attention of new tokens q [T,Hq,D] over the slots that their sequences hold,
     their own among them (appended before): table, lens, cu as for paged_append.  Returns
     (O [T,Hq,D] bf16, lse [T,Hq] fp32); rows of no sequence are not written."""
-    if q.dim() != 3 or kp.dim() != 4:
-        raise ValueError("q must be [T, Hq, D] and kp [pages, H, page, D]")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
     T, Hq, D = rows = q.shape
-    pages, H, page, _ = shape = kp.shape
     dev = _device(q, "q")
     _fit(q, torch.bfloat16, dev, rows, "q")
-    if shape[3] != D or vp.shape != shape:
-        raise ValueError(f"kp and vp must be [pages, H, page, {D}], got {list(shape)} and {list(vp.shape)}")
-    pk, pv = _page_stride(kp, dev, "kp"), _page_stride(vp, dev, "vp")
-    n, most = _held(table, lens, cu, T, dev)
+    pages, H, page, pk, pv, n, most = _paged_args(kp, vp, table, lens, cu, T, D, dev)
     with _on(stream):
         if out is None:
             O, lse = _empty_as(q), torch.empty((T, Hq), dtype=torch.float32, device=q.device)
@@ -659,18 +664,14 @@ def paged_mass(q, lse, kp, scores, table, lens, cu=None, scale: float = 0.0, dec
     """scores [pages,H,page] fp32 = decay * scores + the attention weight that each held key
     receives from the rows of q [T,Hq,D], whose log-sum-exp lse [T,Hq] is paged_attn's.  The
     rows may be the last ones of each chunk only (an observation window).  Returns scores."""
-    if q.dim() != 3 or kp.dim() != 4:
-        raise ValueError("q must be [T, Hq, D] and kp [pages, H, page, D]")
-    T, Hq, D = q.shape
-    pages, H, page, d = kp.shape
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq, D = rows = q.shape
     dev = _device(q, "q")
-    _fit(q, torch.bfloat16, dev, q.shape, "q")
+    _fit(q, torch.bfloat16, dev, rows, "q")
     _fit(lse, torch.float32, dev, (T, Hq), "lse")
-    if d != D:
-        raise ValueError(f"kp must be [pages, H, page, {D}], got {list(kp.shape)}")
-    pk = _page_stride(kp, dev, "kp")
+    pages, H, page, pk, _, n, most = _paged_args(kp, None, table, lens, cu, T, D, dev)
     _fit(scores, torch.float32, dev, (pages, H, page), "scores")
-    n, most = _held(table, lens, cu, T, dev)
     if workspace is None:
         with _on(stream):
             workspace = torch.empty(_paged_workspace("mass", dev, T, n, Hq, H, D, most, page), dtype=torch.uint8,
@@ -691,13 +692,9 @@ def paged_evict(kp, vp, scores, table, lens, s: int, w: int, k: int, out=None, s
     length; new_lens [n] int32)."""
     if kp.dim() != 4:
         raise ValueError("kp must be [pages, H, page, D]")
-    pages, H, page, D = shape = kp.shape
-    dev = _device(kp, "kp")
-    if vp.shape != shape:
-        raise ValueError(f"vp must be {list(shape)}, got {list(vp.shape)}")
-    pk, pv = _page_stride(kp, dev, "kp"), _page_stride(vp, dev, "vp")
+    D, dev = kp.shape[3], _device(kp, "kp")
+    pages, H, page, pk, pv, n, most = _paged_args(kp, vp, table, lens, None, table.shape[0], D, dev)
     _fit(scores, torch.float32, dev, (pages, H, page), "scores")
-    n, most = _held(table, lens, None, table.shape[0], dev)
     B = s + w + k
     if out is None:
         with _on(stream):
