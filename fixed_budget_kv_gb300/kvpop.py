@@ -184,6 +184,23 @@ def _on(stream):
     return _here if stream is None else torch.cuda.stream(stream)
 
 
+class _Scratch:
+    """A workspace for one call, from torch's allocator and back to it in the order of the stream: the
+    first tensor that a call makes next to a launch costs the host 5 us, plain memory half a one."""
+
+    __slots__ = ("nbytes", "handle", "ptr")
+
+    def __init__(self, nbytes, handle):
+        self.nbytes, self.handle = nbytes, handle
+
+    def __enter__(self):
+        self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(self.nbytes, self.handle)
+        return self.ptr, self.nbytes
+
+    def __exit__(self, *_):
+        torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
+
+
 def device_status(reset: bool = True):
     out = (c_i32 * 4)()
     st = load().kvpop_device_status(ctypes.cast(out, c_void_p), int(reset))
@@ -620,6 +637,14 @@ def _paged_workspace(what, dev, T, n, Hq, H, D, most, page) -> int:
     return nb.value
 
 
+def _paged_scratch(what, workspace, dev, T, n, Hq, H, D, most, page, handle):
+    """Address and bytes of the caller's workspace, or of one for this call."""
+    if workspace is None:
+        return _Scratch(_paged_workspace(what, dev, T, n, Hq, H, D, most, page), handle)
+    _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
+    return contextlib.nullcontext((workspace.data_ptr(), workspace.numel()))
+
+
 def paged_attn_workspace_size(T, n, Hq, H, D, max_pages, page) -> int:
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     return _paged_workspace("attn", dev, T, n, Hq, H, D, max_pages, page)
@@ -640,20 +665,17 @@ def paged_attn(q, kp, vp, table, lens, cu=None, scale: float = 0.0, workspace=No
     dev = _device(q, "q")
     _fit(q, torch.bfloat16, dev, rows, "q")
     pages, H, page, pk, pv, n, most = _paged_args(kp, vp, table, lens, cu, T, D, dev)
-    with _on(stream):
-        if out is None:
+    if out is None:
+        with _on(stream):
             O, lse = _empty_as(q), torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-        else:
-            O, lse = out
-            _fit(O, torch.bfloat16, dev, rows, "O")
-            _fit(lse, torch.float32, dev, (T, Hq), "lse")
-        if workspace is None:
-            workspace = torch.empty(_paged_workspace("attn", dev, T, n, Hq, H, D, most, page), dtype=torch.uint8,
-                                    device=q.device)
-        else:
-            _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
-    st = load().kvpop_paged_attn(_p(q), T, n, Hq, H, D, scale, _p(cu), _p(lens), _p(table), most, _p(kp), pk, _p(vp), pv,
-                                 pages, page, _p(O), _p(lse), _p(workspace), workspace.numel(), _stream(stream))
+    else:
+        O, lse = out
+        _fit(O, torch.bfloat16, dev, rows, "O")
+        _fit(lse, torch.float32, dev, (T, Hq), "lse")
+    s = _stream(stream)
+    with _paged_scratch("attn", workspace, dev, T, n, Hq, H, D, most, page, s) as (ws, nb):
+        st = load().kvpop_paged_attn(_p(q), T, n, Hq, H, D, scale, _p(cu), _p(lens), _p(table), most, _p(kp), pk, _p(vp), pv,
+                                     pages, page, _p(O), _p(lse), ws, nb, s)
     if st:
         _check(st, "kvpop_paged_attn")
     return O, lse
@@ -672,14 +694,10 @@ def paged_mass(q, lse, kp, scores, table, lens, cu=None, scale: float = 0.0, dec
     _fit(lse, torch.float32, dev, (T, Hq), "lse")
     pages, H, page, pk, _, n, most = _paged_args(kp, None, table, lens, cu, T, D, dev)
     _fit(scores, torch.float32, dev, (pages, H, page), "scores")
-    if workspace is None:
-        with _on(stream):
-            workspace = torch.empty(_paged_workspace("mass", dev, T, n, Hq, H, D, most, page), dtype=torch.uint8,
-                                    device=q.device)
-    else:
-        _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
-    st = load().kvpop_paged_mass(_p(q), _p(lse), T, n, Hq, H, D, scale, decay, _p(cu), _p(lens), _p(table), most, _p(kp), pk,
-                                 pages, page, _p(scores), _p(workspace), workspace.numel(), _stream(stream))
+    s = _stream(stream)
+    with _paged_scratch("mass", workspace, dev, T, n, Hq, H, D, most, page, s) as (ws, nb):
+        st = load().kvpop_paged_mass(_p(q), _p(lse), T, n, Hq, H, D, scale, decay, _p(cu), _p(lens), _p(table), most, _p(kp),
+                                     pk, pages, page, _p(scores), ws, nb, s)
     if st:
         _check(st, "kvpop_paged_mass")
     return scores
