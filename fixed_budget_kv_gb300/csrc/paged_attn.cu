@@ -9,8 +9,8 @@
 // boxes of a page, or of 128 slots of one.  Decode rows are bound by memory (one flop a byte a
 // row), chunks by the tensor core and the softmax.
 //
-// Work split: an item is one (sequence, row block, KV head), in that order, and has kSetup
-// units of setup and then a unit for each tile.  CTA c takes the c-th part of all units, one
+// Work split: an item is one (sequence, row block, KV head), in that order, and has units of
+// setup and then for each tile, by what these take.  CTA c takes the c-th part of all units, one
 // CTA an SM, however ragged the chunks and lengths, which only the device knows.  A CTA's tiles
 // fall into segments of one item each, of at most kRunTiles, whose running maximum, sum and
 // unnormalised O are added up in a slot of the workspace.  An item whose tiles are all a CTA's
@@ -33,6 +33,13 @@
 // core wants the type of V: each weight by up to 2^-8 of itself, independently, which leaves O
 // off by about 1.3e-3 of its size beside the 1.7e-3 of its own rounding.  The row sum is not
 // rounded.
+//
+// Measured (8 KV heads, G = 4, D = 128, one GB300, calls in a chain): one row each of 64 sequences
+// of 500 .. 16 001 slots 185 us, 96% of the copy rate; 4096 tokens at the end of 32 768 slots
+// 1.46 ms, 1417 TFLOP/s (74% of the burst rate), bound by the issue of products (1.26 ms without
+// the softmax) and the hand-overs S -> softmax -> P V; a step of 12 sequences, two long chunks
+// among ten short ones and decode rows, 181 us, 1070 TFLOP/s (the chunks' rate, 15 us of merge,
+// start and switches).
 #include <string.h>
 
 #include <atomic>

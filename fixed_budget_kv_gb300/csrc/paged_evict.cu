@@ -13,6 +13,10 @@
 // heads, moves K (with the scores) or V of a head in rising order, a batch of rows at a time: loads,
 // barrier, stores.  The next batch's sources lie at or above its own slots, so behind everything stored
 // before: nothing is lost and no second copy is needed.  Bound by memory.
+//
+// Measured (8 KV heads, D = 128, one GB300): 64 sequences of 1700 .. 4099 slots to 2048, 845 MB: select
+// 19 us, move 134 us (5.8 TB/s), in a chain of calls 181 us; one of 131 072 slots to 4096: 18 us
+// (the barriers of eight clusters) and 7-16 us (rows in and out of 128 SMs), in a chain 32 us.
 #include <atomic>
 
 #include "paged.cuh"
@@ -27,7 +31,9 @@ constexpr int kSet = 2048, kTied = 8192;
 constexpr int kCacheBytes = 163840;  // for the keys of a CTA's part, at most
 constexpr int kMaxCluster = 8;
 constexpr int kMoveBatch = 8;  // pieces that a thread has in flight
-constexpr int kMoveFew = 1024, kMoveMany = 256;  // threads of a CTA with few heads and with many
+// Threads of a CTA with few heads and with many (64 sequences to 2048 slots, a first pass on cold
+// caches: 128 threads 216 us, 256 199, 512 185, 1024 198).
+constexpr int kMoveFew = 1024, kMoveMany = 512;
 
 struct EvictParams {
   Paged c;
