@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
       if (p.c.n > 32 && u < end) {  // back to the window in which the share begins
         int at = 0;
 #pragma unroll 1
-        for (int w0 = 0;; w0 += 32) {
+        for (int w0 = 0; w0 < p.c.n; w0 += 32) {
           at = window(w0, at);
           if (u < at) break;
         }
@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             // the sequence: the one of the window whose units these are
             const unsigned hit = __ballot_sync(0xffffffffu, g.units > 0 && base <= u && u < base + g.units);
             if (hit == 0) {
-              window(j0 + 32, u);  // u is the window's end
+              if (j0 + 32 < p.c.n) window(j0 + 32, u);  // u is the window's end
+              else end = u;  // only where lens or cu change under the call
               continue;
             }
             const int l = __ffs(hit) - 1, b = __shfl_sync(0xffffffffu, base, l);

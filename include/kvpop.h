@@ -460,6 +460,8 @@ kvpop_status kvpop_prefix_attn(const void* q, const void* pk, const void* pv, in
  * call's _workspace_size() bytes, 256-byte aligned; contents undefined between calls, so calls
  * that overlap in time need one each.  Sequences that overlap to more than T rows in all
  * record KVPOP_ERR_INVALID_ARG in the status words, and nothing is computed.
+ * What a call writes overlaps nothing else that it reads (new_lens may be lens), and lens, cu
+ * and table stay as they are until it has run.
  * Errors of all: INVALID_ARG, UNSUPPORTED (sizes, alignment), CUDA.
  * ---------------------------------------------------------------------- */
 kvpop_status kvpop_paged_append(const void* k_new, int64_t k_new_stride, const void* v_new, int64_t v_new_stride, int T,

@@ -683,6 +683,21 @@ def test_against_the_contiguous_calls(D, G, S, page):
         assert float((got - target[0, h]).abs().max()) <= 2e-2
 
 
+@pytest.mark.parametrize("chunk,last", [(100, 10), (300, 32), (40, 1), (513, 300)])
+def test_observation_window(chunk, last):
+    """The attention of whole chunks, and the weight that only their last rows give."""
+    lens = [chunk + 333, chunk, 700 + chunk]
+    c = Held(lens, 2, 32, 128, seed=chunk)
+    cu = sums([chunk] * 3)
+    q = c.randn(3 * chunk, 8, 128)
+    O, lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32(cu))
+    check_attn(O, lse, q, c, cu)
+    rows = torch.cat([torch.arange(x - last, x) for x in cu[1:]]).cuda()
+    before = c.scores.clone()
+    got = kvpop.paged_mass(q[rows], lse[rows], c.kp, c.scores, c.table, c.lens, i32(sums([last] * 3)), decay=0.5)
+    check_mass(got, before, q[rows], lse[rows], c, sums([last] * 3), 0.5)
+
+
 def test_two_graphs_in_turn():
     """Two captured steps on the same cache, replayed in turn on two streams' order: each has its
     own workspace, and each replay equals the eager calls."""
