@@ -140,7 +140,7 @@ struct Bars {
   uint64_t k_full[NK], k_empty[NK];
   uint64_t q_full[NQS], q_empty[NQS];
   uint64_t s_full[4], s_empty[4];
-  uint64_t x_full[2];
+  uint64_t x_full[2][2];  // [tile][buffer]
   uint64_t l_full[kLseStages], l_empty[kLseStages];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t drain;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->s_empty[i], 4 * kGroups);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&bars->x_full[i], 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars->x_full[i >> 1][i & 1], 4);
     for (int i = 0; i < kLseStages; ++i) {
       mbar_init(&bars->l_full[i], 1);
       mbar_init(&bars->l_empty[i], 16);
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     const uint64_t s2 = pack2(p.scale_log2, p.scale_log2);
     float total = 0.0f;
     uint32_t ns = 0;  // parity of this tile's next product
-    uint32_t nx = 0;  // items finished
+    uint32_t nx = 0;  // sums joined
     Ring<kLseStages> r;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -649,16 +649,17 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
         r.skip(1);
       }
       if (!ok) break;
-      if (WIDE && s.ends()) {
-        // the second warpgroup's sums join the first's.  Two buffers: it is never two items ahead, as
-        // TMEM is handed back by both
+      if (WIDE && s.ends() && seen) {
+        // The second warpgroup's sums join the first's, unless no row has seen the tile: both are 0
+        // then.  Of the tiles that were seen it is at most one ahead, as TMEM is handed back by both:
+        // two buffers, each with a barrier of its own
         float* x_s = reinterpret_cast<float*>(smem + L::x_off) + (nx & 1) * kBlockKeys;
         if (half == 1) {
           x_s[row] = total;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->x_full[rt]);
+          if (lane == 0) mbar_arrive(&bars->x_full[rt][nx & 1]);
         } else {
-          if (!(ok = wait_bar(&bars->x_full[rt], nx & 1, SITE_PAGED_SOFTMAX, 3))) break;
+          if (!(ok = wait_bar(&bars->x_full[rt][nx & 1], nx >> 1 & 1, SITE_PAGED_SOFTMAX, 3))) break;
           total += x_s[row];
         }
         ++nx;

@@ -698,6 +698,21 @@ def test_observation_window(chunk, last):
     check_mass(got, before, q[rows], lse[rows], c, sums([last] * 3), 0.5)
 
 
+@pytest.mark.parametrize("chunk,length", [(64, 90), (64, 300), (70, 130), (129, 700)])
+def test_short_items_in_turn(chunk, length):
+    """Many items of one or a few tiles of rows for every SM, with tiles of keys that no row sees."""
+    n = 150
+    c = Held([length + i % 3 for i in range(n)], 4, 32, 64, seed=length)
+    q, cu = c.randn(n * chunk, 16, 64), sums([chunk] * n)
+    O, lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32(cu))
+    check_attn(O, lse, q, c, cu)
+    before = c.scores.clone()
+    got = kvpop.paged_mass(q, lse, c.kp, c.scores, c.table, c.lens, i32(cu))
+    check_mass(got, before, q, lse, c, cu, 1.0)
+    for _ in range(20):
+        assert torch.equal(kvpop.paged_mass(q, lse, c.kp, before.clone(), c.table, c.lens, i32(cu)), got)
+
+
 def test_two_graphs_in_turn():
     """Two captured steps on the same cache, replayed in turn on two streams' order: each has its
     own workspace, and each replay equals the eager calls."""
