@@ -594,13 +594,26 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           tc_fence_after();
           uint64_t acc0 = 0, acc1 = 0;  // packed fp32 pairs
           uint32_t ra[32], rb[32];
+          auto add_chunk = [&](const uint32_t(&x)[32], const float* lse2) {
+#pragma unroll
+            for (int cc = 0; cc < 32; cc += 4) {
+              const float4 lv = *reinterpret_cast<const float4*>(lse2 + cc);
+              const uint64_t x0 = fma2(pack2(__uint_as_float(x[cc]), __uint_as_float(x[cc + 1])), s2, pack2(lv.x, lv.y));
+              const uint64_t x1 = fma2(pack2(__uint_as_float(x[cc + 2]), __uint_as_float(x[cc + 3])), s2, pack2(lv.z, lv.w));
+              float e0, e1, e2, e3;
+              unpack2(x0, e0, e1);
+              unpack2(x1, e2, e3);
+              acc0 = add2(acc0, pack2(ex2_approx(e0), ex2_approx(e1)));
+              acc1 = add2(acc1, pack2(ex2_approx(e2), ex2_approx(e3)));
+            }
+          };
           auto hand_back = [&]() {  // all of the tile's columns are in registers
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->s_empty[rt]);
           };
-          tmem_ld32(tl, ra);
           if (!masked) {
+            tmem_ld32(tl, ra);
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
               uint32_t(&x)[32] = (ch & 1) ? rb : ra;
@@ -608,37 +621,35 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
               tmem_wait_ld_dep(x);
               if (ch < 3) tmem_ld32(tl + (ch + 1) * 32, nxt);
               else hand_back();
-#pragma unroll
-              for (int cc = 0; cc < 32; cc += 4) {
-                const float4 lv = *reinterpret_cast<const float4*>(l2 + ch * 32 + cc);
-                const uint64_t x0 = fma2(pack2(__uint_as_float(x[cc]), __uint_as_float(x[cc + 1])), s2, pack2(lv.x, lv.y));
-                const uint64_t x1 = fma2(pack2(__uint_as_float(x[cc + 2]), __uint_as_float(x[cc + 3])), s2, pack2(lv.z, lv.w));
-                float e0, e1, e2, e3;
-                unpack2(x0, e0, e1);
-                unpack2(x1, e2, e3);
-                acc0 = add2(acc0, pack2(ex2_approx(e0), ex2_approx(e1)));
-                acc1 = add2(acc1, pack2(ex2_approx(e2), ex2_approx(e3)));
-              }
+              add_chunk(x, l2 + ch * 32);
             }
           } else {
-            // columns below lo are of tokens before the key's own
+            // Columns below lo are of tokens before the key's own, from cols on of other sequences
             const int cols = s.columns(c, p.log_p, p.log_g) - 128 * half;
             const int lo = (max(0, t - a - (c << p.log_p)) << p.log_g) - 128 * half;
-            const int chunks = min(4, max(1, (cols + 31) >> 5));
-            float m = 0.0f;
+            const int lo_any = __shfl_sync(0xffffffffu, lo, 0), lo_all = __shfl_sync(0xffffffffu, lo, 31);
+            const int ch1 = min(4, (cols + 31) >> 5);
+            const bool foreign = c >= part || none_s[r.st];
+            int ch = max(0, lo_any >> 5);
+            if (ch < ch1) tmem_ld32(tl + ch * 32, ra);
+            else hand_back();
 #pragma unroll 1
-            for (int ch = 0; ch < chunks; ++ch) {
+            for (; ch < ch1; ++ch) {
               tmem_wait_ld_dep(ra);
-              if (ch + 1 == chunks) hand_back();
+              if (ch + 1 == ch1) hand_back();
+              if (ch * 32 < lo_all) {
+                const int below = lo - ch * 32;
 #pragma unroll
-              for (int cc = 0; cc < 32; ++cc) {
-                const int col = ch * 32 + cc;
-                const float lv = l2[col], e = fmaf(__uint_as_float(ra[cc]), p.scale_log2, lv);
-                m += col >= lo && col < cols && lv != neg_inf() ? ex2_approx(e) : 0.0f;
+                for (int cc = 0; cc < 32; ++cc) ra[cc] = cc < below ? 0xff800000u : ra[cc];
               }
-              if (ch + 1 < chunks) tmem_ld32(tl + (ch + 1) * 32, ra);
+              if (foreign) {
+                // their -lse is -inf, and a finite product with it adds nothing
+#pragma unroll
+                for (int cc = 0; cc < 32; ++cc) ra[cc] = __float_as_uint(fminf(__uint_as_float(ra[cc]), 3.4e38f));
+              }
+              add_chunk(ra, l2 + ch * 32);
+              if (ch + 1 < ch1) tmem_ld32(tl + (ch + 1) * 32, ra);
             }
-            acc0 = pack2(m, 0.0f);
           }
           float y0, y1;
           unpack2(add2(acc0, acc1), y0, y1);
