@@ -24,13 +24,15 @@
 //   warps 4-19   four warpgroups that sum 128 columns each, one thread a key
 // TMEM columns are handed back as soon as they are in registers, and the tensor core works on the
 // other tiles meanwhile.  A thread sums 128 columns by themselves before it adds them to its total:
-// long chunks would lose digits in one running sum.
+// long chunks would lose digits in one running sum.  A tile with masked columns is taken 32 columns
+// at a time: those before a warp's first key are not read, and what a key does not see becomes -inf
+// before the same sum (512 tokens, G = 8, over 16 384 slots 130 us with a conditional sum, 115 so).
 //
 // Measured (8 KV heads, G = 4, D = 128, one GB300, calls in a chain): one row each of 64 sequences
 // of 500 .. 16 001 slots 104 us, 88% of the copy rate; 32 rows over 131 072 slots 52 us, 78%;
-// 4096 tokens over 32 768 slots 0.73-0.76 ms, 1350-1420 TFLOP/s (70-74% of the burst rate): eight
-// products of 256 columns take 1300 cycles beside the other traffic of shared memory (1024 alone),
-// and the sums 1250 until TMEM is handed back.
+// 4096 tokens over 32 768 slots 0.70 ms, 1470 TFLOP/s (76% of the burst rate): eight products of 256
+// columns take 1300 cycles beside the other traffic of shared memory (1024 alone), and the sums as
+// long.  Without the exponentials 0.62 ms, without the loads of lse either 0.56.
 #include <string.h>
 
 #include <atomic>
@@ -46,7 +48,7 @@ constexpr int kKeys = 128;
 // Two forms of the kernel.  Narrow: a block of four tiles of K against query tiles of up to 128
 // columns, one summing warpgroup a tile.  Wide: two tiles against 256 columns, two warpgroups a tile.
 // The issuing thread takes about 85 cycles for a product's instruction and 300 between two tiles, the
-// tensor core 65 for 128 columns and 130 for 256: wide keeps it busy (4096 rows over 32 768 slots
+// tensor core 65 for 128 columns and 130 for 256: wide keeps it busy (4096 tokens over 32 768 slots
 // 742 us against 800), narrow has twice the keys on their way from memory (decode rows).
 template <bool WIDE>
 struct Form {
@@ -79,6 +81,7 @@ struct MassParams {
   int Hq, G, log_g, log_p;  // query tiles of 2^log_p tokens
   int q_bytes;              // of a query tile's box and 64 columns
   int block_keys;
+  int own_tiles;  // query tiles as long as a block of slots; 0 in the narrow form
   float scale_log2, decay;
 };
 
@@ -89,6 +92,12 @@ struct Seq {
 };
 // The first query tile that sees slot t.
 __device__ __forceinline__ int first_tile(int a, int log_p, int t) { return max(0, t - a) >> log_p; }
+// Units of setup of block b of slots.  A block with the chunk's own slots has masked query tiles, which
+// take half as long again or more in the wide form (2048 tokens, G = 16, over 8192 slots 207 us without
+// this, 176 with, 180 with a whole tile each; the narrow form loses by any).
+__device__ __forceinline__ int setup_units(const MassParams& p, const Seq& s, int b) {
+  return kSetup + ((b + 1) * p.block_keys > s.len - s.c ? min(p.own_tiles, s.nq) / 2 : 0);
+}
 // Units of blocks 0 .. m - 1 for one head.
 __device__ __forceinline__ int units_before(const MassParams& p, const Seq& s, int m) {
   const int a = s.len - s.c;
@@ -97,7 +106,9 @@ __device__ __forceinline__ int units_before(const MassParams& p, const Seq& s, i
   const int b0 = a > 0 ? (a + p.block_keys - 1) / p.block_keys : 0;
   const int n = max(0, m - b0);
   const long long f0 = first_tile(a, p.log_p, b0 * p.block_keys);
-  return (int)((long long)m * (s.nq + kSetup) - (n * f0 + (long long)n * (n - 1) / 2 * (p.block_keys >> p.log_p)));
+  const int own = max(0, m - max(0, a) / p.block_keys);  // blocks with slots of the chunk
+  return (int)((long long)m * (s.nq + kSetup) - (n * f0 + (long long)n * (n - 1) / 2 * (p.block_keys >> p.log_p)) +
+               (long long)own * (setup_units(p, s, s.nb) - kSetup));
 }
 __device__ __forceinline__ Seq sequence(const MassParams& p, int i) {
   Seq s;
@@ -449,10 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       // the sequence, block of slots and head of the item that holds unit u, the block's units for
       // one head, and the first of the item's; looked up once and counted on
       Seq q = {};
-      int seq = 0, kb = 0, h = 0, per = 0, at = 0, pg = 0, seg_pg = 0;
+      int seq = 0, kb = 0, h = 0, per = 0, at = 0, setup = 0, pg = 0, seg_pg = 0;
       bool known = false;
       auto enter_block = [&]() {  // lane l reads a table entry of the block, for all of its heads
-        per = q.nq - first_tile(q.len - q.c, p.log_p, kb * kBlockKeys) + kSetup;
+        per = q.nq - first_tile(q.len - q.c, p.log_p, kb * kBlockKeys) + (setup = setup_units(p, q, kb));
         const int slot = kb * kBlockKeys + lane / kBoxes * kKeys + (lane % kBoxes << log_box);
         pg = p.c.pages;
         if (lane / kBoxes < kTiles && lane % kBoxes < kKeys >> log_box && slot < q.len) {
@@ -504,15 +515,15 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           const int a = q.len - q.c, q_lo = first_tile(a, p.log_p, s.slot0), off = u - at;
           // this CTA's units of the item from here on, as long as the same tiles are seen, up to a run
           // of query tiles: [off, stop)
-          const int t0 = max(off - kSetup, 0);
-          int stop = min(min(per, off + (end - u)), max(off, kSetup) + kRunTiles);
+          const int t0 = max(off - setup, 0);
+          int stop = min(min(per, off + (end - u)), max(off, setup) + kRunTiles);
           s.tiles = 0;
           for (int rt = 0; rt < kTiles && s.slot0 + rt * kKeys < s.len; ++rt) {
             const int f = first_tile(a, p.log_p, s.slot0 + rt * kKeys) - q_lo;
             if (f <= t0) ++s.tiles;
-            else stop = min(stop, f + kSetup);
+            else stop = min(stop, f + setup);
           }
-          const int t1 = max(stop - kSetup, 0);
+          const int t1 = max(stop - setup, 0);
           s.q0 = q_lo + t0;
           s.NQ = t1 - t0;
           seg_pg = pg;
@@ -523,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                     (own ? 8 : 0);
           if (n == 0 && t0 > 0) {
             // the work begins inside an item; the second of its CTAs leaves word of it
-            const int first = at + kSetup;
+            const int first = at + setup;
             split = {seq, sh.cta_of(first) + 1 == (int)blockIdx.x ? h : -1, kb, sh.cta_of(at + per - 1)};
           }
           u += stop - off;
@@ -791,8 +802,11 @@ extern "C" kvpop_status kvpop_paged_mass(const void* q, const float* lse, int T,
     return KVPOP_ERR_UNSUPPORTED;
   }
   const int G = Hq / H, box = min(page, kKeys);
-  // wide from 256 rows a sequence and head on (their mean: only the device knows each)
-  const bool wide = (long long)T * G >= 256ll * n;
+  // Wide from 512 rows a sequence and head on, and 32 G tokens (their mean: only the device knows each).
+  // Wide against narrow, one sequence, D = 128, us: over 16 384 slots of 8 heads 64 tokens of G = 4 17.5
+  // against 19, 96 27 against 23, 128 25 against 27, 1024 99 against 113; over 8192 slots of 4 heads G = 16
+  // 256 tokens 46 against 39, 512 61 against 64, 2048 176 against 194.
+  const bool wide = (long long)T * G >= 512ll * n && T >= 32ll * G * n;
   const int cols = wide ? Form<true>::kCols : Form<false>::kCols;
   // a decode step's rows lie alone: their boxes take no other sequence's along
   const int tokens = cu ? cols / G : 1;
@@ -815,6 +829,7 @@ extern "C" kvpop_status kvpop_paged_mass(const void* q, const float* lse, int T,
   while ((1 << prm.log_g) < G) ++prm.log_g;
   prm.log_p = (wide ? 8 : 7) - prm.log_g;
   prm.block_keys = wide ? Form<true>::kBlockKeys : Form<false>::kBlockKeys;
+  prm.own_tiles = wide ? prm.block_keys >> prm.log_p : 0;
   prm.q_bytes = tokens * G * 128;
   prm.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
   prm.decay = decay;

@@ -110,6 +110,10 @@ CASES = [
     ([1], [20000], 8, 4, 128, 64),                              # one row over all SMs
     ([1] * 9, [1 + 900 * i for i in range(9)], 8, 8, 128, 64),
     ([700], [5000], 8, 4, 128, 64),
+    ([600, 3, 0, 200], [900, 700, 40, 200], 2, 4, 128, 32),     # a long chunk beside others, for 512 rows a sequence
+    ([530], [777], 2, 1, 128, 16),
+    ([521], [2000], 1, 16, 64, 256),                            # sixteen tokens a row tile
+    ([1030, 1100], [1030, 3001], 2, 1, 64, 64),
 ]
 
 
@@ -698,7 +702,7 @@ def test_observation_window(chunk, last):
     check_mass(got, before, q[rows], lse[rows], c, sums([last] * 3), 0.5)
 
 
-@pytest.mark.parametrize("chunk,length", [(64, 90), (64, 300), (70, 130), (129, 700)])
+@pytest.mark.parametrize("chunk,length", [(64, 90), (64, 300), (70, 130), (128, 140), (129, 280), (129, 700)])
 def test_short_items_in_turn(chunk, length):
     """Many items of one or a few tiles of rows for every SM, with tiles of keys that no row sees."""
     n = 150
