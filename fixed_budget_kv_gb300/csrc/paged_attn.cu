@@ -654,12 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
           // them is larger, which is what moves it.  So most tiles need no maximum (a chunk of 4096 tokens
           // over 32 768 slots 1.46 ms against 1.54); the others are done again from the registers.
           float lt = 0.0f;
-          bool redo = true;
-          if (__all_sync(0xffffffffu, m_ref != neg_inf())) {
-            lt = weights();
-            redo = __any_sync(0xffffffffu, lt > 256.0f);
-          }
-          if (redo) {
+          bool known = __all_sync(0xffffffffu, m_ref != neg_inf()), last = false;
+#pragma unroll 1
+          while (true) {
+            if (known) {
+              lt = weights();
+              if (last || !__any_sync(0xffffffffu, lt > 256.0f)) break;
+            }
             float mt = neg_inf();
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) mt = fmaxf(mt, max32(sr[ch]));
@@ -683,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
                 tmem_st32(tl + o_col + cd * 32, r);
               }
             }
-            lt = weights();
+            known = last = true;
           }
           l += lt;
           tmem_wait_st();
