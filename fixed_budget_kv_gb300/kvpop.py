@@ -184,23 +184,6 @@ def _on(stream):
     return _here if stream is None else torch.cuda.stream(stream)
 
 
-class _Scratch:
-    """A workspace for one call, from torch's allocator and back to it in the order of the stream: the
-    first tensor that a call makes next to a launch costs the host 5 us, plain memory half a one."""
-
-    __slots__ = ("nbytes", "handle", "ptr")
-
-    def __init__(self, nbytes, handle):
-        self.nbytes, self.handle = nbytes, handle
-
-    def __enter__(self):
-        self.ptr = torch._C._cuda_cudaCachingAllocator_raw_alloc(self.nbytes, self.handle)
-        return self.ptr, self.nbytes
-
-    def __exit__(self, *_):
-        torch._C._cuda_cudaCachingAllocator_raw_delete(self.ptr)
-
-
 def device_status(reset: bool = True):
     out = (c_i32 * 4)()
     st = load().kvpop_device_status(ctypes.cast(out, c_void_p), int(reset))
@@ -638,11 +621,19 @@ def _paged_workspace(what, dev, T, n, Hq, H, D, most, page) -> int:
 
 
 def _paged_scratch(what, workspace, dev, T, n, Hq, H, D, most, page, handle):
-    """Address and bytes of the caller's workspace, or of one for this call."""
+    """Address and bytes of the caller's workspace, or of one for this call, which goes back by
+    _scratch_back: plain memory of torch's allocator, taken and given in the order of the stream (the
+    first tensor that a call makes next to a launch costs the host 5 us, plain memory half a one)."""
     if workspace is None:
-        return _Scratch(_paged_workspace(what, dev, T, n, Hq, H, D, most, page), handle)
+        nb = _paged_workspace(what, dev, T, n, Hq, H, D, most, page)
+        return torch._C._cuda_cudaCachingAllocator_raw_alloc(nb, handle), nb
     _fit(workspace, torch.uint8, dev, workspace.shape, "workspace")
-    return contextlib.nullcontext((workspace.data_ptr(), workspace.numel()))
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _scratch_back(workspace, ws):
+    if workspace is None:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
 
 
 def paged_attn_workspace_size(T, n, Hq, H, D, max_pages, page) -> int:
@@ -665,17 +656,22 @@ def paged_attn(q, kp, vp, table, lens, cu=None, scale: float = 0.0, workspace=No
     dev = _device(q, "q")
     _fit(q, torch.bfloat16, dev, rows, "q")
     pages, H, page, pk, pv, n, most = _paged_args(kp, vp, table, lens, cu, T, D, dev)
-    if out is None:
-        with _on(stream):
-            O, lse = _empty_as(q), torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    else:
+    if out is not None:
         O, lse = out
         _fit(O, torch.bfloat16, dev, rows, "O")
         _fit(lse, torch.float32, dev, (T, Hq), "lse")
+    elif stream is None:
+        O, lse = torch.empty_like(q), torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    else:
+        with _on(stream):
+            O, lse = torch.empty_like(q), torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     s = _stream(stream)
-    with _paged_scratch("attn", workspace, dev, T, n, Hq, H, D, most, page, s) as (ws, nb):
+    ws, nb = _paged_scratch("attn", workspace, dev, T, n, Hq, H, D, most, page, s)
+    try:
         st = load().kvpop_paged_attn(_p(q), T, n, Hq, H, D, scale, _p(cu), _p(lens), _p(table), most, _p(kp), pk, _p(vp), pv,
                                      pages, page, _p(O), _p(lse), ws, nb, s)
+    finally:
+        _scratch_back(workspace, ws)
     if st:
         _check(st, "kvpop_paged_attn")
     return O, lse
@@ -695,9 +691,12 @@ def paged_mass(q, lse, kp, scores, table, lens, cu=None, scale: float = 0.0, dec
     pages, H, page, pk, _, n, most = _paged_args(kp, None, table, lens, cu, T, D, dev)
     _fit(scores, torch.float32, dev, (pages, H, page), "scores")
     s = _stream(stream)
-    with _paged_scratch("mass", workspace, dev, T, n, Hq, H, D, most, page, s) as (ws, nb):
+    ws, nb = _paged_scratch("mass", workspace, dev, T, n, Hq, H, D, most, page, s)
+    try:
         st = load().kvpop_paged_mass(_p(q), _p(lse), T, n, Hq, H, D, scale, decay, _p(cu), _p(lens), _p(table), most, _p(kp),
                                      pk, pages, page, _p(scores), ws, nb, s)
+    finally:
+        _scratch_back(workspace, ws)
     if st:
         _check(st, "kvpop_paged_mass")
     return scores
