@@ -36,7 +36,7 @@
 //
 // Measured (8 KV heads, G = 4, D = 128, one GB300, calls in a chain): one row each of 64 sequences
 // of 500 .. 16 001 slots 185 us, 96% of the copy rate; 4096 tokens at the end of 32 768 slots
-// 1.46 ms, 1417 TFLOP/s (74% of the burst rate), bound by the issue of products (1.26 ms without
+// 1.43-1.46 ms, 1410-1440 TFLOP/s (74% of the burst rate), bound by the issue of products (1.26 ms without
 // the softmax) and the hand-overs S -> softmax -> P V; a step of 12 sequences, two long chunks
 // among ten short ones and decode rows, 181 us, 1070 TFLOP/s (the chunks' rate, 15 us of merge,
 // start and switches).
