@@ -83,6 +83,7 @@ struct MassParams {
   int block_keys;
   int own_tiles;  // query tiles as long as a block of slots; 0 in the narrow form
   float scale_log2, decay;
+  float limit;  // a product up to it stays finite when it is scaled
 };
 
 // A sequence: rows [lo, lo + c), slots, blocks of slots, query tiles and units.  A sequence without
@@ -654,9 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 for (int cc = 0; cc < 32; ++cc) ra[cc] = cc < below ? 0xff800000u : ra[cc];
               }
               if (foreign) {
-                // their -lse is -inf, and a finite product with it adds nothing
+                // their -lse is -inf, and a finite product with it adds nothing; a NaN becomes the limit
 #pragma unroll
-                for (int cc = 0; cc < 32; ++cc) ra[cc] = __float_as_uint(fminf(__uint_as_float(ra[cc]), 3.4e38f));
+                for (int cc = 0; cc < 32; ++cc) ra[cc] = __float_as_uint(fminf(__uint_as_float(ra[cc]), p.limit));
               }
               add_chunk(ra, l2 + ch * 32);
               if (ch + 1 < ch1) tmem_ld32(tl + (ch + 1) * 32, ra);
@@ -832,6 +833,7 @@ extern "C" kvpop_status kvpop_paged_mass(const void* q, const float* lse, int T,
   prm.own_tiles = wide ? prm.block_keys >> prm.log_p : 0;
   prm.q_bytes = tokens * G * 128;
   prm.scale_log2 = (scale > 0.0f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+  prm.limit = 1e38f / fmaxf(1.0f, prm.scale_log2);
   prm.decay = decay;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (D == 128) return wide ? launch<128, true>(prm, ctas, cs) : launch<128, false>(prm, ctas, cs);

@@ -269,6 +269,26 @@ def test_places_behind_a_length_are_never_used(bad, chunks):
     assert torch.equal(kvpop.paged_mass(q, want[1], c.kp, s0, c.table, c.lens, i32(cu)), m0)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3.0e38])
+@pytest.mark.parametrize("scale", [0.0, 3.0])
+@pytest.mark.parametrize("chunks", [[3, 1], [40, 29], [133, 150]], ids=str)
+def test_rows_of_others_add_nothing(bad, scale, chunks):
+    """Rows behind the sequences, which share tiles with theirs, and rows that saw nothing hold
+    anything, at scales that would take a large product to infinity."""
+    c = Held([300, 280], 2, 32, 64, seed=9)
+    T, cu = sum(chunks), sums(chunks)
+    q = 0.1 * c.randn(T + 40, 8, 64)
+    lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32(cu), scale=scale)[1]
+    lse[T:] = 0.0
+    lse[1, 2] = -math.inf
+    before = c.scores.clone()
+    want = kvpop.paged_mass(q, lse, c.kp, c.scores.clone(), c.table, c.lens, i32(cu), scale=scale)
+    check_mass(want, before, q, lse, c, cu, 1.0, scale)
+    q[T:], lse[T:] = bad, bad
+    q[1, 2] = bad
+    assert torch.equal(kvpop.paged_mass(q, lse, c.kp, c.scores, c.table, c.lens, i32(cu), scale=scale), want)
+
+
 def test_rows_outside_the_sequences():
     c = Held([300, 200], 2, 32, 64, seed=3)
     q, cu = c.randn(20, 4, 64), [3, 9, 15]
