@@ -2,9 +2,9 @@
 // rows: scores_t = decay scores_t + sum over rows r >= t - (len - c), heads g < G of
 // exp(scale q_{r,hG+g} . k_t - lse_{r,hG+g}).
 //
-// The transposed product S' = K Q^T has a key in each TMEM lane, so that a thread sums its own
-// key's row and nothing is exchanged; every term is a probability, so a plain fp32 sum needs no
-// running maximum.  A CTA holds a block of a head's slots, four 128-slot tiles of K (narrow) or two
+// The transposed product S' = K Q^T has a key in each TMEM lane, so that a warp sums its own keys'
+// rows and exchanges nothing but four threads' parts at an item's end; every term is a probability,
+// so a plain fp32 sum needs no running maximum.  A CTA holds a block of a head's slots, four 128-slot tiles of K (narrow) or two
 // (wide), while query tiles of 128 (256) columns, tokens by the G heads, stream past.  Chunks are
 // bound by the tensor core beside one exponential a (row, slot); decode rows and observation
 // windows by reading K.
@@ -21,18 +21,18 @@
 //   warp 2       query tiles and their -lse, in log2 units
 //   warp 3       the CTA's share of the units and its table entries, handed to the others
 //                segment by segment
-//   warps 4-19   four warpgroups that sum 128 columns each, one thread a key
+//   warps 4-19   four warpgroups that sum 128 columns each
 // TMEM columns are handed back as soon as they are in registers, and the tensor core works on the
-// other tiles meanwhile.  A thread sums 128 columns by themselves before it adds them to its total:
+// other tiles meanwhile.  A thread sums a tile's columns by themselves before it adds them to its total:
 // long chunks would lose digits in one running sum.  A tile with masked columns is taken 32 columns
 // at a time: those before a warp's first key are not read, and what a key does not see becomes -inf
 // before the same sum (512 tokens, G = 8, over 16 384 slots 130 us with a conditional sum, 115 so).
 //
 // Measured (8 KV heads, G = 4, D = 128, one GB300, calls in a chain): one row each of 64 sequences
 // of 500 .. 16 001 slots 104 us, 88% of the copy rate; 32 rows over 131 072 slots 52 us, 78%;
-// 4096 tokens over 32 768 slots 0.70 ms, 1470 TFLOP/s (76% of the burst rate): eight products of 256
-// columns take 1300 cycles beside the other traffic of shared memory (1024 alone), and the sums as
-// long.  Without the exponentials 0.62 ms, without the loads of lse either 0.56.
+// 4096 tokens over 32 768 slots 0.65-0.68 ms, 1520-1580 TFLOP/s (79-82% of the burst rate), bound by
+// the products beside the exponentials (a step before, at 0.69: 0.62 without the exponentials, 0.56
+// without the loads of lse either).
 #include <string.h>
 
 #include <atomic>
@@ -178,6 +178,22 @@ struct Layout : Form<WIDE> {
   static constexpr int total = misc_off + 8 + 4 * kLseStages;
   static_assert(total <= 232448, "shared memory of one CTA");
 };
+
+// 32 columns of a warp's 32 TMEM lanes.  Registers keys_reg(k, j) and the next hold lane id / 4 + 8 k,
+// columns 8 j + 2 (id mod 4) and the next.
+__host__ __device__ constexpr int keys_reg(int k, int j) { return 16 * (k >> 1) + 4 * j + 2 * (k & 1); }
+__device__ __forceinline__ void tmem_ld_keys(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr + (16u << 16)));
+}
 
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant__ MassParams p) {
@@ -566,10 +582,17 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
     // ------------------------------------------------------------ sums
     const int rt = (warp - 4) / (4 * kGroups), half = (warp - 4) / 4 % kGroups;  // tile of the block, columns of it
     const int quarter = warp & 3;
-    const int row = rt * kKeys + quarter * 32 + lane;  // key of the block
+    // Narrow: a thread sums the columns of one key.  Wide: of four of the warp's 32 keys, lane / 4 + 8 k, a
+    // quarter of the columns, two of each eight, so that it needs a quarter of the rows' lse (a load for
+    // a whole warp counts for two or three of shared memory's cycles, beside what the tensor core reads:
+    // 4096 tokens over 32 768 slots 688 us with one key, 652 with four; the narrow form is 2-4% slower with
+    // four).  In the end key lane / 4 + 8 (lane mod 4) is its own.
+    constexpr int kOwn = WIDE ? 4 : 1;
+    const int sub = lane >> 2, pair = 2 * (lane & 3);
+    const int row = rt * kKeys + quarter * 32 + (WIDE ? sub + 4 * pair : lane);  // of the block
     const uint32_t tl = tbase + ((uint32_t)(quarter * 32) << 16) + kCols * rt + 128 * half;
     const uint64_t s2 = pack2(p.scale_log2, p.scale_log2);
-    float total = 0.0f;
+    float totals[kOwn] = {};
     uint32_t ns = 0;  // parity of this tile's next product
     uint32_t nx = 0;  // sums joined
     Ring<kLseStages> r;
@@ -578,7 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
       if (!wait_bar(&bars->seg_full[n % kSegs], (n / kSegs) & 1, SITE_PAGED_SOFTMAX, 9)) break;
       const Seg& s = segs[n % kSegs];
       if (s.NQ == 0) break;
-      if (s.begins()) total = 0.0f;
+      if (s.begins()) {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) totals[k] = 0.0f;
+      }
       const int t = s.slot0 + row, a = s.len - s.c;
       const bool on = t < s.len, finish = on && half == 0 && s.ends() && s.whole();
       // the slot's old score, on its way while the products run
@@ -604,19 +630,32 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           if (!(ok = wait_bar(&bars->s_full[rt], ns, SITE_PAGED_SOFTMAX, 2))) break;
           ns ^= 1;
           tc_fence_after();
-          uint64_t acc0 = 0, acc1 = 0;  // packed fp32 pairs
+          uint64_t acc[WIDE ? 4 : 2] = {};  // packed fp32 pairs
           uint32_t ra[32], rb[32];
+          auto load = [](uint32_t addr, uint32_t(&x)[32]) {
+            if constexpr (WIDE) tmem_ld_keys(addr, x);
+            else tmem_ld32(addr, x);
+          };
+          auto add_pair = [&](uint64_t& to, uint32_t x0, uint32_t x1, float l0, float l1) {
+            float e0, e1;
+            unpack2(fma2(pack2(__uint_as_float(x0), __uint_as_float(x1)), s2, pack2(l0, l1)), e0, e1);
+            to = add2(to, pack2(ex2_approx(e0), ex2_approx(e1)));
+          };
           auto add_chunk = [&](const uint32_t(&x)[32], const float* lse2) {
+            if constexpr (WIDE) {
 #pragma unroll
-            for (int cc = 0; cc < 32; cc += 4) {
-              const float4 lv = *reinterpret_cast<const float4*>(lse2 + cc);
-              const uint64_t x0 = fma2(pack2(__uint_as_float(x[cc]), __uint_as_float(x[cc + 1])), s2, pack2(lv.x, lv.y));
-              const uint64_t x1 = fma2(pack2(__uint_as_float(x[cc + 2]), __uint_as_float(x[cc + 3])), s2, pack2(lv.z, lv.w));
-              float e0, e1, e2, e3;
-              unpack2(x0, e0, e1);
-              unpack2(x1, e2, e3);
-              acc0 = add2(acc0, pack2(ex2_approx(e0), ex2_approx(e1)));
-              acc1 = add2(acc1, pack2(ex2_approx(e2), ex2_approx(e3)));
+              for (int j = 0; j < 4; ++j) {
+                const float2 lv = *reinterpret_cast<const float2*>(lse2 + 8 * j + pair);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) add_pair(acc[k], x[keys_reg(k, j)], x[keys_reg(k, j) + 1], lv.x, lv.y);
+              }
+            } else {
+#pragma unroll
+              for (int cc = 0; cc < 32; cc += 4) {
+                const float4 lv = *reinterpret_cast<const float4*>(lse2 + cc);
+                add_pair(acc[0], x[cc], x[cc + 1], lv.x, lv.y);
+                add_pair(acc[1], x[cc + 2], x[cc + 3], lv.z, lv.w);
+              }
             }
           };
           auto hand_back = [&]() {  // all of the tile's columns are in registers
@@ -625,34 +664,46 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             if (lane == 0) mbar_arrive(&bars->s_empty[rt]);
           };
           if (!masked) {
-            tmem_ld32(tl, ra);
+            load(tl, ra);
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
               uint32_t(&x)[32] = (ch & 1) ? rb : ra;
               uint32_t(&nxt)[32] = (ch & 1) ? ra : rb;
               tmem_wait_ld_dep(x);
-              if (ch < 3) tmem_ld32(tl + (ch + 1) * 32, nxt);
+              if (ch < 3) load(tl + (ch + 1) * 32, nxt);
               else hand_back();
               add_chunk(x, l2 + ch * 32);
             }
           } else {
             // Columns below lo are of tokens before the key's own, from cols on of other sequences
             const int cols = s.columns(c, p.log_p, p.log_g) - 128 * half;
-            const int lo = (max(0, t - a - (c << p.log_p)) << p.log_g) - 128 * half;
-            const int lo_any = __shfl_sync(0xffffffffu, lo, 0), lo_all = __shfl_sync(0xffffffffu, lo, 31);
+            const int first = s.slot0 + rt * kKeys + quarter * 32 - a - (c << p.log_p);
+            auto lo = [&](int key) { return (max(0, first + key) << p.log_g) - 128 * half; };
             const int ch1 = min(4, (cols + 31) >> 5);
             const bool foreign = c >= part || none_s[r.st];
-            int ch = max(0, lo_any >> 5);
-            if (ch < ch1) tmem_ld32(tl + ch * 32, ra);
+            int ch = max(0, lo(0) >> 5);
+            if (ch < ch1) load(tl + ch * 32, ra);
             else hand_back();
 #pragma unroll 1
             for (; ch < ch1; ++ch) {
               tmem_wait_ld_dep(ra);
               if (ch + 1 == ch1) hand_back();
-              if (ch * 32 < lo_all) {
-                const int below = lo - ch * 32;
+              if (ch * 32 < lo(31)) {
+                if constexpr (WIDE) {
 #pragma unroll
-                for (int cc = 0; cc < 32; ++cc) ra[cc] = cc < below ? 0xff800000u : ra[cc];
+                  for (int k = 0; k < 4; ++k) {
+                    const int below = lo(sub + 8 * k) - ch * 32 - pair;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                      for (int e = 0; e < 2; ++e)
+                        ra[keys_reg(k, j) + e] = 8 * j + e < below ? 0xff800000u : ra[keys_reg(k, j) + e];
+                  }
+                } else {
+                  const int below = lo(lane) - ch * 32;
+#pragma unroll
+                  for (int cc = 0; cc < 32; ++cc) ra[cc] = cc < below ? 0xff800000u : ra[cc];
+                }
               }
               if (foreign) {
                 // their -lse is -inf, and a finite product with it adds nothing; a NaN becomes the limit
@@ -660,18 +711,33 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
                 for (int cc = 0; cc < 32; ++cc) ra[cc] = __float_as_uint(fminf(__uint_as_float(ra[cc]), p.limit));
               }
               add_chunk(ra, l2 + ch * 32);
-              if (ch + 1 < ch1) tmem_ld32(tl + (ch + 1) * 32, ra);
+              if (ch + 1 < ch1) load(tl + (ch + 1) * 32, ra);
             }
           }
-          float y0, y1;
-          unpack2(add2(acc0, acc1), y0, y1);
-          total += y0 + y1;
+#pragma unroll
+          for (int k = 0; k < kOwn; ++k) {
+            float y0, y1;
+            unpack2(WIDE ? acc[k] : add2(acc[0], acc[1]), y0, y1);
+            totals[k] += y0 + y1;
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->l_empty[r.st]);
         r.skip(1);
       }
       if (!ok) break;
+      float total = totals[0];
+      if constexpr (WIDE) {
+        if (s.ends()) {  // of the key, from the four threads that have a part of it
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float y = totals[k];
+            y += __shfl_xor_sync(0xffffffffu, y, 1);
+            y += __shfl_xor_sync(0xffffffffu, y, 2);
+            if (pair == 2 * k) total = y;
+          }
+        }
+      }
       if (WIDE && s.ends() && seen) {
         // The second warpgroup's sums join the first's, unless no row has seen the tile: both are 0
         // then.  Of the tiles that were seen it is at most one ahead, as TMEM is handed back by both:
