@@ -30,7 +30,7 @@
 //
 // Measured (8 KV heads, G = 4, D = 128, one GB300, calls in a chain): one row each of 64 sequences
 // of 500 .. 16 001 slots 104 us, 88% of the copy rate; 32 rows over 131 072 slots 52 us, 78%;
-// 4096 tokens over 32 768 slots 0.65-0.68 ms, 1520-1580 TFLOP/s (79-82% of the burst rate), bound by
+// 4096 tokens over 32 768 slots 0.65-0.69 ms, 1490-1580 TFLOP/s (77-82% of the burst rate), bound by
 // the products beside the exponentials (a step before, at 0.69: 0.62 without the exponentials, 0.56
 // without the loads of lse either).
 #include <string.h>
