@@ -660,6 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
             if (known) {
               lt = weights();
               if (last || !__any_sync(0xffffffffu, lt > 256.0f)) break;
+              // these weights are written over: stores to the same columns are in order only behind a wait
+              tmem_wait_st();
             }
             float mt = neg_inf();
 #pragma unroll

@@ -248,6 +248,27 @@ def test_growing_scores():
     check_attn(O, lse, q, c, [0, 3])
 
 
+@pytest.mark.parametrize("chunk", [3, 40, 70, 150])
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_taken_again(D, chunk):
+    """Scores that grow by about three at every tile in some rows of each warp and fall in others: the
+    weights against the old reference are stored, then taken again and stored over, at every tile.  The same
+    bits each time."""
+    n = 1700
+    c = Held([n], 2, 32, D, seed=chunk)
+    u = c.randn(D).float()
+    q = (u * torch.linspace(-1, 1, chunk * 8, device="cuda")[torch.randperm(chunk * 8, generator=c.gen, device="cuda")][:, None])
+    q = q.bfloat16().view(chunk, 8, D)
+    k = u * (torch.linspace(-1, 1, n, device="cuda")[:, None] * 20 * math.sqrt(D) / float(u @ u))
+    for h in range(2):
+        ref.put(c.kp, c.table, 0, h, torch.arange(n).cuda(), (k + 0.1 * c.randn(n, D).float()).bfloat16())
+    O, lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32([0, chunk]))
+    check_attn(O, lse, q, c, [0, chunk])
+    for _ in range(20):
+        again = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, i32([0, chunk]))
+        assert torch.equal(again[0], O) and torch.equal(again[1], lse)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3.0e38])
 @pytest.mark.parametrize("chunks", [[1, 1], [40, 1], [70, 3]], ids=str)
 def test_places_behind_a_length_are_never_used(bad, chunks):
