@@ -195,6 +195,16 @@ __device__ __forceinline__ void tmem_ld_keys(uint32_t taddr, uint32_t (&r)[32]) 
       : "r"(taddr + (16u << 16)));
 }
 
+// ... and 8 columns: registers 2 k and the next hold lane id / 4 + 8 k
+__device__ __forceinline__ void tmem_ld_keys8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr + (16u << 16)));
+}
+
 template <int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant__ MassParams p) {
   using L = Layout<D, WIDE>;
@@ -206,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
   float* lse_s = reinterpret_cast<float*>(smem + L::lse_off);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::misc_off);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc_off + 4);
-  int* none_s = reinterpret_cast<int*>(smem + L::misc_off + 8);  // [stage] whether a row of it has lse = -inf
+  int* none_s = reinterpret_cast<int*>(smem + L::misc_off + 8);  // [stage] bit 0: a row of it has lse = -inf; bit 1: NaN
   const uint32_t sbase = smem_u32(smem);
   const int warp = warp_id(), lane = lane_id();
 
@@ -401,19 +411,21 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
           q.skip(1);
           ++loads;
           float y[kCols / 32];
-          bool none = false;
+          bool none = false, nan = false;
 #pragma unroll
           for (int u = 0; u < kCols / 32; ++u) {
             none |= x[u] == neg_inf();
+            nan |= x[u] != x[u];
             y[u] = x[u] == neg_inf() ? neg_inf() : -x[u] * 1.4426950408889634f;
           }
           if (c + 1 < s.q0 + s.NQ) read(c + 1);
           none = __any_sync(0xffffffffu, none);
+          nan = __any_sync(0xffffffffu, nan);
           if (!(ok = wait_bar(&bars->l_empty[r.st], r.ph ^ 1, SITE_PAGED_PRODUCER, 3))) break;
 #pragma unroll
           for (int u = 0; u < kCols / 32; u += 4)
             reinterpret_cast<float4*>(lse_s)[(r.st * kCols + u * 32) / 4 + lane] = make_float4(y[u], y[u + 1], y[u + 2], y[u + 3]);
-          if (lane == 0) none_s[r.st] = none;
+          if (lane == 0) none_s[r.st] = none | nan << 1;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->l_full[r.st]);
           r.skip(1);
@@ -680,8 +692,33 @@ __global__ void __launch_bounds__(kThreads, 1) mass_kernel(const __grid_constant
             const int first = s.slot0 + rt * kKeys + quarter * 32 - a - (c << p.log_p);
             auto lo = [&](int key) { return (max(0, first + key) << p.log_g) - 128 * half; };
             const int ch1 = min(4, (cols + 31) >> 5);
-            const bool foreign = c >= part || none_s[r.st];
+            const int none = none_s[r.st];
+            const bool foreign = c >= part || none;
             int ch = max(0, lo(0) >> 5);
+            if (none & 2) {
+              // a NaN lse, which the -inf of a product would not hide from the slots behind its row: the lse is
+              // masked too, eight columns at a time in the same order
+#pragma unroll 1
+              for (int at = 0; at < ch1 * 32; at += 8) {
+                uint32_t x[8];
+                if constexpr (WIDE) tmem_ld_keys8(tl + at, x);
+                else tmem_ld8(tl + at, x);
+                tmem_wait_ld_dep8(x);
+#pragma unroll
+                for (int u = 0; u < 8; u += 2) {
+                  const int key = WIDE ? sub + 4 * u : lane, col = at + (WIDE ? pair : u);
+                  float v[2], l[2];
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const bool hidden = col + e < lo(key);
+                    v[e] = hidden ? neg_inf() : fminf(__uint_as_float(x[u + e]), p.limit);
+                    l[e] = hidden ? neg_inf() : l2[col + e];
+                  }
+                  add_pair(acc[WIDE ? u / 2 : u / 2 & 1], __float_as_uint(v[0]), __float_as_uint(v[1]), l[0], l[1]);
+                }
+              }
+              ch = ch1;
+            }
             if (ch < ch1) load(tl + ch * 32, ra);
             else hand_back();
 #pragma unroll 1

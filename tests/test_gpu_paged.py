@@ -360,6 +360,34 @@ def test_rows_that_saw_nothing_add_nothing():
     assert torch.isnan(ref.slots(got, c.table, 0, 0, 100)).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,chunk,rows", [(4, 40, [13]), (4, 40, [35]), (2, 150, [0, 77]), (1, 600, [100, 431]),
+                                          (2, 300, [1, 140, 298]), (8, 400, [65])], ids=str)
+def test_nan_of_a_row_stays_in_the_slots_it_sees(D, G, chunk, rows):
+    """A NaN lse anywhere in a chunk, in both forms: the slots that its row sees are NaN, and those
+    behind it and of other heads have the bits that they have without it."""
+    H, lens = 2, [700, 1030]
+    c = Held(lens, H, 32, D, seed=chunk + D)
+    q, cu = c.randn(2 * chunk, H * G, D), i32([0, chunk, 2 * chunk])
+    lse = kvpop.paged_attn(q, c.kp, c.vp, c.table, c.lens, cu)[1]
+    want = kvpop.paged_mass(q, lse, c.kp, c.scores.clone(), c.table, c.lens, cu)
+    nan_q = q.clone()
+    for r in rows:  # of the second sequence and the first head's last query head
+        nan_q[chunk + r, G - 1, 5] = float("nan")
+    bad = kvpop.paged_attn(nan_q, c.kp, c.vp, c.table, c.lens, cu)[1]
+    assert int(torch.isnan(bad).sum()) == len(rows)
+    got = kvpop.paged_mass(nan_q, bad, c.kp, c.scores.clone(), c.table, c.lens, cu)
+    same = kvpop.paged_mass(q, bad, c.kp, c.scores.clone(), c.table, c.lens, cu)
+    assert torch.equal(torch.isnan(got), torch.isnan(same)) and torch.equal(got.nan_to_num(-1), same.nan_to_num(-1))
+    last = lens[1] - chunk + max(rows)  # the last slot that one of them sees
+    mine, clean = ref.slots(got, c.table, 1, 0, lens[1]), ref.slots(want, c.table, 1, 0, lens[1])
+    assert torch.isnan(mine[:last + 1]).all()
+    assert torch.equal(mine[last + 1:], clean[last + 1:])
+    assert torch.equal(ref.slots(got, c.table, 1, 1, lens[1]), ref.slots(want, c.table, 1, 1, lens[1]))
+    for h in range(H):
+        assert torch.equal(ref.slots(got, c.table, 0, h, lens[0]), ref.slots(want, c.table, 0, h, lens[0]))
+
+
 def test_lengths_and_rows_out_of_range_are_clamped():
     c = Held([150, 96], 1, 32, 64, seed=5)
     c.table[:, 3:] = -1
