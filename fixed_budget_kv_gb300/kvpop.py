@@ -538,7 +538,7 @@ def prefix_attn(q, pk, pv, cu=None, lens=None, join=None, scale: float = 0.0, wo
 def _page_stride(x, dev, name):
     """Elements between the pages of a bf16 [pages, H, page, D] cache whose pages are contiguous."""
     if x.is_contiguous() and x.dtype is torch.bfloat16 and x.get_device() == dev:
-        return x.stride(0)
+        return x.stride(0) if x.shape[0] > 1 else x.numel()  # of one page it means nothing
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if x.dtype is not torch.bfloat16:

@@ -479,6 +479,22 @@ def test_strided_pools():
     assert torch.equal(pool[:, keep], rest[:, keep])
 
 
+def test_one_page_of_any_stride():
+    """A cache of one page, as a view whose stride over pages is a head's."""
+    c = Held([50], 4, 64, 128, seed=15, spare=0)
+    assert c.kp.shape[0] == 1
+    q, k, v, cu = c.randn(7, 8, 128), c.randn(7, 4, 128), c.randn(7, 4, 128), i32([0, 7])
+    odd = [x[0][:, None].clone().transpose(0, 1) for x in (c.kp, c.vp)]
+    assert odd[0].is_contiguous() and odd[0].stride(0) == 64 * 128
+    results = []
+    for kp, vp, scores in ((c.kp, c.vp, c.scores.clone()), (*odd, c.scores.clone())):
+        kvpop.paged_append(k, v, kp, vp, c.table, c.lens, cu, scores=scores)
+        O, lse = kvpop.paged_attn(q, kp, vp, c.table, c.lens, cu)
+        kvpop.paged_mass(q, lse, kp, scores, c.table, c.lens, cu)
+        results.append([O, lse, *kvpop.paged_evict(kp, vp, scores, c.table, c.lens, 2, 9, 20), kp, vp, scores])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 def test_sequences_may_share_pages_they_read():
     lens = [300, 300, 300]
     c = Held([300], 2, 64, 128, seed=7)

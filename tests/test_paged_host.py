@@ -120,6 +120,16 @@ def test_binding_refuses_host_tensors():
         kvpop.paged_evict(kp, kp, kp[..., 0].float(), table, lens, 1, 1, 1)
 
 
+def test_stride_of_one_page():
+    """The stride of a dimension of one means nothing, whatever a view makes of it."""
+    x = torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16)
+    dev = x.get_device()
+    for view in (x.transpose(0, 1), x[:, 0][None], x.as_strided((1, 4, 16, 64), (7, 1024, 64, 1))):
+        assert view.is_contiguous() and kvpop._page_stride(view, dev, "kp") == 4096
+    x = torch.zeros(3, 4, 16, 64, dtype=torch.bfloat16)
+    assert kvpop._page_stride(x, dev, "kp") == 4096
+
+
 def cache(gen, n, H, page, D, lens):
     held = [-(-x // page) for x in lens]
     order = torch.randperm(sum(held) + 1, generator=gen)
