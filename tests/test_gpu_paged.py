@@ -177,6 +177,23 @@ def test_append(case, packed):
         assert torch.equal(c.scores, want[2])
 
 
+@pytest.mark.parametrize("H,D", [(9, 128), (16, 128), (21, 128), (17, 64), (32, 64), (39, 64)])
+def test_append_of_many_heads(H, D):
+    """More heads than a warp takes at a time, and what is left over."""
+    lens, cu = [100, 7, 260], [0, 30, 31, 171]
+    c = Held(lens, H, 32, D, seed=H)
+    qkv = c.randn(171, 3 * H * D)
+    k, v = qkv[:, H * D:2 * H * D].view(171, H, D), qkv[:, 2 * H * D:].view(171, H, D)
+    want = [x.clone() for x in (c.kp, c.vp, c.scores)]
+    for i, n in enumerate(lens):
+        t = torch.arange(n - (cu[i + 1] - cu[i]), n).cuda()
+        for h in range(H):
+            for x, y in zip(want, (k[cu[i]:cu[i + 1], h], v[cu[i]:cu[i + 1], h], 0.0)):
+                ref.put(x, c.table, i, h, t, y)
+    kvpop.paged_append(k, v, c.kp, c.vp, c.table, c.lens, i32(cu), scores=c.scores)
+    assert all(torch.equal(a, b) for a, b in zip((c.kp, c.vp, c.scores), want))
+
+
 EVICT = [
     # lens, H, page, D, (s, w, k)
     ([6], 1, 16, 64, (1, 1, 3)),
@@ -449,6 +466,56 @@ def test_pages_that_do_not_exist_are_reported(bad):
     kept, new = kvpop.paged_evict(c.kp, c.vp, c.scores, table, c.lens, 2, 2, 30)
     assert kvpop.device_status(reset=True)[0] == 1
     assert new.tolist() == [34, 34] and (kept >= 0).all()
+
+
+@pytest.mark.parametrize("lens,gone", [([300, 97], [(0, 0), (0, 5), (1, 1)]), ([300, 97], [(0, 18), (1, 0), (1, 2)]),
+                                       ([9000, 8500], [(0, 0), (0, 100), (0, 101), (0, 300), (1, 531)])], ids=str)
+@pytest.mark.parametrize("bad", [-1, 1 << 30])
+def test_eviction_where_pages_do_not_exist(lens, gone, bad):
+    """Slots of a page that does not exist rank last, behind any score and by their place; nothing moves
+    from or to them.  Sinks, slots between and the window; one CTA a head and a cluster of them."""
+    H, page, s, w, k = 2, 16, 3, 20, 41
+    c = Held(lens, H, page, 64, seed=len(gone) + lens[0])
+    B = s + w + k
+    few = 0.004 if lens[0] > 1000 else 0.1  # fewer slots with a finite score than stay: the ties of the others count
+    c.scores = torch.where(torch.rand(c.scores.shape, generator=c.gen, device="cuda") < few, c.scores.log(), -math.inf)
+    table = c.table.clone()
+    for i, p in gone:
+        table[i, p] = bad
+    want = [x.clone() for x in (c.kp, c.vp, c.scores)]
+    lists = torch.full((2, H, B), -1, dtype=torch.int32)
+    for i, length in enumerate(lens):
+        exists = [(i, t // page) not in gone for t in range(length)]
+        for h in range(H):
+            sc = [x if e else -math.inf for x, e in zip(ref.slots(c.scores, c.table, i, h, length).tolist(), exists)]
+            best = sorted(range(s, length - w), key=lambda t: (-sc[t], t))[:k]
+            stay = list(range(s)) + sorted(best) + list(range(length - w, length))
+            lists[i, h] = torch.tensor(stay, dtype=torch.int32)
+            moves = [(j, t) for j, t in enumerate(stay) if exists[j] and exists[t]]
+            src = torch.tensor([t for _, t in moves], device="cuda")
+            for x, old in zip(want, (c.kp, c.vp, c.scores)):
+                ref.put(x, c.table, i, h, torch.tensor([j for j, _ in moves]).cuda(), ref.slots(old, c.table, i, h, length)[src])
+    kept, new = kvpop.paged_evict(c.kp, c.vp, c.scores, table, c.lens, s, w, k)
+    assert kvpop.device_status(reset=True)[0] == 1
+    assert torch.equal(kept.cpu(), lists) and new.tolist() == [B, B]
+    assert all(torch.equal(a, b) for a, b in zip((c.kp, c.vp, c.scores), want))
+
+
+@pytest.mark.parametrize("width", [1, 40, 600, 8192])
+def test_a_table_wider_than_the_sequences(width):
+    """The same bits from every call whatever the table's width."""
+    lens, cu = [900, 33, 2100, 512] * 9, i32(sums([3, 1, 40, 2] * 9))
+    c = Held(lens, 8, 64, 64, seed=41)
+    tables = [c.table, torch.cat([c.table, torch.full((36, width), 1 << 20, dtype=torch.int32, device="cuda")], 1)]
+    q, k, v = c.randn(46 * 9, 16, 64), c.randn(46 * 9, 8, 64), c.randn(46 * 9, 8, 64)
+    results = []
+    for table in tables:
+        kp, vp, scores = c.kp.clone(), c.vp.clone(), c.scores.clone()
+        kvpop.paged_append(k, v, kp, vp, table, c.lens, cu, scores=scores)
+        O, lse = kvpop.paged_attn(q, kp, vp, table, c.lens, cu)
+        kvpop.paged_mass(q, lse, kp, scores, table, c.lens, cu)
+        results.append([O, lse, kp, vp, scores.clone(), *kvpop.paged_evict(kp, vp, scores, table, c.lens, 4, 60, 200), scores])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
 
 
 def test_strided_pools():
