@@ -518,6 +518,16 @@ def test_a_table_wider_than_the_sequences(width):
     assert all(torch.equal(a, b) for a, b in zip(*results))
 
 
+def test_few_heads_in_a_wide_table():
+    """A cluster for a head that has a few slots."""
+    c = Held([300, 97, 5], 1, 16, 64, seed=43)
+    want = ref.evict(c.kp, c.vp, c.scores, c.table, c.lens_list, 4, 32, 64)
+    table = torch.cat([c.table, torch.full((3, 8192), -5, dtype=torch.int32, device="cuda")], 1)
+    kept, new = kvpop.paged_evict(c.kp, c.vp, c.scores, table, c.lens, 4, 32, 64)
+    assert torch.equal(kept, want[3]) and torch.equal(new, want[4])
+    assert all(torch.equal(a, b) for a, b in zip((c.kp, c.vp, c.scores), want))
+
+
 def test_strided_pools():
     """K and V of several layers in one pool: pages that are apart."""
     lens, chunks = [200, 70, 129], [20, 1, 129]
