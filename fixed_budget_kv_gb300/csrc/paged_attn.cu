@@ -34,12 +34,17 @@
 // off by about 1.3e-3 of its size beside the 1.7e-3 of its own rounding.  The row sum is not
 // rounded.
 //
+// The exponentials are ex2.approx.ftz and the logarithm of lse is __log2f: a few units of 2^-22 each,
+// small beside the rounded weights, and beside the products' own fp32 roundings in lse.
+//
 // Measured (8 KV heads, G = 4, D = 128, one GB300, calls in a chain): one row each of 64 sequences
 // of 500 .. 16 001 slots 185 us, 96% of the copy rate; 4096 tokens at the end of 32 768 slots
-// 1.43-1.46 ms, 1410-1440 TFLOP/s (74% of the burst rate), bound by the issue of products (1.26 ms without
+// 1.46-1.49 ms in a continuous run, at the power cap's 1.93 GHz, 1380-1410 TFLOP/s (72-73% of the burst
+// rate; 1.35 ms in the first 50 ms, at 2.07 GHz), bound by the issue of products (1.26 ms without
 // the softmax) and the hand-overs S -> softmax -> P V; a step of 12 sequences, two long chunks
-// among ten short ones and decode rows, 181 us, 1070 TFLOP/s (the chunks' rate, 15 us of merge,
-// start and switches).
+// among ten short ones and decode rows, 181-185 us, 1050-1070 TFLOP/s (the chunks' rate, 15 us of
+// merge, start and switches).  At D = 64 an event costs more than half as much: 4096 tokens over
+// 32 768 slots 1.21 ms, 854 TFLOP/s.
 #include <string.h>
 
 #include <atomic>

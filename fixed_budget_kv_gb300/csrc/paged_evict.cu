@@ -15,8 +15,8 @@
 // before: nothing is lost and no second copy is needed.  Bound by memory.
 //
 // Measured (8 KV heads, D = 128, one GB300): 64 sequences of 1700 .. 4099 slots to 2048, 845 MB: select
-// 19 us, move 134 us (5.8 TB/s), in a chain of calls 181 us; one of 131 072 slots to 4096: 18 us
-// (the barriers of eight clusters) and 7-16 us (rows in and out of 128 SMs), in a chain 32 us.
+// 19 us, move 134 us (5.8 TB/s), in a chain of calls 180 us; one of 131 072 slots to 4096: 18 us
+// (the barriers of eight clusters) and 7-16 us (rows in and out of 128 SMs), in a chain 30-32 us.
 #include <atomic>
 
 #include "paged.cuh"
@@ -459,6 +459,11 @@ extern "C" kvpop_status kvpop_paged_evict(void* kp, int64_t kp_stride, void* vp,
   const long long heads = (long long)n * H, most = (long long)max_pages * page;
   int CS = 1;
   while (CS < kMaxCluster && heads * CS * 2 <= 2ll * num_sms() && most / (CS * 2) >= 2048) CS *= 2;
+  // The host knows the table's width, not the lengths.  A table for more slots than the sequences have
+  // leaves fewer CTAs an SM: 64 sequences of 1700 .. 4099 slots to 2048 take 180 us with a tight table
+  // and 160 with one for 131 072 slots (252 and 232 of 8000 .. 16 001), 200 of 1000 .. 3001 with 2 heads
+  // of D = 64 31 and 39.  Room for four CTAs an SM at any width: 180, 262 and 34, but 328 instead of
+  // 272 for 64 sequences of 16 000 .. 32 001, whose keys are then read again.
   prm.held = (int)min((long long)(kCacheBytes / 16 * 8 / 9), most / CS / 4 + 4);
   auto select = CS > 1 ? evict_select<1024> : evict_select<512>;
   static std::atomic<uint64_t> ready{0};  // bit d: the kernels are set up on device d

@@ -27,12 +27,16 @@
 // long chunks would lose digits in one running sum.  A tile with masked columns is taken 32 columns
 // at a time: those before a warp's first key are not read, and what a key does not see becomes -inf
 // before the same sum (512 tokens, G = 8, over 16 384 slots 130 us with a conditional sum, 115 so).
+// Where such a tile has a row whose lse is NaN, that -inf alone would not keep it from the slots that the
+// row does not see: a path of its own masks the lse too (104 us for the decode rows below without it).
+// The exponentials are ex2.approx.ftz, within a few units of 2^-22 of themselves.
 //
 // Measured (8 KV heads, G = 4, D = 128, one GB300, calls in a chain): one row each of 64 sequences
-// of 500 .. 16 001 slots 104 us, 88% of the copy rate; 32 rows over 131 072 slots 52 us, 78%;
-// 4096 tokens over 32 768 slots 0.65-0.69 ms, 1490-1580 TFLOP/s (77-82% of the burst rate), bound by
+// of 500 .. 16 001 slots 106 us, 86% of the copy rate; 32 rows over 131 072 slots 52 us, 78%;
+// 4096 tokens over 32 768 slots 0.70-0.73 ms in a continuous run, at the power cap's 1.93 GHz, 1410-1470
+// TFLOP/s (73-76% of the burst rate; 0.65 ms in the first 50 ms, at 2.07 GHz), bound by
 // the products beside the exponentials (a step before, at 0.69: 0.62 without the exponentials, 0.56
-// without the loads of lse either).
+// without the loads of lse either).  At D = 64 0.58 ms, 882 TFLOP/s.
 #include <string.h>
 
 #include <atomic>

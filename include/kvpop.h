@@ -439,7 +439,8 @@ kvpop_status kvpop_prefix_attn(const void* q, const void* pk, const void* pv, in
  *
  * kvpop_paged_mass: for every slot t < lens[i] and head h
  *     scores = decay * scores + sum over the rows that see t, g < G of exp(s_t - lse_row)
- *   with kvpop_paged_attn's lse (a row whose lse is -inf adds nothing).  Fewer rows than the
+ *   with kvpop_paged_attn's lse (a row whose lse is -inf adds nothing; one whose lse is NaN makes
+ *   the slots that it sees NaN, and no others).  Fewer rows than the
  *   attention had may be given: the chunk's last ones (an observation window at a prompt's
  *   end) with their cu.  decay in [0, 1]; 0 does not read the old scores.  The sums are taken
  *   in a fixed order: the same bits every run.
